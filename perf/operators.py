@@ -31,6 +31,7 @@ HP = {"lr": 1e-3, "momentum": 0.95, "weight_decay": 0.01, "eps": 1e-7,
 BLOCK_512 = "512x512,512x512,512x512,512x512,512x2048,2048x512,512,512"
 BLOCK_4096 = ("4096x4096,1024x4096,1024x4096,4096x4096,14336x4096,4096x14336,14336x4096,"
               "4096,4096")
+RAGGED = "1000x333,777x510,1x640,1025x2049,300x3x3x7,33"
 TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
 
@@ -40,10 +41,10 @@ def listed():
         # unit a step runs, where latency counts
         {"name": "momentum-block512-r4", "op": "momentum", "shapes": BLOCK_512, "R": 4,
          "layout": "per_param", "grad": "bf16", "update": "bf16"},
-        # accumulated fp32 gradients, a flat parameter and three ranks: every
-        # shard begins off the vector grid
-        {"name": "momentum-block512-flat-r3-f32", "op": "momentum", "shapes": BLOCK_512, "R": 3,
-         "layout": "flat", "grad": "f32", "update": "f32"},
+        # accumulated fp32 gradients of odd sizes over three ranks: pieces and
+        # rows begin off the vector grid
+        {"name": "momentum-ragged-r3-f32", "op": "momentum", "shapes": RAGGED, "R": 3,
+         "layout": "per_param", "grad": "f32", "update": "f32"},
         # a block of hidden 4096 over eight ranks: 218M parameters, 3.5 GB of
         # gradients, bound by memory
         {"name": "momentum-block4096-flat-r8", "op": "momentum", "shapes": BLOCK_4096, "R": 8,
@@ -72,8 +73,8 @@ def listed():
         # the update of the three units' masters with the parameter's recast
         {"name": "apply-block512-r4", "op": "apply", "shapes": BLOCK_512, "R": 4,
          "layout": "per_param", "ortho": "bf16", "param": "bf16"},
-        {"name": "apply-block512-flat-r3-f32", "op": "apply", "shapes": BLOCK_512, "R": 3,
-         "layout": "flat", "ortho": "f32", "param": "f32"},
+        {"name": "apply-ragged-r3-f32", "op": "apply", "shapes": RAGGED, "R": 3,
+         "layout": "per_param", "ortho": "f32", "param": "f32"},
         {"name": "apply-block4096-flat-r8", "op": "apply", "shapes": BLOCK_4096, "R": 8,
          "layout": "flat", "ortho": "bf16", "param": "bf16"},
     ]
