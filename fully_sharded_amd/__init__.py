@@ -8,6 +8,9 @@ the step of one unit with the next unit's gather), and beyond the per-step path
 fsdp_reshard_plan / fsdp_reshard / fsdp_reshard_batch (restore at another
 world size), fsdp_grad_accumulate, fsdp_allreduce_avg (the DDP comparator)
 and StepGraph (fsdp_step_graph_*: a unit loop replayed as one HIP graph).
+Beside AdamW, the Muon optimiser on a unit's matrices: Muon (the choice of
+matrices, fsdp_muon_plan), fsdp_muon_momentum, fsdp_orthogonalize,
+fsdp_muon_apply, and the whole step, fsdp_muon_shard_step.
 rows and unit_buffers allocate device arrays placed so that the streams a
 kernel touches at one offset do not share HBM channels.
 """
@@ -20,3 +23,8 @@ from .binding import (  # noqa: F401
     fsdp_reshard, fsdp_reshard_batch, fsdp_reshard_plan, fsdp_shard_pack, lib,
 )
 from .buffers import rows, unit_buffers  # noqa: F401,E402
+from .muon import (  # noqa: F401,E402
+    MUON, Muon, bind_muon_apply, bind_muon_momentum, bind_muon_shard_step, bind_orthogonalize,
+    fsdp_muon_apply, fsdp_muon_momentum, fsdp_muon_plan, fsdp_muon_shard_step,
+    fsdp_orthogonalize,
+)

@@ -38,6 +38,14 @@ class AdamWHParams(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double)]
 
 
+class MuonHParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("weight_decay", ctypes.c_double), ("eps", ctypes.c_double),
+                ("ns_a", ctypes.c_double), ("ns_b", ctypes.c_double), ("ns_c", ctypes.c_double),
+                ("ns_steps", ctypes.c_int32), ("nesterov", ctypes.c_int32),
+                ("scale", ctypes.c_int32)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("numel_full", ctypes.c_int64), ("shard_numel", ctypes.c_int64),
                 ("world", ctypes.c_int32), ("n_params", ctypes.c_int32),
@@ -131,6 +139,34 @@ _SIGS = {
     "fsdp_allreduce_avg": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p),
                                           ctypes.c_int32, ctypes.POINTER(ctypes.c_void_p),
                                           ctypes.c_int32, ctypes.c_void_p]),
+    "fsdp_muon_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
+                                      ctypes.POINTER(ctypes.c_int32),
+                                      ctypes.POINTER(ctypes.c_void_p)]),
+    "fsdp_muon_destroy": (None, [ctypes.c_void_p]),
+    "fsdp_muon_prepare": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "fsdp_muon_workspace": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32,
+                                           ctypes.POINTER(ctypes.c_int64),
+                                           ctypes.POINTER(ctypes.c_int64)]),
+    "fsdp_muon_work_items": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.POINTER(ctypes.c_int64), ctypes.c_int64,
+                                            ctypes.POINTER(ctypes.c_int64)]),
+    "fsdp_muon_momentum": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(MuonHParams),
+                                          ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32,
+                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_int32, ctypes.c_void_p]),
+    "fsdp_orthogonalize": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(MuonHParams),
+                                          ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                          ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                          ctypes.c_void_p]),
+    "fsdp_muon_apply": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(MuonHParams),
+                                       ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "fsdp_muon_shard_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(MuonHParams),
+                                            ctypes.POINTER(AdamWHParams), ctypes.c_int64,
+                                            ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p]),
 }
 
 

@@ -1,0 +1,561 @@
+// Host side of the Muon step: the choice of matrices, its work tables, and
+// the C entry points' checks and launches.
+#include "muon.hpp"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "checks.hpp"
+#include "ops.hpp"
+
+namespace fsdp {
+namespace {
+
+constexpr int64_t kItem = 1024;           // elements per work item of the per-element kernels
+constexpr int64_t kMaxSide = int64_t(1) << 30;
+constexpr int64_t kNormChunk = 4096;      // least elements per partial sum
+constexpr int64_t kNormParts = 1024;      // most partial sums per matrix
+constexpr int kTile = 128;                // side of a product's tile
+constexpr int kConvert = 64;              // side of a conversion's tile
+constexpr int kXcds = 8;
+
+int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// Cut [dst, dst + len) <- src at multiples of kItem in the destination.
+void emit(int64_t dst, int64_t src, int64_t len, int32_t mat, std::vector<MuonItem>& out) {
+  while (len > 0) {
+    const int64_t n = std::min(len, (dst / kItem + 1) * kItem - dst);
+    out.push_back(MuonItem{dst, src, static_cast<int32_t>(n), mat});
+    dst += n;
+    src += n;
+    len -= n;
+  }
+}
+
+// Workgroups go to the 8 accelerator dies in turn, each with its own L2: a
+// matrix's tiles (in an order that keeps neighbours together) are cut in 8
+// contiguous parts, one for each die, and the parts dealt out in turn.
+class Deal {
+ public:
+  void add(const std::vector<MuonTile>& tiles) {
+    const int64_t n = static_cast<int64_t>(tiles.size());
+    int64_t at = 0;
+    for (int k = 0; k < kXcds; ++k) {
+      // the longer parts go to the dies that have fewer so far
+      const int64_t take = n / kXcds + (k < n % kXcds ? 1 : 0);
+      auto& q = queue_[(next_ + k) % kXcds];
+      q.insert(q.end(), tiles.begin() + at, tiles.begin() + at + take);
+      at += take;
+    }
+    next_ = static_cast<int>((next_ + n) % kXcds);
+  }
+  std::vector<MuonTile> dealt() const {
+    std::vector<MuonTile> out;
+    size_t longest = 0;
+    for (const auto& q : queue_) longest = std::max(longest, q.size());
+    for (size_t r = 0; r < longest; ++r)
+      for (int x = 0; x < kXcds; ++x)
+        if (r < queue_[x].size()) out.push_back(queue_[x][r]);
+    return out;
+  }
+
+ private:
+  std::vector<MuonTile> queue_[kXcds];
+  int next_ = 0;  // dies before this one have one tile more than the others
+};
+
+// Tiles of a grid of ni x nj, in bands of 8 rows, column by column: any 32
+// consecutive ones (a die's compute units) share 8 row panels and 4 column
+// panels.  lower: those of the lower triangle.
+std::vector<MuonTile> grid(int32_t mat, int64_t ni, int64_t nj, bool lower) {
+  std::vector<MuonTile> out;
+  for (int64_t b = 0; b < ni; b += 8)
+    for (int64_t j = 0; j < nj; ++j)
+      for (int64_t i = b; i < std::min(ni, b + 8); ++i)
+        if (!lower || i >= j)
+          out.push_back(MuonTile{mat, static_cast<int32_t>(i), static_cast<int32_t>(j), 0});
+  return out;
+}
+
+}  // namespace
+
+fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* params,
+                       fsdp_muon* mu) {
+  mu->R = plan->R;
+  mu->T = plan->T;
+  mu->S = plan->S;
+  const int32_t n_all = static_cast<int32_t>(plan->params.size());
+  std::vector<int32_t> chosen(n_all, -1);  // matrix number of a parameter
+  for (int32_t k = 0; k < n_params; ++k) {
+    const int32_t p = params[k];
+    if (p < 0 || p >= n_all || chosen[p] >= 0 || plan->shapes[p].size() < 2)
+      return FSDP_ERR_INVALID_ARG;
+    const Param& q = plan->params[p];
+    if (q.d0 > kMaxSide || q.row > kMaxSide) return FSDP_ERR_UNSUPPORTED;
+    chosen[p] = k;
+    MuonMat t{};
+    t.flat_off = q.flat_off;
+    t.rows = q.d0;
+    t.cols = q.row;
+    t.tall = t.rows > t.cols;
+    t.m = static_cast<int32_t>(std::min(t.rows, t.cols));
+    t.n = static_cast<int32_t>(std::max(t.rows, t.cols));
+    t.mp = static_cast<int32_t>(round_up(t.m, kMuonPad));
+    t.np = static_cast<int32_t>(round_up(t.n, kMuonPad));
+    t.off_x = mu->nx;
+    t.off_a = mu->na;
+    t.off_d = mu->nd;
+    t.index = p;
+    mu->nx += int64_t(t.mp) * t.np;
+    mu->na += int64_t(t.mp) * t.mp;
+    mu->nd += t.mp;
+    const int64_t numel = t.rows * t.cols;
+    t.norm_chunk =
+        std::max(kNormChunk, round_up((numel + kNormParts - 1) / kNormParts, kNormChunk));
+    t.norm_first = static_cast<int32_t>(mu->n_partial);
+    t.norm_count = static_cast<int32_t>((numel + t.norm_chunk - 1) / t.norm_chunk);
+    mu->n_partial += t.norm_count;
+    mu->mats.push_back(t);
+  }
+  // grids first: a table that is refused is not built
+  int64_t n_convert = 0, n_wide = 0, n_square = 0;
+  for (const MuonMat& t : mu->mats) {
+    n_convert += int64_t(t.mp / kConvert) * (t.np / kConvert);
+    const int64_t si = (t.mp + kTile - 1) / kTile, sj = (t.np + kTile - 1) / kTile;
+    n_wide += si * sj;
+    n_square += si * (si + 1) / 2;
+    if (n_convert > kMaxItems || n_wide > kMaxItems || n_square > kMaxItems)
+      return FSDP_ERR_UNSUPPORTED;
+  }
+  if (mu->n_partial > kMaxItems) return FSDP_ERR_UNSUPPORTED;
+
+  // the per-element work: the plan's runs, cut where parameters end
+  std::vector<Work> rest;
+  auto split = [&](int64_t shard, int64_t flat, int64_t len) {
+    // first parameter that ends after `flat`
+    size_t p = std::upper_bound(plan->params.begin(), plan->params.end(), flat,
+                                [](int64_t x, const Param& q) { return x < q.flat_off + q.numel; }) -
+               plan->params.begin();
+    for (; len > 0; ++p) {
+      const Param& q = plan->params[p];
+      const int64_t n = std::min(len, q.flat_off + q.numel - flat);
+      if (chosen[p] < 0) {
+        push_run(rest, shard, flat, n);
+      } else {
+        emit(shard, flat, n, chosen[p], mu->apply);
+        emit(flat, shard, n, chosen[p], mu->momentum);
+      }
+      shard += n;
+      flat += n;
+      len -= n;
+    }
+  };
+  for (const Work& w : plan->shard_runs) {
+    if (w.src < 0)
+      push_run(rest, w.dst, -1, w.len);
+    else
+      split(w.dst, w.src, w.len);
+  }
+  if (static_cast<int64_t>(mu->apply.size()) > kMaxItems ||
+      static_cast<int64_t>(mu->momentum.size()) > kMaxItems ||
+      count_items(rest, kShardChunk) > kMaxItems)
+    return FSDP_ERR_UNSUPPORTED;
+  emit_items(rest, kShardChunk, mu->rest.host);
+  std::sort(mu->momentum.begin(), mu->momentum.end(),
+            [](const MuonItem& a, const MuonItem& b) { return a.dst < b.dst; });
+
+  for (int32_t k = 0; k < n_params; ++k) {
+    const MuonMat& t = mu->mats[k];
+    for (int32_t i = 0; i < t.norm_count; ++i) mu->norm.push_back(MuonTile{k, i, 0, 0});
+    const int64_t ri = (t.tall ? t.np : t.mp) / kConvert, cj = (t.tall ? t.mp : t.np) / kConvert;
+    for (int64_t i = 0; i < ri; ++i)
+      for (int64_t j = 0; j < cj; ++j)
+        mu->convert.push_back(MuonTile{k, static_cast<int32_t>(i), static_cast<int32_t>(j), 0});
+  }
+  // products: the longest sums first, so that the short ones fill the end
+  std::vector<int32_t> order(n_params);
+  for (int32_t k = 0; k < n_params; ++k) order[k] = k;
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int32_t a, int32_t b) { return mu->mats[a].np > mu->mats[b].np; });
+  Deal square;
+  for (int32_t k : order) {
+    const int64_t s = (mu->mats[k].mp + kTile - 1) / kTile;
+    square.add(grid(k, s, s, true));
+  }
+  mu->square = square.dealt();
+  std::stable_sort(order.begin(), order.end(),
+                   [&](int32_t a, int32_t b) { return mu->mats[a].mp > mu->mats[b].mp; });
+  Deal wide;
+  for (int32_t k : order) {
+    const MuonMat& t = mu->mats[k];
+    wide.add(grid(k, (t.np + kTile - 1) / kTile, (t.mp + kTile - 1) / kTile, false));
+  }
+  mu->wide = wide.dealt();
+  return FSDP_OK;
+}
+
+MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split) {
+  MuonWorkspace w{};
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_up(bytes, 256);
+    return here;
+  };
+  const int64_t x = mu->nx * 2, a = mu->na * 2;
+  w.partial = take(mu->n_partial * 8);
+  w.coef = take(static_cast<int64_t>(mu->mats.size()) * 16);
+  w.adiag = take(mu->nd * 4);
+  w.bdiag = take(mu->nd * 4);
+  w.xh = take(x);
+  w.th[0] = take(x);
+  w.th[1] = take(x);
+  w.tl[0] = take(x);
+  // the low part of the transpose is only read by the workgroup that
+  // replaces it, unless it is an operand too
+  w.tl[1] = split ? take(x) : w.tl[0];
+  w.xl = split ? take(x) : 0;
+  w.ah = take(a);
+  w.bh = take(a);
+  w.al = split ? take(a) : 0;
+  w.bl = split ? take(a) : 0;
+  w.bytes = at;
+  return w;
+}
+
+}  // namespace fsdp
+
+using fsdp::Range;
+using fsdp::Ranges;
+using fsdp::aligned;
+using fsdp::any_overlap;
+using fsdp::dtype_size;
+using fsdp::overlap;
+using fsdp::range_of;
+using fsdp::valid_dtype;
+
+fsdp_status fsdp_muon::device(fsdp::MuonDevice* out) const {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return FSDP_ERR_HIP;
+  }
+  int64_t at[8], bytes = 0;
+  const void* from[7] = {mats.data(),   norm.data(),     convert.data(), square.data(),
+                         wide.data(),   momentum.data(), apply.data()};
+  const size_t size[7] = {mats.size() * sizeof(fsdp::MuonMat),
+                          norm.size() * sizeof(fsdp::MuonTile),
+                          convert.size() * sizeof(fsdp::MuonTile),
+                          square.size() * sizeof(fsdp::MuonTile),
+                          wide.size() * sizeof(fsdp::MuonTile),
+                          momentum.size() * sizeof(fsdp::MuonItem),
+                          apply.size() * sizeof(fsdp::MuonItem)};
+  for (int k = 0; k < 7; ++k) {
+    at[k] = bytes;
+    bytes += (static_cast<int64_t>(size[k]) + 255) / 256 * 256;
+  }
+  std::lock_guard<std::mutex> lock(mu_);
+  auto it = dev_.find(dev);
+  if (it == dev_.end()) {
+    void* mem = nullptr;
+    if (hipMalloc(&mem, static_cast<size_t>(bytes)) != hipSuccess) {
+      (void)hipGetLastError();
+      return FSDP_ERR_OUT_OF_MEMORY;
+    }
+    for (int k = 0; k < 7; ++k)
+      if (size[k] && hipMemcpy(static_cast<char*>(mem) + at[k], from[k], size[k],
+                               hipMemcpyHostToDevice) != hipSuccess) {
+        (void)hipGetLastError();
+        (void)hipFree(mem);
+        return FSDP_ERR_HIP;
+      }
+    it = dev_.emplace(dev, mem).first;
+  }
+  const char* b = static_cast<const char*>(it->second);
+  out->mats = reinterpret_cast<const fsdp::MuonMat*>(b + at[0]);
+  out->norm = reinterpret_cast<const fsdp::MuonTile*>(b + at[1]);
+  out->convert = reinterpret_cast<const fsdp::MuonTile*>(b + at[2]);
+  out->square = reinterpret_cast<const fsdp::MuonTile*>(b + at[3]);
+  out->wide = reinterpret_cast<const fsdp::MuonTile*>(b + at[4]);
+  out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[5]);
+  out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[6]);
+  return FSDP_OK;
+}
+
+fsdp_muon::~fsdp_muon() {
+  for (auto& kv : dev_) (void)hipFree(kv.second);
+}
+
+namespace {
+
+fsdp_status check(const fsdp_muon_hparams* hp) {
+  if (!hp) return FSDP_ERR_INVALID_ARG;
+  const double all[] = {hp->lr, hp->momentum, hp->weight_decay, hp->eps,
+                        hp->ns_a, hp->ns_b, hp->ns_c};
+  for (double x : all)
+    if (!std::isfinite(x)) return FSDP_ERR_INVALID_ARG;
+  if (hp->lr < 0 || !(hp->momentum >= 0 && hp->momentum < 1) || hp->weight_decay < 0 ||
+      !(hp->eps >= 1e-300) || std::fabs(hp->ns_a) > 16 || std::fabs(hp->ns_b) > 16 ||
+      std::fabs(hp->ns_c) > 16 || hp->ns_steps < 1 || hp->ns_steps > 16 ||
+      (hp->nesterov != 0 && hp->nesterov != 1) || hp->scale < FSDP_MUON_SCALE_NONE ||
+      hp->scale > FSDP_MUON_SCALE_RMS)
+    return FSDP_ERR_INVALID_ARG;
+  return FSDP_OK;
+}
+
+fsdp::MuonScalars scalars(const fsdp_muon_hparams* hp) {
+  return fsdp::MuonScalars{hp->momentum, 1.0 - hp->momentum, 1.0 - hp->lr * hp->weight_decay,
+                           hp->lr,       hp->nesterov,       hp->scale};
+}
+
+// The gradients of a call, checked: R replicas [T], or the reduced [R][S].
+fsdp_status take_grads(const fsdp_muon* mu, const void* const* grads, int32_t grad_dtype,
+                       int32_t replicas, fsdp::PtrArray* g, Ranges* reads, bool* vec) {
+  if (!grads || !valid_dtype(grad_dtype) || (replicas != 0 && replicas != 1))
+    return FSDP_ERR_INVALID_ARG;
+  if (!replicas && grad_dtype != FSDP_F32) return FSDP_ERR_INVALID_ARG;
+  const int64_t es = dtype_size(grad_dtype);
+  for (int q = 0; q < (replicas ? mu->R : 1); ++q) {
+    if (!grads[q] || !aligned(grads[q], es)) return FSDP_ERR_INVALID_ARG;
+    g->p[q] = grads[q];
+    reads->push_back(range_of(grads[q], (replicas ? mu->T : mu->R * mu->S) * es));
+    *vec = *vec && aligned(grads[q], 16);
+  }
+  return FSDP_OK;
+}
+
+bool meet(const Ranges& writes, const Ranges& reads) {
+  for (const Range& w : writes)
+    for (const Range& r : reads)
+      if (overlap(w, r)) return true;
+  return any_overlap(writes);
+}
+
+// The products of one fsdp_orthogonalize, arguments checked.
+fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
+                          const fsdp_muon_hparams* hp, const void* update, int32_t update_dt,
+                          void* ortho, int32_t ortho_dt, char* ws, const fsdp::Sink& sink) {
+  fsdp::MuonArgs a{};
+  a.mats = d.mats;
+  a.ws = ws;
+  a.split = ortho_dt == FSDP_F32;
+  a.w = fsdp::muon_workspace(mu, a.split);
+  const double poly[3] = {hp->ns_a, hp->ns_b, hp->ns_c};
+  auto with = [&](const fsdp::MuonTile* t, const std::vector<fsdp::MuonTile>& host) {
+    a.tiles = t;
+    a.n_tiles = static_cast<int64_t>(host.size());
+    return a;
+  };
+  hipError_t e = fsdp::launch_muon_norm(with(d.norm, mu->norm), update, update_dt, sink);
+  if (e == hipSuccess)
+    e = fsdp::launch_muon_convert(with(d.convert, mu->convert), update, update_dt, hp->eps, poly,
+                                  sink);
+  for (int s = 0; s < hp->ns_steps && e == hipSuccess; ++s) {
+    e = fsdp::launch_muon_gram(with(d.square, mu->square), sink);
+    if (e == hipSuccess) e = fsdp::launch_muon_poly(a, s == 0, poly, sink);
+    if (e == hipSuccess)
+      e = fsdp::launch_muon_step(with(d.wide, mu->wide), s & 1, s == 0, s == hp->ns_steps - 1,
+                                 poly, ortho, ortho_dt, sink);
+  }
+  return fsdp::status_of(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+fsdp_status fsdp_muon_plan(const fsdp_plan* plan, int32_t n_params, const int32_t* params,
+                           fsdp_muon** out) {
+  if (!out) return FSDP_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!plan || n_params < 1 || !params) return FSDP_ERR_INVALID_ARG;
+  fsdp_muon* mu = new (std::nothrow) fsdp_muon();
+  if (!mu) return FSDP_ERR_OUT_OF_MEMORY;
+  const fsdp_status st =
+      fsdp::guarded([&] { return fsdp::build_muon(plan, n_params, params, mu); });
+  if (st != FSDP_OK) {
+    delete mu;
+    return st;
+  }
+  *out = mu;
+  return FSDP_OK;
+}
+
+void fsdp_muon_destroy(fsdp_muon* mu) { delete mu; }
+
+fsdp_status fsdp_muon_prepare(const fsdp_muon* mu, void* stream) {
+  (void)stream;
+  return fsdp::guarded([&]() -> fsdp_status {
+    if (!mu) return FSDP_ERR_INVALID_ARG;
+    fsdp::MuonDevice d;
+    const fsdp::Work* w = nullptr;
+    const fsdp_status st = mu->device(&d);
+    return st != FSDP_OK ? st : mu->rest.device(&w);
+  });
+}
+
+fsdp_status fsdp_muon_workspace(const fsdp_muon* mu, int32_t update_dtype, int32_t ortho_dtype,
+                                int64_t* ortho_bytes, int64_t* step_bytes) {
+  if (!mu || !valid_dtype(update_dtype) || !valid_dtype(ortho_dtype)) return FSDP_ERR_INVALID_ARG;
+  if (ortho_bytes) *ortho_bytes = fsdp::muon_workspace(mu, ortho_dtype == FSDP_F32).bytes;
+  if (step_bytes)
+    *step_bytes = fsdp::muon_workspace(mu, false).bytes + (mu->T * 2 + 255) / 256 * 256;
+  return FSDP_OK;
+}
+
+fsdp_status fsdp_muon_work_items(const fsdp_muon* mu, int32_t space, int64_t* out,
+                                 int64_t capacity, int64_t* n) {
+  if (!mu || !n || (space != 0 && space != 1)) return FSDP_ERR_INVALID_ARG;
+  const std::vector<fsdp::MuonItem>& items = space == 0 ? mu->apply : mu->momentum;
+  *n = static_cast<int64_t>(items.size());
+  if (!out) return FSDP_OK;
+  if (capacity < *n) return FSDP_ERR_INVALID_ARG;
+  for (size_t i = 0; i < items.size(); ++i) {
+    out[3 * i + 0] = items[i].dst;
+    out[3 * i + 1] = items[i].src;
+    out[3 * i + 2] = items[i].len;
+  }
+  return FSDP_OK;
+}
+
+fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                               const void* const* grads, int32_t grad_dtype,
+                               int32_t grads_are_replicas, float* m, void* update,
+                               int32_t update_dtype, void* stream) {
+  return fsdp::guarded([&]() -> fsdp_status {
+    if (!mu || !m || !update || !valid_dtype(update_dtype)) return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check(hp);
+    if (st != FSDP_OK) return st;
+    const int64_t ues = dtype_size(update_dtype);
+    if (!aligned(m, 4) || !aligned(update, ues)) return FSDP_ERR_INVALID_ARG;
+    fsdp::PtrArray g{};
+    Ranges reads, writes;
+    bool vec = aligned(m, 16) && aligned(update, 16);
+    st = take_grads(mu, grads, grad_dtype, grads_are_replicas, &g, &reads, &vec);
+    if (st != FSDP_OK) return st;
+    writes.push_back(range_of(m, mu->R * mu->S * 4));
+    writes.push_back(range_of(update, mu->T * ues));
+    if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
+    fsdp::MuonDevice d;
+    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    return fsdp::status_of(fsdp::launch_muon_momentum(
+        d.momentum, static_cast<int64_t>(mu->momentum.size()), g, mu->R, grad_dtype,
+        grads_are_replicas != 0, m, update, update_dtype, scalars(hp), vec,
+        fsdp::StreamSink(stream)));
+  });
+}
+
+fsdp_status fsdp_orthogonalize(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                               const void* update, int32_t update_dtype, void* ortho,
+                               int32_t ortho_dtype, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  return fsdp::guarded([&]() -> fsdp_status {
+    if (!mu || !update || !ortho || !workspace || !valid_dtype(update_dtype) ||
+        !valid_dtype(ortho_dtype))
+      return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check(hp);
+    if (st != FSDP_OK) return st;
+    const int64_t need = fsdp::muon_workspace(mu, ortho_dtype == FSDP_F32).bytes;
+    if (workspace_bytes < need || !aligned(workspace, 256) ||
+        !aligned(update, dtype_size(update_dtype)) || !aligned(ortho, dtype_size(ortho_dtype)))
+      return FSDP_ERR_INVALID_ARG;
+    const Range u = range_of(update, mu->T * dtype_size(update_dtype));
+    const Range o = range_of(ortho, mu->T * dtype_size(ortho_dtype));
+    const Range w = range_of(workspace, need);
+    const bool in_place = update == ortho && update_dtype == ortho_dtype;
+    if (overlap(w, u) || overlap(w, o) || (!in_place && overlap(u, o)))
+      return FSDP_ERR_INVALID_ARG;
+    fsdp::MuonDevice d;
+    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    return orthogonalize(mu, d, hp, update, update_dtype, ortho, ortho_dtype,
+                         static_cast<char*>(workspace), fsdp::StreamSink(stream));
+  });
+}
+
+fsdp_status fsdp_muon_apply(const fsdp_muon* mu, const fsdp_muon_hparams* hp, const void* ortho,
+                            int32_t ortho_dtype, float* master, void* param_out,
+                            int32_t param_dtype, void* stream) {
+  return fsdp::guarded([&]() -> fsdp_status {
+    if (!mu || !ortho || !master || !param_out || !valid_dtype(ortho_dtype) ||
+        !valid_dtype(param_dtype))
+      return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check(hp);
+    if (st != FSDP_OK) return st;
+    const int64_t oes = dtype_size(ortho_dtype), pes = dtype_size(param_dtype);
+    if (!aligned(ortho, oes) || !aligned(master, 4) || !aligned(param_out, pes))
+      return FSDP_ERR_INVALID_ARG;
+    Ranges reads, writes;
+    reads.push_back(range_of(ortho, mu->T * oes));
+    writes.push_back(range_of(master, mu->R * mu->S * 4));
+    writes.push_back(range_of(param_out, mu->R * mu->S * pes));
+    if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
+    fsdp::MuonDevice d;
+    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    return fsdp::status_of(fsdp::launch_muon_apply(
+        d.apply, static_cast<int64_t>(mu->apply.size()), d.mats, ortho, ortho_dtype, master,
+        param_out, param_dtype, scalars(hp),
+        aligned(ortho, 16) && aligned(master, 16) && aligned(param_out, 16),
+        fsdp::StreamSink(stream)));
+  });
+}
+
+fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                                 const fsdp_adamw_hparams* adamw, int64_t step,
+                                 const void* const* grads, int32_t grad_dtype, float* master,
+                                 float* m, float* v, void* param_out, int32_t param_dtype,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  return fsdp::guarded([&]() -> fsdp_status {
+    if (!mu || !master || !m || (adamw && !v) || !param_out || !workspace ||
+        !valid_dtype(param_dtype))
+      return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check(hp);
+    if (st != FSDP_OK) return st;
+    fsdp::AdamScalars sc{};
+    if (adamw && (st = fsdp::adam_scalars(adamw, step, &sc)) != FSDP_OK) return st;
+    const int64_t n = mu->R * mu->S, pes = dtype_size(param_dtype);
+    const int64_t update_bytes = (mu->T * 2 + 255) / 256 * 256;
+    const int64_t need = fsdp::muon_workspace(mu, false).bytes + update_bytes;
+    if (workspace_bytes < need || !aligned(workspace, 256) || !aligned(master, 4) ||
+        !aligned(m, 4) || (adamw && !aligned(v, 4)) || !aligned(param_out, pes))
+      return FSDP_ERR_INVALID_ARG;
+    fsdp::PtrArray g{};
+    Ranges reads, writes;
+    bool vec = aligned(master, 16) && aligned(m, 16) && aligned(param_out, 16) &&
+               (!adamw || aligned(v, 16));
+    st = take_grads(mu, grads, grad_dtype, 1, &g, &reads, &vec);
+    if (st != FSDP_OK) return st;
+    writes.push_back(range_of(master, n * 4));
+    writes.push_back(range_of(m, n * 4));
+    if (adamw) writes.push_back(range_of(v, n * 4));
+    writes.push_back(range_of(param_out, n * pes));
+    writes.push_back(range_of(workspace, need));
+    if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
+    fsdp::MuonDevice d;
+    const fsdp::Work* rest = nullptr;
+    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    if (adamw && (st = mu->rest.device(&rest)) != FSDP_OK) return st;
+    const fsdp::StreamSink sink(stream);
+    void* update = workspace;
+    const fsdp::MuonScalars ms = scalars(hp);
+    st = fsdp::status_of(fsdp::launch_muon_momentum(
+        d.momentum, static_cast<int64_t>(mu->momentum.size()), g, mu->R, grad_dtype, true, m,
+        update, FSDP_BF16, ms, vec, sink));
+    if (st == FSDP_OK)
+      st = orthogonalize(mu, d, hp, update, FSDP_BF16, update, FSDP_BF16,
+                         static_cast<char*>(workspace) + update_bytes, sink);
+    if (st == FSDP_OK)
+      st = fsdp::status_of(fsdp::launch_muon_apply(
+          d.apply, static_cast<int64_t>(mu->apply.size()), d.mats, update, FSDP_BF16, master,
+          param_out, param_dtype, ms, vec, sink));
+    if (st == FSDP_OK && adamw && !mu->rest.host.empty())
+      st = fsdp::status_of(fsdp::launch_fused(rest, static_cast<int64_t>(mu->rest.host.size()), g,
+                                              mu->R, grad_dtype, master, m, v, param_out,
+                                              param_dtype, sc, nullptr, vec, sink));
+    return st;
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,135 @@
+// Internal structures of the Muon step: the chosen matrices of a unit, the
+// work tables of its kernels, the workspace's layout and the launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <map>
+#include <mutex>
+#include <vector>
+
+#include "fsdp_mi355x.h"
+#include "kernels.hpp"
+#include "plan.hpp"
+
+namespace fsdp {
+
+// One chosen matrix.  It is worked on with its shorter side first: X is
+// m x n with m <= n, the matrix itself or (tall) its transpose.  Planes
+// hold it with both sides padded to multiples of kMuonPad, zeros there.
+struct MuonMat {
+  int64_t flat_off;    // in the unit's buffers [T]
+  int64_t rows, cols;  // as the parameter has them
+  int64_t off_x;       // first element in a plane of X (mp x np) or of its transpose
+  int64_t off_a;       // first element in a plane of A or B (mp x mp)
+  int64_t off_d;       // first entry of the diagonals of A and B
+  int64_t norm_chunk;  // elements per partial sum of the norm
+  int32_t norm_first, norm_count;  // its partial sums
+  int32_t m, n, mp, np;
+  int32_t tall;  // rows > cols
+  int32_t index;  // of the parameter in the plan
+};
+
+constexpr int kMuonPad = 64;
+
+// A kernel's tile or chunk: which matrix, and where in it.
+struct MuonTile {
+  int32_t mat, i, j, unused;
+};
+
+// Work items of the per-element kernels: `len` elements at `dst` (a
+// multiple-of-1024 window of the destination space) from `src` on.
+struct MuonItem {
+  int64_t dst, src;
+  int32_t len, mat;
+};
+
+// Device copies of the tables, one per device, in one allocation.
+struct MuonDevice {
+  const MuonMat* mats;
+  const MuonTile* norm;       // chunks of the norm's partial sums
+  const MuonTile* convert;    // 64 x 64 tiles of the parameter's own orientation
+  const MuonTile* square;     // lower triangle of A and B
+  const MuonTile* wide;       // tiles of X's transpose
+  const MuonItem* momentum;   // flat space
+  const MuonItem* apply;      // shard space
+};
+
+// Where each part of fsdp_orthogonalize's workspace begins, in bytes.
+// split: every operand in two fp16 parts (FSDP_F32 results).
+struct MuonWorkspace {
+  int64_t partial, coef, adiag, bdiag;
+  int64_t xh, xl, th[2], tl[2], ah, al, bh, bl;
+  int64_t bytes;
+};
+
+// Everything the launchers of the products need.
+struct MuonArgs {
+  const MuonMat* mats;
+  const MuonTile* tiles;
+  int64_t n_tiles;
+  char* ws;
+  MuonWorkspace w;
+  bool split;
+};
+
+}  // namespace fsdp
+
+struct fsdp_muon {
+  int32_t R = 0;
+  int64_t T = 0, S = 0;
+  std::vector<fsdp::MuonMat> mats;
+  std::vector<fsdp::MuonTile> norm, convert, square, wide;
+  std::vector<fsdp::MuonItem> momentum, apply;
+  fsdp::WorkTable rest;  // shard space: all that is not chosen, padding too
+  int64_t nx = 0, na = 0, nd = 0, n_partial = 0;  // plane, diagonal and partial-sum sizes
+
+  // Device tables on the current device, uploaded on first use
+  // (synchronous; freed with the object).
+  fsdp_status device(fsdp::MuonDevice* out) const;
+  ~fsdp_muon();
+
+ private:
+  mutable std::mutex mu_;
+  mutable std::map<int, void*> dev_;
+};
+
+namespace fsdp {
+
+fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* params,
+                       fsdp_muon* mu);
+
+MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split);
+
+// Scalars of the per-element kernels.
+struct MuonScalars {
+  double momentum, one_minus;  // mu, 1 - mu
+  double decay, lr;            // 1 - lr wd, lr
+  int32_t nesterov, scale;
+};
+
+hipError_t launch_muon_momentum(const MuonItem* items, int64_t n, const PtrArray& grads, int R,
+                                int grad_dt, bool replicas, float* m, void* update, int update_dt,
+                                const MuonScalars& sc, bool vec, const Sink& sink);
+
+hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* mats,
+                             const void* ortho, int ortho_dt, float* master, void* param,
+                             int param_dt, const MuonScalars& sc, bool vec, const Sink& sink);
+
+hipError_t launch_muon_norm(const MuonArgs& a, const void* update, int dt, const Sink& sink);
+// The update into the planes of X and its transpose, scaled by a power of
+// two, and the first step's coefficients with what is left of the norm.
+hipError_t launch_muon_convert(const MuonArgs& a, const void* update, int dt, double eps,
+                               const double (&poly)[3], const Sink& sink);
+// A = X X^T.
+hipError_t launch_muon_gram(const MuonArgs& a, const Sink& sink);
+// B = b A + c A A.
+hipError_t launch_muon_poly(const MuonArgs& a, bool first, const double (&poly)[3],
+                            const Sink& sink);
+// X <- a X + B X, from transpose buffer `from` into the other; the last
+// step writes ortho instead.
+hipError_t launch_muon_step(const MuonArgs& a, int from, bool first, bool last,
+                            const double (&poly)[3], void* ortho, int ortho_dt, const Sink& sink);
+
+}  // namespace fsdp

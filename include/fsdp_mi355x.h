@@ -389,6 +389,149 @@ fsdp_status fsdp_step_graph_info(const fsdp_step_graph* graph, int64_t* n_nodes,
  * not supported. */
 fsdp_status fsdp_step_graph_launch(fsdp_step_graph* graph, int64_t step, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Muon: the optimiser step of a unit's matrices, beside AdamW.
+ *
+ * Per matrix the step averages the gradients, keeps a momentum, replaces
+ * the momentum's update by a matrix of the same singular vectors whose
+ * singular values are near 1 (the update "orthogonalised", by
+ * Newton-Schulz products) and subtracts that from the master.  The first
+ * and the last are per element and run on the rank shards; the products
+ * need whole matrices, so the update is written in unit order, gathered,
+ * and the shards read their part of the result.
+ *
+ * A matrix is a parameter of two dimensions or more, its first dimension
+ * (rows) against the product of all others (columns).
+ * --------------------------------------------------------------------- */
+typedef struct fsdp_muon fsdp_muon; /* opaque; immutable once created */
+
+enum {
+  FSDP_MUON_SCALE_NONE = 0,   /* scale 1                                  */
+  FSDP_MUON_SCALE_ASPECT = 1, /* sqrt(max(1, rows / columns))             */
+  FSDP_MUON_SCALE_RMS = 2     /* 0.2 sqrt(max(rows, columns)): an update
+                                 of about AdamW's root mean square        */
+};
+
+typedef struct fsdp_muon_hparams {
+  double lr;                  /* >= 0 */
+  double momentum;            /* in [0, 1) */
+  double weight_decay;        /* >= 0, decoupled: p <- p (1 - lr wd) */
+  double eps;                 /* >= 1e-300, added to the Frobenius norm */
+  double ns_a, ns_b, ns_c;    /* the polynomial a x + b x^3 + c x^5 of one
+                                 Newton-Schulz step; each at most 16 in
+                                 absolute value */
+  int32_t ns_steps;           /* in [1, 16] */
+  int32_t nesterov;           /* 0 or 1 */
+  int32_t scale;              /* FSDP_MUON_SCALE_* */
+} fsdp_muon_hparams;
+
+/* Choose the parameters of `plan` that Muon updates: n_params >= 1 distinct
+ * indices, each of a parameter of at least two dimensions (else
+ * FSDP_ERR_INVALID_ARG).  Host only; *out owns a new object, freed by
+ * fsdp_muon_destroy; the plan may be destroyed afterwards.
+ * FSDP_ERR_UNSUPPORTED when a call's work would not fit one launch's grid,
+ * or when a matrix has more than 2^30 rows or columns. */
+fsdp_status fsdp_muon_plan(const fsdp_plan* plan, int32_t n_params, const int32_t* params,
+                           fsdp_muon** out);
+
+/* Free it with its device tables.  No call using it may still be in flight.
+ * NULL is ignored. */
+void fsdp_muon_destroy(fsdp_muon* mu);
+
+/* Upload its work tables to the current device now (synchronous).
+ * Optional: the calls below do it on first use; needed before a capture. */
+fsdp_status fsdp_muon_prepare(const fsdp_muon* mu, void* stream);
+
+/* Bytes of the workspaces the calls below take, for updates and results of
+ * these types: *ortho_bytes for fsdp_orthogonalize, *step_bytes for
+ * fsdp_muon_shard_step (its update and result are FSDP_BF16; the types
+ * given do not change it).  Either pointer may be NULL. */
+fsdp_status fsdp_muon_workspace(const fsdp_muon* mu, int32_t update_dtype, int32_t ortho_dtype,
+                                int64_t* ortho_bytes, int64_t* step_bytes);
+
+/* The work items of the two per-element calls (host copy), as
+ * fsdp_plan_work_items: space 0 = fsdp_muon_apply's (dst: shard space [R][S],
+ * src: flat index), space 1 = fsdp_muon_momentum's (dst: flat index, src:
+ * shard space).  Each space covers the chosen parameters' elements once and
+ * nothing else. */
+fsdp_status fsdp_muon_work_items(const fsdp_muon* mu, int32_t space, int64_t* out,
+                                 int64_t capacity, int64_t* n);
+
+/* Momentum of the averaged gradient, and the gathered update.  For every
+ * element of the chosen parameters, at flat index i and shard place (r, j):
+ *   g = the reduce-scatter-average of fsdp_reduce_scatter_avg (fp32)
+ *   m[r][j] <- mu m + (1 - mu) g     in IEEE double, rounded once to fp32
+ *   update[i] = (1 - mu) g + mu m[r][j] (nesterov) or m[r][j]
+ *               in IEEE double from the new m, rounded to fp32 and, for
+ *               FSDP_BF16, then to bf16
+ * so the shards' momentum is updated and the update all-gathered in one
+ * pass over the gradients.
+ *   grads, grad_dtype, grads_are_replicas: as fsdp_adamw_shard_step.
+ *   m: [R][S] fp32, read and written in place; update: [T] of update_dtype.
+ *   m and update are disjoint from each other and from the gradients.
+ *   Other parameters' elements and padding are neither read nor written. */
+fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                               const void* const* grads, int32_t grad_dtype,
+                               int32_t grads_are_replicas, float* m, void* update,
+                               int32_t update_dtype, void* stream);
+
+/* Orthogonalise the update of every chosen matrix, U (rows x columns):
+ *   X = U / (|U|_F + eps)
+ *   ns_steps times:  A = X X^T,  X <- a X + (b A + c A A) X
+ * (with X^T X on the right where rows > columns: the same matrix, smaller
+ * products).  ortho gets the last X, in unit order.
+ *   Products take operands of 11 significant bits (fp16, scaled by powers
+ *   of two) and sum in fp32; the term a X and the diagonals of A and
+ *   b A + c A A are kept in about 22 and 24 bits.  With ortho FSDP_BF16 the result is
+ *   within about the rounding to bf16 of the exact one.  With FSDP_F32
+ *   every operand is kept as two fp16 parts and each product is the sum of
+ *   three: an error near that of fp32 products, at three times the work.
+ *   The steps' intermediate values must stay below 16 (X) and 64 (A and
+ *   b A + c A A): so they do for coefficients that map [0, 1.3] into
+ *   itself.  A matrix of zeros gives zeros.  One that holds an infinity
+ *   or a NaN gives NaN throughout; other matrices are not affected.
+ *   update, ortho: [T] of their types; the same buffer (same type), or
+ *   disjoint.  Elements outside the chosen parameters are neither read nor
+ *   written.
+ *   workspace: ortho_bytes of fsdp_muon_workspace, 256-byte aligned,
+ *   disjoint from both, contents undefined before and after.  Calls that
+ *   may overlap in time (other streams, replays of captured graphs) need
+ *   a workspace each. */
+fsdp_status fsdp_orthogonalize(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                               const void* update, int32_t update_dtype, void* ortho,
+                               int32_t ortho_dtype, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
+/* The master's update and the parameter's recast, for every element of the
+ * chosen parameters:
+ *   master[r][j] <- p (1 - lr wd) - (lr scale) ortho[i]   in IEEE double,
+ *                   rounded once to fp32
+ *   param_out[r][j] = the new master cast to param_dtype
+ *   ortho: [T] of ortho_dtype; master: [R][S] fp32; param_out: [R][S] of
+ *   param_dtype; pairwise disjoint.  Other parameters' elements and
+ *   padding are neither read nor written. */
+fsdp_status fsdp_muon_apply(const fsdp_muon* mu, const fsdp_muon_hparams* hp, const void* ortho,
+                            int32_t ortho_dtype, float* master, void* param_out,
+                            int32_t param_dtype, void* stream);
+
+/* One optimiser step of a unit: fsdp_muon_momentum, fsdp_orthogonalize (in
+ * place) and fsdp_muon_apply on the chosen parameters, the update and its
+ * result in bf16 in the workspace; and, with adamw given, the fused AdamW
+ * step of fsdp_adamw_shard_step with step counter `step` on all the others
+ * (the same results, bit for bit) and on the padding.  With adamw NULL the
+ * others and the padding are left as they are, and v and step are not used
+ * (v may be NULL).
+ *   grads: R gradient replicas [T] of grad_dtype; m holds Muon's momentum
+ *   for the chosen parameters and AdamW's first moment for the others.
+ *   master, m, v, param_out, gradients and workspace are pairwise disjoint
+ *   (two gradients may be the same).  workspace: step_bytes of
+ *   fsdp_muon_workspace, 256-byte aligned, used as fsdp_orthogonalize's. */
+fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
+                                 const fsdp_adamw_hparams* adamw, int64_t step,
+                                 const void* const* grads, int32_t grad_dtype, float* master,
+                                 float* m, float* v, void* param_out, int32_t param_dtype,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code (an fsdp_status value; any
  * other number gives "unknown status"). */
 const char* fsdp_status_string(int32_t status);

@@ -1,0 +1,128 @@
+"""Oracle of the Muon step: NumPy, float64 where the definition is, fp32 where
+the library's contract rounds.  Test infrastructure only."""
+
+from __future__ import annotations
+
+import numpy as np
+
+from oracle import fsdp_oracle as O
+
+POLY = (3.4445, -4.7750, 2.0315)
+
+
+def matrices(shapes):
+    """Parameters of two dimensions or more: (index, offset, rows, columns)."""
+    out, at = [], 0
+    for p, s in enumerate(shapes):
+        n = int(np.prod(s))
+        if len(s) >= 2:
+            out.append((p, at, s[0], n // s[0]))
+        at += n
+    return out
+
+
+def shard_map(po):
+    """[T] -> place in the buffer [R*S]."""
+    m = np.full(po.T, -1, np.int64)
+    for r in range(po.R):
+        for f0, s0, n in po.pieces(r):
+            m[f0:f0 + n] = r * po.S + s0 + np.arange(n)
+    return m
+
+
+def chosen_mask(shapes, params):
+    """[T]: whether an element belongs to a chosen parameter."""
+    ends = np.cumsum([0] + [int(np.prod(s)) for s in shapes])
+    mask = np.zeros(ends[-1], bool)
+    for p in params:
+        mask[ends[p]:ends[p + 1]] = True
+    return mask
+
+
+def widen(a):
+    """fp32 values of fp32, or of bf16 bits."""
+    return (a.astype(np.uint32) << 16).view(np.float32) if a.dtype == np.uint16 else a
+
+
+def cast(a, dtype):
+    return O.bf16_rne(a) if dtype == "bf16" else a.astype(np.float32)
+
+
+def mean(grads):
+    """fp32, in rank order, one division."""
+    s = widen(grads[0]).copy()
+    for g in grads[1:]:
+        s = s + widen(g)
+    return s / np.float32(len(grads))
+
+
+def momentum(g, m, mu, nesterov):
+    """One element-wise update from the averaged fp32 gradient."""
+    gd = (1.0 - mu) * g.astype(np.float64)
+    new = (mu * m.astype(np.float64) + gd).astype(np.float32)
+    u = (gd + mu * new.astype(np.float64)).astype(np.float32) if nesterov else new
+    return new, u
+
+
+def scale_of(rows, cols, scale):
+    if scale == "aspect":
+        return np.sqrt(np.float64(max(1.0, rows / cols)))
+    if scale == "rms":
+        return 0.2 * np.sqrt(np.float64(max(rows, cols)))
+    return 1.0
+
+
+def apply(p, x, lr, wd, scale):
+    return (p.astype(np.float64) * (1.0 - lr * wd) -
+            (lr * scale) * x.astype(np.float64)).astype(np.float32)
+
+
+def orthogonalize(u, steps=5, eps=1e-7, poly=POLY):
+    """The definition, float64."""
+    a, b, c = poly
+    x = u.astype(np.float64)
+    x = x / (np.sqrt((x * x).sum()) + eps)
+    t = x.shape[0] > x.shape[1]
+    x = x.T if t else x
+    for _ in range(steps):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T if t else x
+
+
+def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
+    """The definition with the library's documented precision: operands of
+    11 bits (split: of 22) under power-of-two scales, fp32 sums, the residual
+    in two parts and the diagonals of A and B in fp32.  What it is off the definition by
+    is what the kernels may be off by."""
+    f32 = np.float32
+
+    def parts(x, s):
+        hi = (x * f32(s)).astype(np.float16).astype(f32)
+        lo = (x * f32(s) - hi).astype(np.float16).astype(f32)
+        return hi / f32(s), lo / f32(s)
+
+    def prod(p, q):
+        r = p[0] @ q[0]
+        return r + (p[0] @ q[1] + p[1] @ q[0]) if split else r
+
+    norm = np.sqrt((u.astype(np.float64) ** 2).sum()) + eps
+    e = int(np.floor(np.log2(norm)))
+    f = 2.0 ** e / norm
+    x = (u.astype(np.float64) * 2.0 ** -e).astype(f32)
+    t = x.shape[0] > x.shape[1]
+    x = np.ascontiguousarray(x.T if t else x)
+    for s in range(steps):
+        a, b, c = [f32(k) for k in ((poly[0] * f, poly[1] * f ** 3, poly[2] * f ** 5)
+                                    if s == 0 else poly)]
+        x = parts(x, 4096)
+        g = prod(x, (x[0].T, x[1].T))
+        d = np.diag(g).copy()
+        g = parts(g - np.diag(d), 1024)
+        own = g[0] + g[1] if split else g[0]
+        y = (b + c * (d[:, None] + d[None])) * own + c * prod(g, g)
+        d = d * (b + c * d) + np.diag(y)
+        np.fill_diagonal(y, 0)
+        y = parts(y, 1024)
+        x = (a + d)[:, None] * (x[0] + x[1]) + prod(y, x)
+    return x.T if t else x
