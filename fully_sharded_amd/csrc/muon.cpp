@@ -18,7 +18,7 @@ constexpr int64_t kItem = 1024;           // elements per work item of the per-e
 constexpr int64_t kMaxSide = int64_t(1) << 30;
 constexpr int64_t kNormChunk = 4096;      // least elements per partial sum
 constexpr int64_t kNormParts = 1024;      // most partial sums per matrix
-constexpr int kTile = 128;                // side of a product's tile
+constexpr int64_t kCus = 256;             // compute units
 constexpr int kConvert = 64;              // side of a conversion's tile
 constexpr int kXcds = 8;
 
@@ -40,7 +40,7 @@ void emit(int64_t dst, int64_t src, int64_t len, int32_t mat, std::vector<MuonIt
 // contiguous parts, one for each die, and the parts dealt out in turn.
 class Deal {
  public:
-  void add(const std::vector<MuonTile>& tiles) {
+  void add(const std::vector<MuonGemmTile>& tiles) {
     const int64_t n = static_cast<int64_t>(tiles.size());
     int64_t at = 0;
     for (int k = 0; k < kXcds; ++k) {
@@ -52,8 +52,8 @@ class Deal {
     }
     next_ = static_cast<int>((next_ + n) % kXcds);
   }
-  std::vector<MuonTile> dealt() const {
-    std::vector<MuonTile> out;
+  std::vector<MuonGemmTile> dealt() const {
+    std::vector<MuonGemmTile> out;
     size_t longest = 0;
     for (const auto& q : queue_) longest = std::max(longest, q.size());
     for (size_t r = 0; r < longest; ++r)
@@ -63,21 +63,50 @@ class Deal {
   }
 
  private:
-  std::vector<MuonTile> queue_[kXcds];
+  std::vector<MuonGemmTile> queue_[kXcds];
   int next_ = 0;  // dies before this one have one tile more than the others
 };
 
 // Tiles of a grid of ni x nj, in bands of 8 rows, column by column: any 32
 // consecutive ones (a die's compute units) share 8 row panels and 4 column
 // panels.  lower: those of the lower triangle.
-std::vector<MuonTile> grid(int32_t mat, int64_t ni, int64_t nj, bool lower) {
-  std::vector<MuonTile> out;
+std::vector<MuonGemmTile> grid(const MuonMat& t, int32_t mat, int64_t ni, int64_t nj,
+                               bool lower) {
+  std::vector<MuonGemmTile> out;
   for (int64_t b = 0; b < ni; b += 8)
     for (int64_t j = 0; j < nj; ++j)
       for (int64_t i = b; i < std::min(ni, b + 8); ++i)
         if (!lower || i >= j)
-          out.push_back(MuonTile{mat, static_cast<int32_t>(i), static_cast<int32_t>(j), 0});
+          out.push_back(MuonGemmTile{t.off_x, t.off_a, t.flat_off, static_cast<int32_t>(t.off_d),
+                                     static_cast<int32_t>(i), static_cast<int32_t>(j), mat, t.mp,
+                                     t.np, t.m, t.n, t.ldx, t.lda, t.tall, 0});
   return out;
+}
+
+int64_t count(const std::vector<MuonMat>& mats, int64_t tile, bool square) {
+  int64_t n = 0;
+  for (const MuonMat& t : mats) {
+    const int64_t si = (t.mp + tile - 1) / tile, sj = (t.np + tile - 1) / tile;
+    n += square ? si * (si + 1) / 2 : si * sj;
+  }
+  return n;
+}
+
+// The tile of one kind of product (index into kMuonTiles): the largest that
+// still gives every compute unit two.  256 x 256 tiles also need deep sums to
+// pay for their long ends: the step of 72 matrices of hidden 512 (576 such
+// tiles, depth 512) took 126 us with them and 105 with 128 x 128, the step
+// of the hidden-4096 block (depth 4096) 1.64 against 2.1 ms; one block of
+// hidden 512 (192 tiles of 128 x 128) 169 us a pass with those against 157.
+int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool split) {
+  int64_t tiles = 0, rounds = 0;
+  for (const MuonMat& t : mats) {
+    const int64_t n = count({t}, 256, square);
+    tiles += n;
+    rounds += n * (gram ? t.np : t.mp);
+  }
+  if (!split && tiles >= 2 * kCus && rounds >= tiles * 1024) return 2;
+  return count(mats, 128, square) >= 2 * kCus ? 1 : 0;
 }
 
 }  // namespace
@@ -105,12 +134,14 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     t.n = static_cast<int32_t>(std::max(t.rows, t.cols));
     t.mp = static_cast<int32_t>(round_up(t.m, kMuonPad));
     t.np = static_cast<int32_t>(round_up(t.n, kMuonPad));
+    t.ldx = static_cast<int32_t>(muon_pitch(t.np));
+    t.lda = static_cast<int32_t>(muon_pitch(t.mp));
     t.off_x = mu->nx;
     t.off_a = mu->na;
     t.off_d = mu->nd;
     t.index = p;
-    mu->nx += int64_t(t.mp) * t.np;
-    mu->na += int64_t(t.mp) * t.mp;
+    mu->nx += int64_t(t.mp) * t.ldx;
+    mu->na += int64_t(t.mp) * t.lda;
     mu->nd += t.mp;
     const int64_t numel = t.rows * t.cols;
     t.norm_chunk =
@@ -124,13 +155,13 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
   int64_t n_convert = 0, n_wide = 0, n_square = 0;
   for (const MuonMat& t : mu->mats) {
     n_convert += int64_t(t.mp / kConvert) * (t.np / kConvert);
-    const int64_t si = (t.mp + kTile - 1) / kTile, sj = (t.np + kTile - 1) / kTile;
+    const int64_t si = t.mp / kMuonTiles[0], sj = t.np / kMuonTiles[0];
     n_wide += si * sj;
     n_square += si * (si + 1) / 2;
     if (n_convert > kMaxItems || n_wide > kMaxItems || n_square > kMaxItems)
       return FSDP_ERR_UNSUPPORTED;
   }
-  if (mu->n_partial > kMaxItems) return FSDP_ERR_UNSUPPORTED;
+  if (mu->n_partial > kMaxItems || mu->nd > INT32_MAX) return FSDP_ERR_UNSUPPORTED;
 
   // the per-element work: the plan's runs, cut where parameters end
   std::vector<Work> rest;
@@ -176,24 +207,29 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
         mu->convert.push_back(MuonTile{k, static_cast<int32_t>(i), static_cast<int32_t>(j), 0});
   }
   // products: the longest sums first, so that the short ones fill the end
-  std::vector<int32_t> order(n_params);
-  for (int32_t k = 0; k < n_params; ++k) order[k] = k;
-  std::stable_sort(order.begin(), order.end(),
-                   [&](int32_t a, int32_t b) { return mu->mats[a].np > mu->mats[b].np; });
-  Deal square;
-  for (int32_t k : order) {
-    const int64_t s = (mu->mats[k].mp + kTile - 1) / kTile;
-    square.add(grid(k, s, s, true));
+  for (int split = 0; split < 2; ++split) {
+    fsdp_muon::Tiles& to = mu->tiles[split];
+    auto fill = [&](std::vector<MuonGemmTile>& out, int* shape, bool square, bool gram) {
+      *shape = shape_of(mu->mats, square, gram, split != 0);
+      auto depth = [gram](const MuonMat& t) { return gram ? t.np : t.mp; };
+      const int64_t side = kMuonTiles[*shape];
+      std::vector<int32_t> order(n_params);
+      for (int32_t k = 0; k < n_params; ++k) order[k] = k;
+      std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
+        return depth(mu->mats[a]) > depth(mu->mats[b]);
+      });
+      Deal deal;
+      for (int32_t k : order) {
+        const MuonMat& t = mu->mats[k];
+        const int64_t si = (t.mp + side - 1) / side, sj = (t.np + side - 1) / side;
+        deal.add(square ? grid(t, k, si, si, true) : grid(t, k, si, sj, false));
+      }
+      out = deal.dealt();
+    };
+    fill(to.gram, &to.gram_shape, true, true);
+    fill(to.poly, &to.poly_shape, true, false);
+    fill(to.step, &to.step_shape, false, false);
   }
-  mu->square = square.dealt();
-  std::stable_sort(order.begin(), order.end(),
-                   [&](int32_t a, int32_t b) { return mu->mats[a].mp > mu->mats[b].mp; });
-  Deal wide;
-  for (int32_t k : order) {
-    const MuonMat& t = mu->mats[k];
-    wide.add(grid(k, (t.np + kTile - 1) / kTile, (t.mp + kTile - 1) / kTile, false));
-  }
-  mu->wide = wide.dealt();
   return FSDP_OK;
 }
 
@@ -210,14 +246,12 @@ MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split) {
   w.coef = take(static_cast<int64_t>(mu->mats.size()) * 16);
   w.adiag = take(mu->nd * 4);
   w.bdiag = take(mu->nd * 4);
-  w.xh = take(x);
-  w.th[0] = take(x);
-  w.th[1] = take(x);
-  w.tl[0] = take(x);
-  // the low part of the transpose is only read by the workgroup that
-  // replaces it, unless it is an operand too
-  w.tl[1] = split ? take(x) : w.tl[0];
-  w.xl = split ? take(x) : 0;
+  w.xh[0] = take(x);
+  w.xh[1] = take(x);
+  w.xl[0] = take(x);
+  // the low parts are only read by the workgroup that replaces them, unless
+  // they are an operand too
+  w.xl[1] = split ? take(x) : w.xl[0];
   w.ah = take(a);
   w.bh = take(a);
   w.al = split ? take(a) : 0;
@@ -237,26 +271,34 @@ using fsdp::overlap;
 using fsdp::range_of;
 using fsdp::valid_dtype;
 
-fsdp_status fsdp_muon::device(fsdp::MuonDevice* out) const {
+fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess) {
     (void)hipGetLastError();
     return FSDP_ERR_HIP;
   }
-  int64_t at[8], bytes = 0;
-  const void* from[7] = {mats.data(),   norm.data(),     convert.data(), square.data(),
-                         wide.data(),   momentum.data(), apply.data()};
-  const size_t size[7] = {mats.size() * sizeof(fsdp::MuonMat),
-                          norm.size() * sizeof(fsdp::MuonTile),
-                          convert.size() * sizeof(fsdp::MuonTile),
-                          square.size() * sizeof(fsdp::MuonTile),
-                          wide.size() * sizeof(fsdp::MuonTile),
-                          momentum.size() * sizeof(fsdp::MuonItem),
-                          apply.size() * sizeof(fsdp::MuonItem)};
-  for (int k = 0; k < 7; ++k) {
-    at[k] = bytes;
-    bytes += (static_cast<int64_t>(size[k]) + 255) / 256 * 256;
+  constexpr int kParts = 11;
+  const void* from[kParts];
+  int64_t size[kParts], at[kParts], bytes = 0;
+  int n = 0;
+  auto part = [&](const auto& v) {
+    from[n] = v.data();
+    size[n] = static_cast<int64_t>(v.size() * sizeof(v[0]));
+    at[n] = bytes;
+    bytes += (size[n] + 255) / 256 * 256;
+    ++n;
+  };
+  part(mats);
+  part(norm);
+  part(convert);
+  part(momentum);
+  part(apply);
+  for (const Tiles& t : tiles) {
+    part(t.gram);
+    part(t.poly);
+    part(t.step);
   }
+  static_assert(kParts == 5 + 2 * 3);
   std::lock_guard<std::mutex> lock(mu_);
   auto it = dev_.find(dev);
   if (it == dev_.end()) {
@@ -265,8 +307,9 @@ fsdp_status fsdp_muon::device(fsdp::MuonDevice* out) const {
       (void)hipGetLastError();
       return FSDP_ERR_OUT_OF_MEMORY;
     }
-    for (int k = 0; k < 7; ++k)
-      if (size[k] && hipMemcpy(static_cast<char*>(mem) + at[k], from[k], size[k],
+    for (int k = 0; k < kParts; ++k)
+      if (size[k] && hipMemcpy(static_cast<char*>(mem) + at[k], from[k],
+                               static_cast<size_t>(size[k]),
                                hipMemcpyHostToDevice) != hipSuccess) {
         (void)hipGetLastError();
         (void)hipFree(mem);
@@ -278,10 +321,17 @@ fsdp_status fsdp_muon::device(fsdp::MuonDevice* out) const {
   out->mats = reinterpret_cast<const fsdp::MuonMat*>(b + at[0]);
   out->norm = reinterpret_cast<const fsdp::MuonTile*>(b + at[1]);
   out->convert = reinterpret_cast<const fsdp::MuonTile*>(b + at[2]);
-  out->square = reinterpret_cast<const fsdp::MuonTile*>(b + at[3]);
-  out->wide = reinterpret_cast<const fsdp::MuonTile*>(b + at[4]);
-  out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[5]);
-  out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[6]);
+  out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[3]);
+  out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[4]);
+  const Tiles& t = tiles[split ? 1 : 0];
+  const int k = split ? 8 : 5;
+  auto gemm = [&](int i, const std::vector<fsdp::MuonGemmTile>& v, int shape) {
+    return fsdp::MuonTiles{reinterpret_cast<const fsdp::MuonGemmTile*>(b + at[i]),
+                           static_cast<int64_t>(v.size()), shape};
+  };
+  out->gram = gemm(k, t.gram, t.gram_shape);
+  out->poly = gemm(k + 1, t.poly, t.poly_shape);
+  out->step = gemm(k + 2, t.step, t.step_shape);
   return FSDP_OK;
 }
 
@@ -342,23 +392,20 @@ fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
   a.mats = d.mats;
   a.ws = ws;
   a.split = ortho_dt == FSDP_F32;
+  a.low = a.split || update_dt == FSDP_F32;
   a.w = fsdp::muon_workspace(mu, a.split);
   const double poly[3] = {hp->ns_a, hp->ns_b, hp->ns_c};
-  auto with = [&](const fsdp::MuonTile* t, const std::vector<fsdp::MuonTile>& host) {
-    a.tiles = t;
-    a.n_tiles = static_cast<int64_t>(host.size());
-    return a;
-  };
-  hipError_t e = fsdp::launch_muon_norm(with(d.norm, mu->norm), update, update_dt, sink);
+  hipError_t e = fsdp::launch_muon_norm(a, d.norm, static_cast<int64_t>(mu->norm.size()), update,
+                                        update_dt, sink);
   if (e == hipSuccess)
-    e = fsdp::launch_muon_convert(with(d.convert, mu->convert), update, update_dt, hp->eps, poly,
-                                  sink);
+    e = fsdp::launch_muon_convert(a, d.convert, static_cast<int64_t>(mu->convert.size()), update,
+                                  update_dt, hp->eps, poly, sink);
   for (int s = 0; s < hp->ns_steps && e == hipSuccess; ++s) {
-    e = fsdp::launch_muon_gram(with(d.square, mu->square), sink);
-    if (e == hipSuccess) e = fsdp::launch_muon_poly(a, s == 0, poly, sink);
+    e = fsdp::launch_muon_gram(a, d.gram, s & 1, sink);
+    if (e == hipSuccess) e = fsdp::launch_muon_poly(a, d.poly, s == 0, poly, sink);
     if (e == hipSuccess)
-      e = fsdp::launch_muon_step(with(d.wide, mu->wide), s & 1, s == 0, s == hp->ns_steps - 1,
-                                 poly, ortho, ortho_dt, sink);
+      e = fsdp::launch_muon_step(a, d.step, s & 1, s == 0, s == hp->ns_steps - 1, poly, ortho,
+                                 ortho_dt, sink);
   }
   return fsdp::status_of(e);
 }
@@ -392,7 +439,7 @@ fsdp_status fsdp_muon_prepare(const fsdp_muon* mu, void* stream) {
     if (!mu) return FSDP_ERR_INVALID_ARG;
     fsdp::MuonDevice d;
     const fsdp::Work* w = nullptr;
-    const fsdp_status st = mu->device(&d);
+    const fsdp_status st = mu->device(false, &d);
     return st != FSDP_OK ? st : mu->rest.device(&w);
   });
 }
@@ -440,7 +487,7 @@ fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
     writes.push_back(range_of(update, mu->T * ues));
     if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
     fsdp::MuonDevice d;
-    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    if ((st = mu->device(false, &d)) != FSDP_OK) return st;
     return fsdp::status_of(fsdp::launch_muon_momentum(
         d.momentum, static_cast<int64_t>(mu->momentum.size()), g, mu->R, grad_dtype,
         grads_are_replicas != 0, m, update, update_dtype, scalars(hp), vec,
@@ -469,7 +516,7 @@ fsdp_status fsdp_orthogonalize(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
     if (overlap(w, u) || overlap(w, o) || (!in_place && overlap(u, o)))
       return FSDP_ERR_INVALID_ARG;
     fsdp::MuonDevice d;
-    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    if ((st = mu->device(ortho_dtype == FSDP_F32, &d)) != FSDP_OK) return st;
     return orthogonalize(mu, d, hp, update, update_dtype, ortho, ortho_dtype,
                          static_cast<char*>(workspace), fsdp::StreamSink(stream));
   });
@@ -493,7 +540,7 @@ fsdp_status fsdp_muon_apply(const fsdp_muon* mu, const fsdp_muon_hparams* hp, co
     writes.push_back(range_of(param_out, mu->R * mu->S * pes));
     if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
     fsdp::MuonDevice d;
-    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    if ((st = mu->device(false, &d)) != FSDP_OK) return st;
     return fsdp::status_of(fsdp::launch_muon_apply(
         d.apply, static_cast<int64_t>(mu->apply.size()), d.mats, ortho, ortho_dtype, master,
         param_out, param_dtype, scalars(hp),
@@ -535,7 +582,7 @@ fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* h
     if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
     fsdp::MuonDevice d;
     const fsdp::Work* rest = nullptr;
-    if ((st = mu->device(&d)) != FSDP_OK) return st;
+    if ((st = mu->device(false, &d)) != FSDP_OK) return st;
     if (adamw && (st = mu->rest.device(&rest)) != FSDP_OK) return st;
     const fsdp::StreamSink sink(stream);
     void* update = workspace;

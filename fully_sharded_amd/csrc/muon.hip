@@ -1,15 +1,14 @@
 // gfx950 kernels of the Muon step.
 //
 // The per-element kernels (momentum, apply) touch every byte once and are
-// bound by HBM.  The Newton-Schulz products are matrix products of the
-// form D = P Q^T with both operands' rows contiguous along the sum, so one
-// tile loop serves all three of a step:
-//   A  = X X^T          P = Q = X  (m x n)       lower triangle, mirrored
-//   B  = b A + c A A    P = Q = A  (symmetric)   lower triangle, mirrored
-//   X' = a X + B X, as its transpose X'^T = a X^T + X^T B:
-//                       P = X^T (n x m), Q = B (symmetric)
-// The last one writes both X'^T (the next step's P and residual) and X'
-// (the next A's operand), so no product ever needs a transposed read.
+// bound by HBM.  The Newton-Schulz products of one step are
+//   A  = X X^T          lower triangle, mirrored into the upper
+//   B  = b A + c A A    the same (A is symmetric)
+//   X' = a X + B X
+// and share one tile loop.  The rows of A's, B's and the first product's
+// operands lie along the sum; X in the last one lies across it and is
+// transposed on its way from LDS to registers (the 16-bit transposing LDS
+// read), so X is kept, written and read in one orientation only.
 //
 // Operands are fp16: the matrices are bounded (singular values near 1), so
 // a fixed power of two keeps them in range, and fp16 has 3 bits more than
@@ -24,6 +23,8 @@
 //   A A = (A - d)(A - d) + (d_i + d_j) (A - d)_ij + d^2
 //   X'  = (a + e) X + (B - e) X
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "muon.hpp"
 
@@ -295,25 +296,41 @@ struct ConvertArgs {
   const MuonTile* tiles;
   const double* partial;
   float* coef;  // per matrix: a f, b f^3, c f^5
-  _Float16 *xh, *xl, *th, *tl;
+  _Float16 *xh, *xl;  // xl null: the low parts are not wanted
   double eps, a, b, c;
 };
 
-__device__ __forceinline__ void split_half(float x, _Float16& hi, _Float16& lo) {
-  hi = static_cast<_Float16>(x);
-  lo = static_cast<_Float16>(x - static_cast<float>(hi));
-}
-
-// 64 x 64 tiles of the update into X and its transpose.  With |U| + eps =
-// N, the planes get U 2^-e with 2^e <= N < 2^(e+1): exact for bf16
-// updates.  What is left, f = 2^e / N, goes into the first step's
-// coefficients: A is then A f^-2 and X is X f^-1.
+// 64 x 64 tiles of the update into X, transposed where the parameter has
+// more rows than columns.  With |U| + eps = N, the planes get U 2^-e with
+// 2^e <= N < 2^(e+1): exact for bf16 updates.  What is left, f = 2^e / N,
+// goes into the first step's coefficients: A is then A f^-2 and X is X f^-1.
+// A lane has 16 adjacent entries of a row.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ update,
                                                       ConvertArgs a) {
-  __shared__ float tile[64][65];
+  constexpr int Ld = 72;
+  __shared__ __align__(16) _Float16 tile[64 * Ld];
   const MuonTile t = a.tiles[blockIdx.x];
   const MuonMat& mat = a.mats[t.mat];
+  const int64_t r0 = int64_t(t.i) * 64, c0 = int64_t(t.j) * 64;
+  const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
+  const int64_t r = r0 + lr, c = c0 + lc;
+  const T* u = update + mat.flat_off + r * mat.cols + c;
+  float x[16];
+  if (r < mat.rows && c + 16 <= mat.cols &&
+      (reinterpret_cast<uintptr_t>(u) & (4 * sizeof(T) - 1)) == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y[4];
+      El<T>::load4(u + 4 * k, y);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[4 * k + q] = y[q];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      x[k] = r < mat.rows && c + k < mat.cols ? El<T>::load(u + k) : 0.f;
+  }
   double s = 0;
   for (int k = threadIdx.x; k < mat.norm_count; k += kThreads)
     s += a.partial[mat.norm_first + k];
@@ -323,146 +340,304 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
   if (t.i == 0 && t.j == 0 && threadIdx.x == 0) {
     const double f = ldexp(1.0, e) / norm;
     const bool bad = !(norm < INFINITY);
-    float* c = a.coef + 4 * t.mat;
-    c[0] = bad ? NAN : static_cast<float>(a.a * f);
-    c[1] = bad ? NAN : static_cast<float>(a.b * f * f * f);
-    c[2] = bad ? NAN : static_cast<float>(a.c * f * f * f * f * f);
+    float* k = a.coef + 4 * t.mat;
+    k[0] = bad ? NAN : static_cast<float>(a.a * f);
+    k[1] = bad ? NAN : static_cast<float>(a.b * f * f * f);
+    k[2] = bad ? NAN : static_cast<float>(a.c * f * f * f * f * f);
   }
-  const int64_t r0 = int64_t(t.i) * 64, c0 = int64_t(t.j) * 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const T* u = update + mat.flat_off;
-  // the parameter's own orientation, and the other
-  const int64_t ld = mat.tall ? mat.mp : mat.np, ldt = mat.tall ? mat.np : mat.mp;
-  _Float16* oh = (mat.tall ? a.th : a.xh) + mat.off_x;
-  _Float16* ol = mat.tall ? a.tl : a.xl;
-  _Float16* ph = (mat.tall ? a.xh : a.th) + mat.off_x;
-  _Float16* pl = mat.tall ? a.xl : a.tl;
-  for (int k = wave; k < 64; k += kThreads / 64) {
-    const int64_t r = r0 + k, c = c0 + lane;
-    float x = 0.f;
-    if (r < mat.rows && c < mat.cols)
-      x = static_cast<float>(static_cast<double>(El<T>::load(u + r * mat.cols + c)) * scale);
-    tile[k][lane] = x;
-    _Float16 hi, lo;
-    split_half(x, hi, lo);
-    oh[r * ld + c] = hi;
-    if (ol) ol[mat.off_x + r * ld + c] = lo;
-  }
-  __syncthreads();
-  for (int k = wave; k < 64; k += kThreads / 64) {
-    const int64_t c = c0 + k, r = r0 + lane;
-    _Float16 hi, lo;
-    split_half(tile[lane][k], hi, lo);
-    ph[c * ldt + r] = hi;
-    if (pl) pl[mat.off_x + c * ldt + r] = lo;
+  union {
+    _Float16 h[16];
+    u4 v[2];
+  } part;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] = static_cast<float>(static_cast<double>(x[k]) * scale);
+  for (int low = 0; low < (a.xl ? 2 : 1); ++low) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      part.h[k] = static_cast<_Float16>(x[k]);
+      x[k] -= static_cast<float>(part.h[k]);
+    }
+    _Float16* out = (low ? a.xl : a.xh) + mat.off_x;
+    if (!mat.tall) {
+      u4* d = reinterpret_cast<u4*>(out + r * mat.ldx + c);
+      d[0] = part.v[0];
+      d[1] = part.v[1];
+    } else {
+      __syncthreads();
+      u4* d = reinterpret_cast<u4*>(tile + lr * Ld + lc);
+      d[0] = part.v[0];
+      d[1] = part.v[1];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) part.h[k] = tile[(lc + k) * Ld + lr];
+      d = reinterpret_cast<u4*>(out + (c0 + lr) * mat.ldx + r0 + lc);
+      d[0] = part.v[0];
+      d[1] = part.v[1];
+    }
   }
 }
 
 // ---------------------------------------------------------------- products
 struct GemmArgs {
-  const MuonMat* mats;
-  const MuonTile* tiles;
+  const MuonGemmTile* tiles;
   const float* coef;  // non-null: the first step's coefficients, per matrix
   float a, b, c;      // the other steps'
   float *adiag, *bdiag;  // the diagonals of A and B
-  _Float16 *xh, *xl;
-  const _Float16 *th, *tl;  // X^T of this step
-  _Float16 *uh, *ul;        // X^T of the next
+  const _Float16 *xh, *xl;  // X of this step (xl null in the first one: zeros)
+  _Float16 *yh, *yl;        // X of the next
   _Float16 *ah, *al, *bh, *bl;
   void* ortho;
 };
 
 enum Stage { kGram, kPoly, kStep, kLast };
 
-// BM x BN tile of P Q^T, 64 of the sum per round, double-buffered in LDS:
-// a round's loads go straight to LDS and are waited for a round later.
-// Rows of 64 halves are 128 bytes, 8 chunks of 16; chunk c of row r sits at
-// place c ^ (r & 7), so that the 16 rows a wave reads at one place of the
-// sum spread over all banks.  Operand rows past the plane's last are read
-// from the last one; their results are not stored.
-template <int BM, int BN, int WM, int WN, Stage ST, bool SPLIT, typename O>
-__global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs g) {
-  constexpr int NW = WM * WN;
-  constexpr int TM = BM / WM, TN = BN / WN;    // a wave's tile
-  constexpr int FM = TM / 16, FN = TN / 16;    // its 16 x 16 parts
-  constexpr int BK = 64;
-  __shared__ __align__(128) char lds[2][(BM + BN) * BK * 2];
+// A BM x BN tile by WM x WN waves, BK of the sum per round, NS rounds in LDS,
+// registers for WPS waves per SIMD.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int NS_, int WPS_>
+struct Shape {
+  static constexpr int Waves = WPS_;  // per SIMD
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, NS = NS_;
+  static constexpr int NW = WM * WN, Threads = 64 * NW;
+  static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's tile
+  static constexpr int FM = TM / 16, FN = TN / 16;  // its 16 x 16 parts
+  static constexpr int RB = BK * 2;                 // bytes of a row of one round
+  static constexpr int RowsPerLoad = 1024 / RB;     // rows that one wave's load fills
+  static constexpr int LP = BM / RowsPerLoad / NW, LQ = BN / RowsPerLoad / NW;
+  static constexpr int RoundBytes = (BM + BN) * RB;
+};
 
-  const MuonTile t = g.tiles[blockIdx.x];
-  const MuonMat& mat = g.mats[t.mat];
+// The place of 16-byte chunk c of row r in LDS: the 16 rows that a wave reads
+// at one chunk, 128 or 64 bytes apart, spread over all banks.
+template <int BK>
+__device__ __forceinline__ int place(int r, int c) {
+  return BK == 64 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+}
+// The same for rows across the sum (BN entries): a transposing read takes 32
+// bytes of rows 0-3, 8-11, 16-19 and 24-27 (or 4-7, ...) of 32 at a time, so
+// the pairs of chunks move by bits 0, 1 and 3 of the row; rows of 128 bytes
+// alternate by themselves with bit 0.
+template <int BN>
+__device__ __forceinline__ int place_across(int r, int c) {
+  const int b = (r & 3) | ((r >> 1) & 4);
+  return c ^ (BN == 64 ? b & 6 : b << 1);
+}
+
+// 16 bytes per lane from global memory to LDS at a wave-uniform address, lane
+// after lane.  An asm statement (it writes no register): of the builtin the
+// compiler waits for all loads under way before every transposing LDS read,
+// which it cannot tell from a read of the bytes being loaded.  Waited for by
+// wait_and_meet.
+__device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
+               "s"(__builtin_amdgcn_readfirstlane(to))
+               : "memory");
+}
+
+// Wait until at most N of this wave's global accesses are under way and all
+// its LDS reads are done (the builtin, not an asm statement: the compiler
+// counts on from it), then for the other waves.
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+}
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(N < 64);
+  // products stay on their side: those before it hide the loads waited for
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// 4 x 4 half-words over 4 adjacent lanes, transposed: lane s holds (x, y) =
+// entries 0..3 of row s and gets entry s of rows 0..3.
+__device__ __forceinline__ u2 transpose4(u2 v, uint32_t odd_sel, bool high) {
+  // with the neighbour: even lanes entries 0 and 2 of rows (s, s+1), odd
+  // lanes entries 1 and 3 of rows (s-1, s)
+  const uint32_t px = __builtin_amdgcn_mov_dpp(v.x, 0xB1, 0xf, 0xf, true);
+  const uint32_t py = __builtin_amdgcn_mov_dpp(v.y, 0xB1, 0xf, 0xf, true);
+  const uint32_t x = __builtin_amdgcn_perm(px, v.x, odd_sel);
+  const uint32_t y = __builtin_amdgcn_perm(py, v.y, odd_sel);
+  // with the lane two away
+  const uint32_t qx = __builtin_amdgcn_mov_dpp(x, 0x4E, 0xf, 0xf, true);
+  const uint32_t qy = __builtin_amdgcn_mov_dpp(y, 0x4E, 0xf, 0xf, true);
+  return high ? u2{qy, y} : u2{x, qx};
+}
+
+__device__ __forceinline__ u2 pack4(const float (&x)[4]) {
+  union {
+    h4 h;
+    u2 u;
+  } v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v.h[r] = static_cast<_Float16>(x[r]);
+  return v.u;
+}
+
+// 16 of a wave's rows to global memory, 16 bytes per lane, through LDS of the
+// wave's own: v[j] is row lane % 16, columns 16 j + 4 (lane / 16) + 0..3.
+// store(row, col, eight adjacent entries).
+template <int FN, typename F>
+__device__ __forceinline__ void store_rows(char* lds, const u2 (&v)[FN], F store) {
+  constexpr int Ld = (FN * 16 + 8) * 2;  // bytes: rows spread over the banks
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    *reinterpret_cast<u2*>(lds + (lane & 15) * Ld + (j * 16 + (lane >> 4) * 4) * 2) = v[j];
+  constexpr int PerRow = FN * 2, Rows = 64 / PerRow, N = 16 / Rows;
+  const int r = lane / PerRow, c = lane % PerRow * 8;
+  u4 out[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    out[k] = *reinterpret_cast<const u4*>(lds + (k * Rows + r) * Ld + c * 2);
+#pragma unroll
+  for (int k = 0; k < N; ++k) store(k * Rows + r, c, out[k]);
+}
+
+// The same values into a transposed image (columns as rows, ld bytes each).
+template <int FN>
+__device__ __forceinline__ void keep_transposed(char* lds, int ld, int i, const u2 (&v)[FN]) {
+  const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
+  const uint32_t sel = lane & 1 ? 0x03020706u : 0x05040100u;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    *reinterpret_cast<u2*>(lds + (j * 16 + lk * 4 + (lr & 3)) * ld + (i * 16 + (lr & 12)) * 2) =
+        transpose4(v[j], sel, lane & 2);
+}
+
+// A transposed image of R rows of C to global memory.
+template <int R, int C, typename F>
+__device__ __forceinline__ void store_image(const char* lds, F store) {
+  constexpr int Ld = (C + 8) * 2, PerRow = C / 8, Rows = 64 / PerRow, N = R / Rows;
+  constexpr int Batch = N < 8 ? N : 8;
+  const int lane = threadIdx.x & 63;
+  const int r = lane / PerRow, c = lane % PerRow * 8;
+#pragma unroll
+  for (int b = 0; b < N; b += Batch) {
+    u4 out[Batch];
+#pragma unroll
+    for (int k = 0; k < Batch; ++k)
+      out[k] = *reinterpret_cast<const u4*>(lds + ((b + k) * Rows + r) * Ld + c * 2);
+#pragma unroll
+    for (int k = 0; k < Batch; ++k) store((b + k) * Rows + r, c, out[k]);
+  }
+}
+
+// One tile of a product.  A round's loads go straight to LDS, NS - 1 rounds
+// ahead.  The products of one part of a round (32 of the sum) are issued row
+// by row with the LDS reads of the next part and the loads of a later round
+// between them: issued in one go, those loads keep a wave from its products
+// for a thousand cycles.  Operand rows and columns past the plane's last are
+// read from the last ones; their results are not stored.
+template <typename S, Stage ST, bool SPLIT, typename O>
+__global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0)) void k_gemm(
+    GemmArgs g) {
+  constexpr int FM = S::FM, FN = S::FN, TM = S::TM, TN = S::TN, BK = S::BK, NS = S::NS;
+  constexpr int BM = S::BM, BN = S::BN, RB = S::RB, LP = S::LP, LQ = S::LQ;
+  constexpr bool kAcross = ST == kStep || ST == kLast;  // Q lies across the sum
+  constexpr bool kMirror = ST == kGram || ST == kPoly;
+  // a wave's part of LDS after the sums: 16 rows, and a transposed image
+  // (fp32 results: one of fp32, either way round)
+  constexpr int kRows = 16 * (TN + 8) * 2;
+  constexpr int kImage = ST == kStep ? 0 : TN * (TM + 8) * 2;
+  constexpr int kOut = ST == kLast && sizeof(O) == 4 ? (TM + 1) * (TN + 1) * 4 : kImage + kRows;
+  constexpr int kLds = S::RoundBytes * NS > kOut * S::NW ? S::RoundBytes * NS : kOut * S::NW;
+  __shared__ __align__(128) char lds[kLds];
+
+  const MuonGemmTile t = g.tiles[blockIdx.x];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int lr = lane & 15, lk = lane >> 4;
 
-  const int mp = mat.mp, np = mat.np;
+  const int mp = t.mp, np = t.np;
   const _Float16 *ph, *pl = nullptr, *qh, *ql = nullptr;
   int prows, qrows, depth;
+  int ld, lp, lq;  // of the result and of the operands
   if constexpr (ST == kGram) {
-    ph = qh = g.xh + mat.off_x;
-    if (SPLIT) pl = ql = g.xl + mat.off_x;
+    ph = qh = g.xh + t.off_x;
+    if (SPLIT) pl = ql = g.xl + t.off_x;
     prows = qrows = mp;
+    ld = t.lda;
+    lp = lq = t.ldx;
     depth = np;
   } else if constexpr (ST == kPoly) {
-    ph = qh = g.ah + mat.off_a;
-    if (SPLIT) pl = ql = g.al + mat.off_a;
+    ph = qh = g.ah + t.off_a;
+    if (SPLIT) pl = ql = g.al + t.off_a;
     prows = qrows = mp;
+    ld = lp = lq = t.lda;
     depth = mp;
   } else {
-    ph = g.th + mat.off_x;
-    qh = g.bh + mat.off_a;
+    ph = g.bh + t.off_a;
+    qh = g.xh + t.off_x;
     if (SPLIT) {
-      pl = g.tl + mat.off_x;
-      ql = g.bl + mat.off_a;
+      pl = g.bl + t.off_a;
+      ql = g.xl + t.off_x;
     }
-    prows = np;
-    qrows = mp;
+    prows = mp;
+    qrows = np;
+    lp = t.lda;
+    ld = lq = t.ldx;
     depth = mp;
   }
   const int i0 = t.i * BM, j0 = t.j * BN;
 
-  // this lane's part of a round's loads: rows 8 apart per wave, one chunk
-  constexpr int LP = BM / 8 / NW, LQ = BN / 8 / NW;
+  // this lane's part of a round's loads, from the round's first element
   int64_t po[LP], qo[LQ];
   {
-    const int r = lane >> 3, c = (lane & 7) ^ r;
+    constexpr int PerRow = BK / 8;
+    const int r = lane / PerRow, c = place<BK>(r, lane % PerRow);
 #pragma unroll
     for (int k = 0; k < LP; ++k) {
-      const int row = i0 + (wave * LP + k) * 8 + r;
-      po[k] = int64_t(row < prows ? row : prows - 1) * depth + c * 8;
+      const int row = i0 + (wave * LP + k) * S::RowsPerLoad + r;
+      po[k] = int64_t(row < prows ? row : prows - 1) * lp + c * 8;
     }
+    if constexpr (kAcross) {
+      constexpr int Chunks = BN / 8, Rows = 64 / Chunks;
 #pragma unroll
-    for (int k = 0; k < LQ; ++k) {
-      const int row = j0 + (wave * LQ + k) * 8 + r;
-      qo[k] = int64_t(row < qrows ? row : qrows - 1) * depth + c * 8;
+      for (int k = 0; k < LQ; ++k) {
+        const int row = (wave * LQ + k) * Rows + lane / Chunks;
+        const int col = j0 + place_across<BN>(row, lane % Chunks) * 8;
+        qo[k] = int64_t(row) * lq + (col < np ? col : np - 8);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < LQ; ++k) {
+        const int row = j0 + (wave * LQ + k) * S::RowsPerLoad + r;
+        qo[k] = int64_t(row < qrows ? row : qrows - 1) * lq + c * 8;
+      }
     }
   }
+  const int64_t qstep = kAcross ? int64_t(BK) * lq : BK;
   const int rounds = depth / BK;
   const int total = SPLIT ? 3 * rounds : rounds;
-  auto issue = [&](int it, int buf) {
-    const _Float16 *p = ph, *q = qh;
+  // where round `it` begins in P and Q
+  struct From {
+    const _Float16 *p, *q;
+  };
+  auto from = [&](int it) {
+    From f{ph, qh};
     int k = it;
     if constexpr (SPLIT) {  // the small products first: high low, low high, high high
       const int part = it / rounds;
       k = it - part * rounds;
-      if (part == 0) q = ql;
-      if (part == 1) p = pl;
+      if (part == 0) f.q = ql;
+      if (part == 1) f.p = pl;
     }
-    p += k * BK;
-    q += k * BK;
-    char* base = lds[buf];
-#pragma unroll
-    for (int x = 0; x < LP; ++x)
-      __builtin_amdgcn_global_load_lds(
-          reinterpret_cast<const __attribute__((address_space(1))) void*>(
-              reinterpret_cast<uintptr_t>(p + po[x])),
-          (__attribute__((address_space(3))) void*)(base + (wave * LP + x) * 1024), 16, 0, 0);
-#pragma unroll
-    for (int x = 0; x < LQ; ++x)
-      __builtin_amdgcn_global_load_lds(
-          reinterpret_cast<const __attribute__((address_space(1))) void*>(
-              reinterpret_cast<uintptr_t>(q + qo[x])),
-          (__attribute__((address_space(3))) void*)(base + BM * 128 + (wave * LQ + x) * 1024), 16,
-          0, 0);
+    f.p += int64_t(k) * BK;
+    f.q += k * qstep;
+    return f;
+  };
+  // load x of a round's LP + LQ
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+  auto load = [&](const From& f, int buf, int x) {
+    const uint32_t base = lds0 + buf * S::RoundBytes + (x < LP ? 0 : BM * RB);
+    const _Float16* from1 = x < LP ? f.p + po[x < LP ? x : 0] : f.q + qo[x < LP ? 0 : x - LP];
+    const int at = x < LP ? wave * LP + x : wave * LQ + x - LP;
+    load_to_lds(from1, base + at * 1024);
   };
 
   f4 acc[FM][FN];
@@ -494,36 +669,175 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs g) {
       for (int j = 0; j < FN; ++j) sum[i][j] = f4{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int lr = lane & 15, lk = lane >> 4;
-  issue(0, 0);
-  for (int it = 0; it < total; ++it) {
-    // every wave's loads of this round have landed, and every wave has
-    // read the last round's buffer
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (it + 1 < total) issue(it + 1, (it + 1) & 1);
-    const char* base = lds[it & 1];
+  // ---- LDS to registers
+  constexpr int KK = BK / 32;
+  h8 p[2][FM], q[2][FN];
+  const int pat = (wm * TM + lr) * RB;
+  int qat[kAcross ? FN : 1];
+  if constexpr (kAcross) {
+    const int row = lk * 8 + (lr >> 2);  // and 4 more for the second half
 #pragma unroll
-    for (int kk = 0; kk < BK / 32; ++kk) {
-      h8 p[FM], q[FN];
+    for (int j = 0; j < FN; ++j)
+      qat[j] = BM * RB + row * BN * 2 +
+               place_across<BN>(row, wn * (TN / 8) + j * 2 + ((lr & 3) >> 1)) * 16 +
+               (lr & 1) * 8;
+  } else {
+    qat[0] = BM * RB + (wn * TN + lr) * RB;
+  }
+  auto fetch_p = [&](int buf, int kk, int set, int i) {
+    p[set][i] = *reinterpret_cast<const h8*>(lds + buf * S::RoundBytes +
+                                             place<BK>(lr, kk * 4 + lk) * 16 + pat +
+                                             i * 16 * RB);
+  };
+  auto fetch_q = [&](int buf, int kk, int set, int j) {
+    if constexpr (kAcross) {
+      typedef short s4 __attribute__((ext_vector_type(4)));
+      union {
+        s4 s[2];
+        h8 h;
+      } v;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        const int row = wm * TM + i * 16 + lr;
-        p[i] = *reinterpret_cast<const h8*>(base + row * 128 + (((kk * 4 + lk) ^ (row & 7)) * 16));
-      }
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int row = wn * TN + j * 16 + lr;
-        q[j] = *reinterpret_cast<const h8*>(base + BM * 128 + row * 128 +
-                                            (((kk * 4 + lk) ^ (row & 7)) * 16));
-      }
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q[j], p[i], acc[i][j], 0, 0, 0);
+      for (int half = 0; half < 2; ++half)
+        v.s[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4*)(lds + buf * S::RoundBytes + qat[j] +
+                                                    (kk * 32 + half * 4) * BN * 2));
+      q[set][j] = v.h;
+    } else {
+      q[set][j] = *reinterpret_cast<const h8*>(lds + buf * S::RoundBytes +
+                                               place<BK>(lr, kk * 4 + lk) * 16 + qat[0] +
+                                               j * 16 * RB);
     }
-    if (SPLIT && (it & 1)) flush();
+  };
+  // The products of operand set `set`, with the next operands (other set)
+  // read from `buf`, part kk, and with LOADS the loads of round f into
+  // buffer `into` between their rows.
+  auto products = [&](int set, int buf, int kk, auto loads, const From& f, int into) {
+    constexpr int kFetch = FM + FN, kLoad = LP + LQ;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int x = i * kFetch / FM; x < (i + 1) * kFetch / FM; ++x) {
+        if (x < FN)
+          fetch_q(buf, kk, set ^ 1, x);
+        else
+          fetch_p(buf, kk, set ^ 1, x - FN);
+      }
+      if constexpr (decltype(loads)::value) {
+#pragma unroll
+        for (int x = i * kLoad / FM; x < (i + 1) * kLoad / FM; ++x) load(f, into, x);
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(q[set][j], p[set][i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // What the results are added to: A's or X's own entries, 16 rows at a time,
+  // Ahead sets of them in registers: all, asked for before the sums begin, or
+  // as many as fit after them.  Loads and stores are waited for in order, so
+  // with one set ahead each set waited for the stores of the one before.
+  const int rb = i0 + wm * TM, cb = j0 + wn * TN;
+  constexpr bool kEarly = S::BM <= 128;
+  constexpr int Ahead = kEarly ? FM : FM / 2;
+  const _Float16* oh = ST == kPoly ? ph : qh;
+  const _Float16* ol = ST == kPoly ? pl : (g.xl ? g.xl + t.off_x : nullptr);
+  h4 h[Ahead][FN], l[Ahead][FN];
+  auto own_rows = [&](int i) {
+    const int64_t at = int64_t(rb + i * 16 + lr) * ld + cb + lk * 4;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      h[i % Ahead][j] = l[i % Ahead][j] = h4{0, 0, 0, 0};
+      if (ST != kGram && rb + i * 16 < prows && cb + j * 16 < qrows) {
+        h[i % Ahead][j] = *reinterpret_cast<const h4*>(oh + at + j * 16);
+        if ((kAcross || SPLIT) && ol)
+          l[i % Ahead][j] = *reinterpret_cast<const h4*>(ol + at + j * 16);
+      }
+    }
+  };
+  float ca = g.a, cb1 = g.b, cc = g.c, di[FM];
+  f4 dj[FN];
+  auto others = [&] {
+    if (g.coef) {
+      ca = g.coef[4 * t.mat];
+      cb1 = g.coef[4 * t.mat + 1];
+      cc = g.coef[4 * t.mat + 2];
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      dj[j] = f4{0.f, 0.f, 0.f, 0.f};
+      if (ST == kPoly && cb + j * 16 < qrows)
+        dj[j] = *reinterpret_cast<const f4*>(g.adiag + t.off_d + cb + j * 16 + lk * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      di[i] = 0.f;
+      if (ST != kGram && rb + i * 16 < prows)
+        di[i] = (ST == kPoly ? g.adiag : g.bdiag)[t.off_d + rb + i * 16 + lr];
+    }
+#pragma unroll
+    for (int i = 0; i < Ahead; ++i) own_rows(i);
+  };
+  if constexpr (kEarly) others();
+
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (s < total) {
+      const From f = from(s);
+#pragma unroll
+      for (int x = 0; x < LP + LQ; ++x) load(f, s, x);
+    }
+  if (total >= NS)
+    wait_and_meet<(NS - 1) * (LP + LQ)>();
+  else
+    wait_and_meet<0>();
+#pragma unroll
+  for (int j = 0; j < FN; ++j) fetch_q(0, 0, 0, j);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) fetch_p(0, 0, 0, i);
+  // Before a round's last part: the next round has landed for every wave, and
+  // every wave is done reading this one, whose buffer is loaded again.  The
+  // last round reads operands that nothing uses: with a tail of its own the
+  // accumulators were copied around in every round.
+  int buf = 0;
+  // round `it`, its last part's operands in set `set`
+  auto one = [&](int it, auto set, auto loads) {
+    const int next = buf + 1 == NS ? 0 : buf + 1;
+    constexpr int kWait = decltype(loads)::value ? (NS - 2) * (LP + LQ) : 0;
+    From f{};
+    if constexpr (KK == 2) {
+      wait_lds();  // set 0: asked for half a round ago
+      products(0, buf, 1, std::false_type{}, f, 0);
+    }
+    wait_and_meet<kWait>();
+    if (decltype(loads)::value) f = from(it + NS);
+    products(set, next, 0, loads, f, buf);
+    buf = next;
+  };
+  int it = 0;
+  if constexpr (KK == 2) {
+    for (; it + NS < total; ++it) {
+      one(it, 1, std::true_type{});
+      if (SPLIT && (it & 1)) flush();
+    }
+    for (; it < total; ++it) {
+      one(it, 1, std::false_type{});
+      if (SPLIT && (it & 1)) flush();
+    }
+  } else {
+    // total is even: the depth is a multiple of 64
+    auto two = [&](auto first, auto second) {
+      one(it, 0, first);
+      one(it + 1, 1, second);
+      if (SPLIT && (it & 2)) flush();
+    };
+    for (; it + 1 + NS < total; it += 2) two(std::true_type{}, std::true_type{});
+    if (it + NS < total) {
+      two(std::true_type{}, std::false_type{});
+      it += 2;
+    }
+    for (; it < total; it += 2) two(std::false_type{}, std::false_type{});
   }
   if constexpr (SPLIT) {
     flush();
@@ -533,111 +847,157 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm(GemmArgs g) {
       for (int j = 0; j < FN; ++j) acc[i][j] = sum[i][j];
   }
 
-  // acc[i][j][r]: row i0 + wm TM + 16 i + lane % 16 of P, row
-  // j0 + wn TN + 16 j + 4 (lane / 16) + r of Q
-  float ca = g.a, cb = g.b, cc = g.c;
-  if (g.coef) {
-    ca = g.coef[4 * t.mat];
-    cb = g.coef[4 * t.mat + 1];
-    cc = g.coef[4 * t.mat + 2];
-  }
+  // ---- the results: acc[i][j][r] is row rb + 16 i + lane % 16 of P, row or
+  // column cb + 16 j + 4 (lane / 16) + r of Q.  Planes are padded to
+  // multiples of 64: whole 16 x 16 parts are inside or outside.
+  char* rows16 = lds + wave * kOut;
+  char* image = rows16 + kRows;
+  constexpr int kImageLd = (TM + 8) * 2;
+  const bool mirror = ST == kLast ? t.tall : t.i != t.j;
+  O* out = static_cast<O*>(g.ortho) + t.flat_off;  // kLast
+  const int64_t cols = t.tall ? t.m : t.n;
+  // 16 bytes of the result where the rows' and the base's alignment allow it
+  const bool vec = ((reinterpret_cast<uintptr_t>(out) | (cols * 2)) & 15) == 0;
+  auto put = [&](int64_t r, int64_t c, int64_t n_rows, u4 v) {
+    if (r >= n_rows || c >= cols) return;
+    u16* d = reinterpret_cast<u16*>(out) + r * cols + c;
+    if (vec && c + 8 <= cols) {
+      *reinterpret_cast<u4*>(d) = v;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < cols) d[k] = static_cast<u16>(v[k / 2] >> (16 * (k & 1)));
+    }
+  };
+  // eight adjacent entries of a plane; it is padded to multiples of 64
+  auto to = [&](_Float16* plane, int64_t first, int64_t second, int n_cols) {
+    return [=](int r, int c, u4 v) {
+      if (second + c < n_cols)
+        *reinterpret_cast<u4*>(plane + (first + r) * ld + second + c) = v;
+    };
+  };
+  _Float16* dh = ST == kStep ? g.yh + t.off_x : (ST == kGram ? g.ah : g.bh) + t.off_a;
+  _Float16* dl = ST == kStep ? g.yl + t.off_x : (ST == kGram ? g.al : g.bl) + t.off_a;
+
+  if constexpr (!kEarly) others();
+  __syncthreads();  // every wave is done with the operands in LDS
+  if (rb >= prows || cb >= qrows) return;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int row = i0 + wm * TM + i * 16 + lr;
-    if (row >= prows) continue;
+    if (rb + i * 16 >= prows) break;
+    const int row = rb + i * 16 + lr;
+    u2 hi[FN], lo[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const int col = j0 + wn * TN + j * 16 + lk * 4;
-      if (col >= qrows) continue;
+      const int col = cb + j * 16 + lk * 4;
       float x[4];
-      const int64_t at = int64_t(row) * mp + col;  // in A, B or X^T
-      if constexpr (ST == kGram) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] = acc[i][j][r] * (kSa / (kSx * kSx));
-          if (row == col + r) {
-            g.adiag[mat.off_d + row] = x[r] * (1.f / kSa);
-            x[r] = 0.f;
-          }
+      for (int r = 0; r < 4; ++r) {
+        const float sum1 = acc[i][j][r];
+        const float own =
+            static_cast<float>(h[i % Ahead][j][r]) + static_cast<float>(l[i % Ahead][j][r]);
+        if constexpr (ST == kGram) {
+          x[r] = sum1 * (kSa / (kSx * kSx));
+        } else if constexpr (ST == kPoly) {
+          x[r] = fmaf(fmaf(cc, di[i] + dj[j][r], cb1), own, cc * (sum1 * (1.f / kSa)));
+        } else {
+          x[r] = fmaf(ca + di[i], own, sum1 * (1.f / kSa));
+          if (ST == kLast) x[r] *= 1.f / kSx;
         }
-      } else if constexpr (ST == kPoly) {
-        const h4 hi = *reinterpret_cast<const h4*>(ph + at);
-        h4 lo = {0, 0, 0, 0};
-        if (SPLIT) lo = *reinterpret_cast<const h4*>(pl + at);
-        const float di = g.adiag[mat.off_d + row];
-        const f4 dj = *reinterpret_cast<const f4*>(g.adiag + mat.off_d + col);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float own = static_cast<float>(hi[r]) + static_cast<float>(lo[r]);
-          x[r] = fmaf(fmaf(cc, di + dj[r], cb), own, cc * (acc[i][j][r] * (1.f / kSa)));
-          if (row == col + r) {
-            g.bdiag[mat.off_d + row] = fmaf(di, fmaf(cc, di, cb), x[r] * (1.f / kSa));
-            x[r] = 0.f;
-          }
-        }
-      } else {
-        const h4 hi = *reinterpret_cast<const h4*>(ph + at);
-        const h4 lo = *reinterpret_cast<const h4*>(g.tl + mat.off_x + at);
-        const f4 d = *reinterpret_cast<const f4*>(g.bdiag + mat.off_d + col);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float own = static_cast<float>(hi[r]) + static_cast<float>(lo[r]);
-          x[r] = fmaf(ca + d[r], own, acc[i][j][r] * (1.f / kSa));
+        if (kMirror && row == col + r) {
+          if (ST == kGram)
+            g.adiag[t.off_d + row] = x[r] * (1.f / kSa);
+          else
+            g.bdiag[t.off_d + row] = fmaf(di[i], fmaf(cc, di[i], cb1), x[r] * (1.f / kSa));
+          x[r] = 0.f;
         }
       }
-      if constexpr (ST == kLast) {
-        O* out = static_cast<O*>(g.ortho) + mat.flat_off;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (row < mat.n && col + r < mat.m)
-            El<O>::store(out + (mat.tall ? int64_t(row) * mat.cols + col + r
-                                         : int64_t(col + r) * mat.cols + row),
-                         x[r] * (1.f / kSx));
-      } else {
-        h4 hi, lo;
+      if constexpr (ST == kLast && sizeof(O) == 4) {
+        // in the parameter's orientation, one element at a time
+        float* f = reinterpret_cast<float*>(rows16);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          _Float16 a, b;
-          split_half(x[r], a, b);
-          hi[r] = a;
-          lo[r] = b;
+          const int y = i * 16 + lr, z = j * 16 + lk * 4 + r;
+          f[t.tall ? z * (TM + 1) + y : y * (TN + 1) + z] = x[r];
         }
-        if constexpr (ST == kStep) {
-          *reinterpret_cast<h4*>(g.uh + mat.off_x + at) = hi;
-          *reinterpret_cast<h4*>(g.ul + mat.off_x + at) = lo;
+      } else if constexpr (ST == kLast) {
+        hi[j] = u2{f32_to_bf16(x[0]) | (f32_to_bf16(x[1]) << 16),
+                   f32_to_bf16(x[2]) | (f32_to_bf16(x[3]) << 16)};
+      } else {
+        union {
+          u2 u;
+          h4 h;
+        } v;
+        v.u = hi[j] = pack4(x);
+        if (ST == kStep || SPLIT) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int64_t x_at = mat.off_x + int64_t(col + r) * np + row;
-            g.xh[x_at] = hi[r];
-            if (SPLIT) g.xl[x_at] = lo[r];
-          }
-        } else {
-          _Float16* dh = (ST == kGram ? g.ah : g.bh) + mat.off_a;
-          _Float16* dl = (ST == kGram ? g.al : g.bl) + mat.off_a;
-          *reinterpret_cast<h4*>(dh + at) = hi;
-          if (SPLIT) *reinterpret_cast<h4*>(dl + at) = lo;
-          if (t.i != t.j) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              dh[int64_t(col + r) * mp + row] = hi[r];
-              if (SPLIT) dl[int64_t(col + r) * mp + row] = lo[r];
-            }
-          }
+          for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(v.h[r]);
+          lo[j] = pack4(x);
         }
+      }
+    }
+    if (i + Ahead < FM) own_rows(i + Ahead);
+    if constexpr (ST == kLast && sizeof(O) == 4) continue;
+    const int r0 = rb + i * 16;
+    if constexpr (ST == kLast) {
+      if (!t.tall)
+        store_rows<FN>(rows16, hi, [&](int r, int c, u4 v) { put(r0 + r, cb + c, t.m, v); });
+    } else {
+      store_rows<FN>(rows16, hi, to(dh, r0, cb, qrows));
+      if constexpr (ST == kStep || SPLIT) store_rows<FN>(rows16, lo, to(dl, r0, cb, qrows));
+    }
+    if (ST != kStep && mirror) keep_transposed<FN>(image, kImageLd, i, hi);
+    if constexpr (SPLIT && kMirror) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {  // for a second image: over the sums
+        acc[i][j][0] = __uint_as_float(lo[j].x);
+        acc[i][j][1] = __uint_as_float(lo[j].y);
+      }
+    }
+  }
+  if constexpr (ST == kLast && sizeof(O) == 4) {
+    const float* f = reinterpret_cast<const float*>(rows16);
+    const int n_rows = t.tall ? TN : TM, width = t.tall ? TM : TN;
+    const int64_t r0 = t.tall ? cb : rb, c0 = t.tall ? rb : cb, last = t.tall ? t.n : t.m;
+    for (int e = lane; e < n_rows * width; e += 64) {
+      const int r = e / width, c = e % width;
+      if (r0 + r < last && c0 + c < cols) out[(r0 + r) * cols + c0 + c] = f[r * (width + 1) + c];
+    }
+  } else if constexpr (ST == kLast) {
+    if (mirror)
+      store_image<TN, TM>(image, [&](int r, int c, u4 v) { put(cb + r, rb + c, t.n, v); });
+  } else if constexpr (kMirror) {
+    if (mirror) {
+      // rows of the image past the plane: tiles of the lower triangle have
+      // their columns inside wherever their rows are
+      store_image<TN, TM>(image, to(dh, cb, rb, prows));
+      if constexpr (SPLIT) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          u2 lo[FN];
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            lo[j] = u2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
+          keep_transposed<FN>(image, kImageLd, i, lo);
+        }
+        store_image<TN, TM>(image, to(dl, cb, rb, prows));
       }
     }
   }
 }
 
-GemmArgs gemm_args(const MuonArgs& a) {
+// `from`: which plane holds X.  Its low parts are replaced in place, by the
+// workgroup that reads them, unless they are an operand too.
+GemmArgs gemm_args(const MuonArgs& a, const MuonGemmTile* tiles, int from) {
   auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
   GemmArgs g{};
-  g.mats = a.mats;
-  g.tiles = a.tiles;
+  g.tiles = tiles;
   g.adiag = reinterpret_cast<float*>(a.ws + a.w.adiag);
   g.bdiag = reinterpret_cast<float*>(a.ws + a.w.bdiag);
-  g.xh = half(a.w.xh);
-  g.xl = half(a.w.xl);
+  g.xh = half(a.w.xh[from]);
+  g.xl = half(a.w.xl[from]);
+  g.yh = half(a.w.xh[1 - from]);
+  g.yl = half(a.w.xl[1 - from]);
   g.ah = half(a.w.ah);
   g.al = half(a.w.al);
   g.bh = half(a.w.bh);
@@ -645,18 +1005,35 @@ GemmArgs gemm_args(const MuonArgs& a) {
   return g;
 }
 
-template <typename A>
-hipError_t launch_one(const void* fn, int64_t blocks, int threads, A& args, const Sink& sink) {
-  void* p[] = {&args};
-  return sink.launch(fn, dim3(static_cast<unsigned>(blocks)), dim3(threads), p, 0);
+using Small = Shape<64, 64, 2, 2, 64, 3, 2>;
+using Mid = Shape<128, 128, 2, 2, 64, 2, 2>;
+using Big = Shape<256, 256, 2, 4, 64, 2, 2>;
+static_assert(Small::BM == kMuonTiles[0] && Mid::BM == kMuonTiles[1] && Big::BM == kMuonTiles[2]);
+
+template <typename S, Stage ST, bool SPLIT, typename O>
+hipError_t launch_shape(GemmArgs& g, int64_t n, const Sink& sink) {
+  void* p[] = {&g};
+  return sink.launch(reinterpret_cast<const void*>(&k_gemm<S, ST, SPLIT, O>),
+                     dim3(static_cast<unsigned>(n)), dim3(S::Threads), p, 0);
 }
 
 template <Stage ST, typename O>
-hipError_t launch_gemm(const MuonArgs& a, GemmArgs& g, const Sink& sink) {
-  const void* fn = a.split
-                       ? reinterpret_cast<const void*>(&k_gemm<128, 128, 2, 2, ST, true, O>)
-                       : reinterpret_cast<const void*>(&k_gemm<128, 128, 2, 2, ST, false, O>);
-  return launch_one(fn, a.n_tiles, 256, g, sink);
+hipError_t launch_gemm(bool split, const MuonTiles& t, GemmArgs& g, const Sink& sink) {
+  if (t.n <= 0) return hipErrorInvalidValue;
+  if constexpr (!(ST == kLast && sizeof(O) == 2)) {
+    if (split)
+      return t.shape == 0 ? launch_shape<Small, ST, true, O>(g, t.n, sink)
+                          : launch_shape<Mid, ST, true, O>(g, t.n, sink);
+  }
+  if constexpr (ST == kLast && sizeof(O) == 4) {
+    return hipErrorInvalidValue;  // fp32 results take split operands
+  } else {
+    switch (t.shape) {
+      case 0: return launch_shape<Small, ST, false, O>(g, t.n, sink);
+      case 1: return launch_shape<Mid, ST, false, O>(g, t.n, sink);
+      default: return launch_shape<Big, ST, false, O>(g, t.n, sink);
+    }
+  }
 }
 
 template <typename G, typename U, int RT, int N>
@@ -718,30 +1095,29 @@ hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* ma
   return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_norm(const MuonArgs& a, const void* update, int dt, const Sink& sink) {
-  if (a.n_tiles <= 0) return hipErrorInvalidValue;
+hipError_t launch_muon_norm(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+                            const void* update, int dt, const Sink& sink) {
+  if (n <= 0) return hipErrorInvalidValue;
   const MuonMat* mats = a.mats;
-  const MuonTile* tiles = a.tiles;
   double* partial = reinterpret_cast<double*>(a.ws + a.w.partial);
   void* p[] = {&mats, &tiles, &update, &partial};
   const void* fn = dt == FSDP_BF16 ? reinterpret_cast<const void*>(&k_norm<u16>)
                                    : reinterpret_cast<const void*>(&k_norm<float>);
-  return sink.launch(fn, dim3(static_cast<unsigned>(a.n_tiles)), dim3(kThreads), p, 0);
+  return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_convert(const MuonArgs& a, const void* update, int dt, double eps,
-                               const double (&poly)[3], const Sink& sink) {
-  if (a.n_tiles <= 0) return hipErrorInvalidValue;
+hipError_t launch_muon_convert(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+                               const void* update, int dt, double eps, const double (&poly)[3],
+                               const Sink& sink) {
+  if (n <= 0) return hipErrorInvalidValue;
   auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
   ConvertArgs c{};
   c.mats = a.mats;
-  c.tiles = a.tiles;
+  c.tiles = tiles;
   c.partial = reinterpret_cast<const double*>(a.ws + a.w.partial);
   c.coef = reinterpret_cast<float*>(a.ws + a.w.coef);
-  c.xh = half(a.w.xh);
-  c.xl = a.split ? half(a.w.xl) : nullptr;
-  c.th = half(a.w.th[0]);
-  c.tl = half(a.w.tl[0]);
+  c.xh = half(a.w.xh[0]);
+  c.xl = a.low ? half(a.w.xl[0]) : nullptr;
   c.eps = eps;
   c.a = poly[0];
   c.b = poly[1];
@@ -749,40 +1125,34 @@ hipError_t launch_muon_convert(const MuonArgs& a, const void* update, int dt, do
   void* p[] = {&update, &c};
   const void* fn = dt == FSDP_BF16 ? reinterpret_cast<const void*>(&k_convert<u16>)
                                    : reinterpret_cast<const void*>(&k_convert<float>);
-  return sink.launch(fn, dim3(static_cast<unsigned>(a.n_tiles)), dim3(kThreads), p, 0);
+  return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_gram(const MuonArgs& a, const Sink& sink) {
-  if (a.n_tiles <= 0) return hipErrorInvalidValue;
-  GemmArgs g = gemm_args(a);
-  return launch_gemm<kGram, float>(a, g, sink);
+hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, int from, const Sink& sink) {
+  GemmArgs g = gemm_args(a, t.tiles, from);
+  return launch_gemm<kGram, u16>(a.split, t, g, sink);
 }
 
-hipError_t launch_muon_poly(const MuonArgs& a, bool first, const double (&poly)[3],
-                            const Sink& sink) {
-  if (a.n_tiles <= 0) return hipErrorInvalidValue;
-  GemmArgs g = gemm_args(a);
+hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
+                            const double (&poly)[3], const Sink& sink) {
+  GemmArgs g = gemm_args(a, t.tiles, 0);
   g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
   g.b = static_cast<float>(poly[1]);
   g.c = static_cast<float>(poly[2]);
-  return launch_gemm<kPoly, float>(a, g, sink);
+  return launch_gemm<kPoly, u16>(a.split, t, g, sink);
 }
 
-hipError_t launch_muon_step(const MuonArgs& a, int from, bool first, bool last,
-                            const double (&poly)[3], void* ortho, int ortho_dt, const Sink& sink) {
-  if (a.n_tiles <= 0) return hipErrorInvalidValue;
-  auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
-  GemmArgs g = gemm_args(a);
+hipError_t launch_muon_step(const MuonArgs& a, const MuonTiles& t, int from, bool first,
+                            bool last, const double (&poly)[3], void* ortho, int ortho_dt,
+                            const Sink& sink) {
+  GemmArgs g = gemm_args(a, t.tiles, from);
   g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
   g.a = static_cast<float>(poly[0]);
-  g.th = half(a.w.th[from]);
-  g.tl = half(a.w.tl[from]);
-  g.uh = half(a.w.th[1 - from]);
-  g.ul = half(a.w.tl[1 - from]);
+  if (first && !a.low) g.xl = nullptr;
   g.ortho = ortho;
-  if (!last) return launch_gemm<kStep, float>(a, g, sink);
-  return ortho_dt == FSDP_BF16 ? launch_gemm<kLast, u16>(a, g, sink)
-                               : launch_gemm<kLast, float>(a, g, sink);
+  if (!last) return launch_gemm<kStep, u16>(a.split, t, g, sink);
+  return ortho_dt == FSDP_BF16 ? launch_gemm<kLast, u16>(a.split, t, g, sink)
+                               : launch_gemm<kLast, float>(a.split, t, g, sink);
 }
 
 }  // namespace fsdp

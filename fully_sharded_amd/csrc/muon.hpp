@@ -21,21 +21,48 @@ namespace fsdp {
 struct MuonMat {
   int64_t flat_off;    // in the unit's buffers [T]
   int64_t rows, cols;  // as the parameter has them
-  int64_t off_x;       // first element in a plane of X (mp x np) or of its transpose
-  int64_t off_a;       // first element in a plane of A or B (mp x mp)
+  int64_t off_x;       // first element in a plane of X (mp rows of ldx)
+  int64_t off_a;       // first element in a plane of A or B (mp rows of lda)
   int64_t off_d;       // first entry of the diagonals of A and B
   int64_t norm_chunk;  // elements per partial sum of the norm
   int32_t norm_first, norm_count;  // its partial sums
   int32_t m, n, mp, np;
+  int32_t ldx, lda;
   int32_t tall;  // rows > cols
   int32_t index;  // of the parameter in the plan
 };
 
 constexpr int kMuonPad = 64;
 
+// Rows of the planes are an odd number of 256-byte blocks apart.  A tile's
+// loads take the same 128 to 512 bytes of many rows, and addresses are
+// spread over the caches' channels by 256 bytes: rows a multiple of 4 KiB
+// apart (sides that are powers of two) all met on one channel.
+inline int64_t muon_pitch(int64_t cols) { return (cols + 127) / 128 * 128 + (((cols + 127) / 128) % 2 ? 0 : 128); }
+
 // A kernel's tile or chunk: which matrix, and where in it.
 struct MuonTile {
   int32_t mat, i, j, unused;
+};
+
+// A product's tile, with all that its workgroup needs: one load at its start
+// instead of a chain of two.
+struct MuonGemmTile {
+  int64_t off_x, off_a, flat_off;
+  int32_t off_d, i, j, mat;
+  int32_t mp, np, m, n;
+  int32_t ldx, lda;
+  int32_t tall, unused;
+};
+
+// Sides of the products' tiles.
+constexpr int kMuonTiles[3] = {64, 128, 256};
+
+// One kind of product's tiles on the device.
+struct MuonTiles {
+  const MuonGemmTile* tiles;
+  int64_t n;
+  int shape;  // index into kMuonTiles
 };
 
 // Work items of the per-element kernels: `len` elements at `dst` (a
@@ -50,8 +77,7 @@ struct MuonDevice {
   const MuonMat* mats;
   const MuonTile* norm;       // chunks of the norm's partial sums
   const MuonTile* convert;    // 64 x 64 tiles of the parameter's own orientation
-  const MuonTile* square;     // lower triangle of A and B
-  const MuonTile* wide;       // tiles of X's transpose
+  MuonTiles gram, poly, step;  // the lower triangles of A and of B, X
   const MuonItem* momentum;   // flat space
   const MuonItem* apply;      // shard space
 };
@@ -60,18 +86,17 @@ struct MuonDevice {
 // split: every operand in two fp16 parts (FSDP_F32 results).
 struct MuonWorkspace {
   int64_t partial, coef, adiag, bdiag;
-  int64_t xh, xl, th[2], tl[2], ah, al, bh, bl;
+  int64_t xh[2], xl[2], ah, al, bh, bl;
   int64_t bytes;
 };
 
 // Everything the launchers of the products need.
 struct MuonArgs {
   const MuonMat* mats;
-  const MuonTile* tiles;
-  int64_t n_tiles;
   char* ws;
   MuonWorkspace w;
   bool split;
+  bool low;  // the update has low parts: fp32, or split operands
 };
 
 }  // namespace fsdp
@@ -80,14 +105,19 @@ struct fsdp_muon {
   int32_t R = 0;
   int64_t T = 0, S = 0;
   std::vector<fsdp::MuonMat> mats;
-  std::vector<fsdp::MuonTile> norm, convert, square, wide;
+  std::vector<fsdp::MuonTile> norm, convert;
+  // the products' tiles for results in bf16, and for split operands
+  struct Tiles {
+    std::vector<fsdp::MuonGemmTile> gram, poly, step;
+    int gram_shape = 0, poly_shape = 0, step_shape = 0;
+  } tiles[2];
   std::vector<fsdp::MuonItem> momentum, apply;
   fsdp::WorkTable rest;  // shard space: all that is not chosen, padding too
   int64_t nx = 0, na = 0, nd = 0, n_partial = 0;  // plane, diagonal and partial-sum sizes
 
   // Device tables on the current device, uploaded on first use
   // (synchronous; freed with the object).
-  fsdp_status device(fsdp::MuonDevice* out) const;
+  fsdp_status device(bool split, fsdp::MuonDevice* out) const;
   ~fsdp_muon();
 
  private:
@@ -117,19 +147,22 @@ hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* ma
                              const void* ortho, int ortho_dt, float* master, void* param,
                              int param_dt, const MuonScalars& sc, bool vec, const Sink& sink);
 
-hipError_t launch_muon_norm(const MuonArgs& a, const void* update, int dt, const Sink& sink);
-// The update into the planes of X and its transpose, scaled by a power of
+hipError_t launch_muon_norm(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+                            const void* update, int dt, const Sink& sink);
+// The update into the planes of X, scaled by a power of
 // two, and the first step's coefficients with what is left of the norm.
-hipError_t launch_muon_convert(const MuonArgs& a, const void* update, int dt, double eps,
-                               const double (&poly)[3], const Sink& sink);
+hipError_t launch_muon_convert(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+                               const void* update, int dt, double eps, const double (&poly)[3],
+                               const Sink& sink);
 // A = X X^T.
-hipError_t launch_muon_gram(const MuonArgs& a, const Sink& sink);
+hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, int from, const Sink& sink);
 // B = b A + c A A.
-hipError_t launch_muon_poly(const MuonArgs& a, bool first, const double (&poly)[3],
+hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
+                            const double (&poly)[3], const Sink& sink);
+// X <- a X + B X, from plane `from` into the other; the last step writes
+// ortho instead.
+hipError_t launch_muon_step(const MuonArgs& a, const MuonTiles& t, int from, bool first,
+                            bool last, const double (&poly)[3], void* ortho, int ortho_dt,
                             const Sink& sink);
-// X <- a X + B X, from transpose buffer `from` into the other; the last
-// step writes ortho instead.
-hipError_t launch_muon_step(const MuonArgs& a, int from, bool first, bool last,
-                            const double (&poly)[3], void* ortho, int ortho_dt, const Sink& sink);
 
 }  // namespace fsdp
