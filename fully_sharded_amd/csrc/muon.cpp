@@ -35,36 +35,47 @@ void emit(int64_t dst, int64_t src, int64_t len, int32_t mat, std::vector<MuonIt
   }
 }
 
-// Workgroups go to the 8 accelerator dies in turn, each with its own L2: a
-// matrix's tiles (in an order that keeps neighbours together) are cut in 8
-// contiguous parts, one for each die, and the parts dealt out in turn.
+// Workgroups go to the 8 accelerator dies in turn, each with its own L2.  A
+// matrix that is a small part of the work goes to one die as a whole, the one
+// with the least so far: its operands are then read into one L2 (72 matrices
+// of hidden 512, their tiles spread over all dies, read 265 MB for A where X
+// has 75, at the fabric's 6 TB/s).  Larger ones are cut in 8 contiguous parts
+// (of an order that keeps neighbours together).  Queues are filled up with
+// empty tiles, so that every die gets its own.
 class Deal {
  public:
-  void add(const std::vector<MuonGemmTile>& tiles) {
+  explicit Deal(int64_t all) : all_(all) {}
+  void add(const std::vector<MuonGemmTile>& tiles, int64_t depth) {
     const int64_t n = static_cast<int64_t>(tiles.size());
+    int order[kXcds];
+    for (int k = 0; k < kXcds; ++k) order[k] = k;
+    std::stable_sort(order, order + kXcds, [&](int a, int b) { return load_[a] < load_[b]; });
+    const int parts = n * depth * kXcds * 3 <= all_ ? 1 : kXcds;
     int64_t at = 0;
-    for (int k = 0; k < kXcds; ++k) {
-      // the longer parts go to the dies that have fewer so far
-      const int64_t take = n / kXcds + (k < n % kXcds ? 1 : 0);
-      auto& q = queue_[(next_ + k) % kXcds];
+    for (int k = 0; k < parts; ++k) {
+      const int64_t take = n / parts + (k < n % parts ? 1 : 0);
+      auto& q = queue_[order[k]];
       q.insert(q.end(), tiles.begin() + at, tiles.begin() + at + take);
+      load_[order[k]] += take * depth;
       at += take;
     }
-    next_ = static_cast<int>((next_ + n) % kXcds);
   }
   std::vector<MuonGemmTile> dealt() const {
     std::vector<MuonGemmTile> out;
+    MuonGemmTile none{};
+    none.mat = -1;
     size_t longest = 0;
     for (const auto& q : queue_) longest = std::max(longest, q.size());
     for (size_t r = 0; r < longest; ++r)
-      for (int x = 0; x < kXcds; ++x)
-        if (r < queue_[x].size()) out.push_back(queue_[x][r]);
+      for (int x = 0; x < kXcds; ++x) out.push_back(r < queue_[x].size() ? queue_[x][r] : none);
+    while (out.back().mat < 0) out.pop_back();
     return out;
   }
 
  private:
   std::vector<MuonGemmTile> queue_[kXcds];
-  int next_ = 0;  // dies before this one have one tile more than the others
+  int64_t load_[kXcds] = {};  // tiles times depth
+  int64_t all_;
 };
 
 // Tiles of a grid of ni x nj, in bands of 8 rows, column by column: any 32
@@ -78,8 +89,9 @@ std::vector<MuonGemmTile> grid(const MuonMat& t, int32_t mat, int64_t ni, int64_
       for (int64_t i = b; i < std::min(ni, b + 8); ++i)
         if (!lower || i >= j)
           out.push_back(MuonGemmTile{t.off_x, t.off_a, t.flat_off, static_cast<int32_t>(t.off_d),
-                                     static_cast<int32_t>(i), static_cast<int32_t>(j), mat, t.mp,
-                                     t.np, t.m, t.n, t.ldx, t.lda, t.tall, 0});
+                                     static_cast<int32_t>(i), static_cast<int32_t>(j),
+                                     mat | (t.tall ? kMuonTall : 0), t.mp,
+                                     t.np, t.m, t.n, t.ldx, t.lda});
   return out;
 }
 
@@ -95,9 +107,13 @@ int64_t count(const std::vector<MuonMat>& mats, int64_t tile, bool square) {
 // The tile of one kind of product (index into kMuonTiles): the largest that
 // still gives every compute unit two.  256 x 256 tiles also need deep sums to
 // pay for their long ends: the step of 72 matrices of hidden 512 (576 such
-// tiles, depth 512) took 126 us with them and 105 with 128 x 128, the step
-// of the hidden-4096 block (depth 4096) 1.64 against 2.1 ms; one block of
-// hidden 512 (192 tiles of 128 x 128) 169 us a pass with those against 157.
+// tiles, depth 512) took 93 us with them and 83 with 128 x 128, a pass over
+// the hidden-4096 block (depth 4096) 13.6 ms and 15.7.  The 32 x 32 tiles,
+// whose four waves share a sum, are for launches that would leave compute
+// units without a tile: one 512 x 512 matrix (36 and 64 tiles of 64 x 64)
+// takes 62 us a pass with them and 90 without; of one block of hidden 512,
+// A (216 tiles, depth up to 2048) gains 6 us a pass, B (216) loses 5 and the
+// step (768) 45.
 int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool split) {
   int64_t tiles = 0, rounds = 0;
   for (const MuonMat& t : mats) {
@@ -105,8 +121,9 @@ int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool spli
     tiles += n;
     rounds += n * (gram ? t.np : t.mp);
   }
-  if (!split && tiles >= 2 * kCus && rounds >= tiles * 1024) return 2;
-  return count(mats, 128, square) >= 2 * kCus ? 1 : 0;
+  if (!split && tiles >= 2 * kCus && rounds >= tiles * 1024) return 3;
+  if (count(mats, 128, square) >= 2 * kCus) return 2;
+  return count(mats, 64, square) <= (gram ? kCus : kCus / 2) ? 0 : 1;
 }
 
 }  // namespace
@@ -149,6 +166,7 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     t.norm_first = static_cast<int32_t>(mu->n_partial);
     t.norm_count = static_cast<int32_t>((numel + t.norm_chunk - 1) / t.norm_chunk);
     mu->n_partial += t.norm_count;
+    if (k >= kMuonTall - 1) return FSDP_ERR_UNSUPPORTED;
     mu->mats.push_back(t);
   }
   // grids first: a table that is refused is not built
@@ -200,29 +218,37 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
 
   for (int32_t k = 0; k < n_params; ++k) {
     const MuonMat& t = mu->mats[k];
-    for (int32_t i = 0; i < t.norm_count; ++i) mu->norm.push_back(MuonTile{k, i, 0, 0});
+    for (int64_t i = 0; i < t.norm_count; ++i)
+      mu->norm.push_back(MuonChunk{t.flat_off + i * t.norm_chunk,
+                                   t.flat_off + std::min((i + 1) * t.norm_chunk, t.rows * t.cols),
+                                   t.norm_first + i, 0});
     const int64_t ri = (t.tall ? t.np : t.mp) / kConvert, cj = (t.tall ? t.mp : t.np) / kConvert;
     for (int64_t i = 0; i < ri; ++i)
       for (int64_t j = 0; j < cj; ++j)
-        mu->convert.push_back(MuonTile{k, static_cast<int32_t>(i), static_cast<int32_t>(j), 0});
+        mu->convert.push_back(MuonConvertTile{
+            t.flat_off, t.off_x, static_cast<int32_t>(t.rows), static_cast<int32_t>(t.cols),
+            t.ldx, static_cast<int32_t>(i), static_cast<int32_t>(j), k, t.norm_first,
+            t.norm_count, t.tall, {}});
   }
   // products: the longest sums first, so that the short ones fill the end
   for (int split = 0; split < 2; ++split) {
     fsdp_muon::Tiles& to = mu->tiles[split];
     auto fill = [&](std::vector<MuonGemmTile>& out, int* shape, bool square, bool gram) {
       *shape = shape_of(mu->mats, square, gram, split != 0);
-      auto depth = [gram](const MuonMat& t) { return gram ? t.np : t.mp; };
+      auto depth = [gram](const MuonMat& t) { return int64_t(gram ? t.np : t.mp); };
       const int64_t side = kMuonTiles[*shape];
       std::vector<int32_t> order(n_params);
       for (int32_t k = 0; k < n_params; ++k) order[k] = k;
       std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
         return depth(mu->mats[a]) > depth(mu->mats[b]);
       });
-      Deal deal;
+      int64_t all = 0;
+      for (const MuonMat& t : mu->mats) all += count({t}, side, square) * depth(t);
+      Deal deal(all);
       for (int32_t k : order) {
         const MuonMat& t = mu->mats[k];
         const int64_t si = (t.mp + side - 1) / side, sj = (t.np + side - 1) / side;
-        deal.add(square ? grid(t, k, si, si, true) : grid(t, k, si, sj, false));
+        deal.add(square ? grid(t, k, si, si, true) : grid(t, k, si, sj, false), depth(t));
       }
       out = deal.dealt();
     };
@@ -248,9 +274,9 @@ MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split) {
   w.bdiag = take(mu->nd * 4);
   w.xh[0] = take(x);
   w.xh[1] = take(x);
-  w.xl[0] = take(x);
-  // the low parts are only read by the workgroup that replaces them, unless
-  // they are an operand too
+  // the low parts, in bf8, are only read by the workgroup that replaces them,
+  // unless they are an operand too, in fp16
+  w.xl[0] = take(split ? x : mu->nx);
   w.xl[1] = split ? take(x) : w.xl[0];
   w.ah = take(a);
   w.bh = take(a);
@@ -319,8 +345,8 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
   }
   const char* b = static_cast<const char*>(it->second);
   out->mats = reinterpret_cast<const fsdp::MuonMat*>(b + at[0]);
-  out->norm = reinterpret_cast<const fsdp::MuonTile*>(b + at[1]);
-  out->convert = reinterpret_cast<const fsdp::MuonTile*>(b + at[2]);
+  out->norm = reinterpret_cast<const fsdp::MuonChunk*>(b + at[1]);
+  out->convert = reinterpret_cast<const fsdp::MuonConvertTile*>(b + at[2]);
   out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[3]);
   out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[4]);
   const Tiles& t = tiles[split ? 1 : 0];
@@ -389,7 +415,6 @@ fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
                           const fsdp_muon_hparams* hp, const void* update, int32_t update_dt,
                           void* ortho, int32_t ortho_dt, char* ws, const fsdp::Sink& sink) {
   fsdp::MuonArgs a{};
-  a.mats = d.mats;
   a.ws = ws;
   a.split = ortho_dt == FSDP_F32;
   a.low = a.split || update_dt == FSDP_F32;

@@ -16,9 +16,10 @@
 // before its rounding to bf16 (1.65e-3), for white, low-rank and steep
 // spectra of 512 x 512 to 1024 x 4096: bf16 operands 0.8-2.4e-2, fp16
 // 1.1-4.7e-3, and fp16 with two things kept finer 0.5-7e-4: the residual a X
-// is read as fp16 high and low parts (its small singular directions would
-// otherwise carry the rounding of the large ones, amplified by a each
-// step), and the diagonals of A and B, their largest part once X is near
+// is read as a high part in fp16 and a low part in bf8 (its small singular
+// directions would otherwise carry the rounding of the large ones, amplified
+// by a each step; a low part in fp16 is no better and one more byte to read
+// and write), and the diagonals of A and B, their largest part once X is near
 // orthogonal, are fp32 vectors d and e beside planes with zeros there:
 //   A A = (A - d)(A - d) + (d_i + d_j) (A - d)_ij + d^2
 //   X'  = (a + e) X + (B - e) X
@@ -259,16 +260,11 @@ __device__ __forceinline__ double block_sum(double x) {
 // Partial sums of squares, in 64 bits: a square of any finite fp32 value is
 // neither infinite nor lost.  One workgroup per chunk.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_norm(const MuonMat* __restrict__ mats,
-                                                   const MuonTile* __restrict__ tiles,
-                                                   const T* __restrict__ update,
+__global__ __launch_bounds__(kThreads) void k_norm(const MuonChunk* __restrict__ chunks,
+                                                   const T* __restrict__ u,
                                                    double* __restrict__ partial) {
-  const MuonTile t = tiles[blockIdx.x];
-  const MuonMat& mat = mats[t.mat];
-  const int64_t lo = int64_t(t.i) * mat.norm_chunk;
-  const int64_t n = mat.rows * mat.cols;
-  const int64_t hi = lo + mat.norm_chunk < n ? lo + mat.norm_chunk : n;
-  const T* u = update + mat.flat_off;
+  const MuonChunk t = chunks[blockIdx.x];
+  const int64_t lo = t.lo, hi = t.hi;
   double s = 0;
   if ((reinterpret_cast<uintptr_t>(u + lo) & (4 * sizeof(T) - 1)) == 0) {
     int64_t e = lo + 4 * threadIdx.x;
@@ -288,15 +284,29 @@ __global__ __launch_bounds__(kThreads) void k_norm(const MuonMat* __restrict__ m
     }
   }
   s = block_sum(s);
-  if (threadIdx.x == 0) partial[mat.norm_first + t.i] = s;
+  if (threadIdx.x == 0) partial[t.to] = s;
+}
+
+// Four values in bf8 (5 bits of exponent, 2 of mantissa), and back.  The low
+// part of a plane's entry is below 2^-11 of it; entries small enough for it
+// to leave bf8's range are below 2^-16 of the largest.
+__device__ __forceinline__ uint32_t pack_bf8(const float (&x)[4]) {
+  int v = __builtin_amdgcn_cvt_pk_bf8_f32(x[0], x[1], 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(x[2], x[3], v, true));
+}
+__device__ __forceinline__ f4 unpack_bf8(uint32_t v) {
+  const auto a = __builtin_amdgcn_cvt_pk_f32_bf8(static_cast<int>(v), false);
+  const auto b = __builtin_amdgcn_cvt_pk_f32_bf8(static_cast<int>(v), true);
+  return f4{a[0], a[1], b[0], b[1]};
 }
 
 struct ConvertArgs {
-  const MuonMat* mats;
-  const MuonTile* tiles;
+  const MuonConvertTile* tiles;
   const double* partial;
   float* coef;  // per matrix: a f, b f^3, c f^5
-  _Float16 *xh, *xl;  // xl null: the low parts are not wanted
+  _Float16* xh;
+  void* xl;    // null: the low parts are not wanted
+  bool bytes;  // they are wanted in bf8
   double eps, a, b, c;
 };
 
@@ -310,8 +320,7 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
                                                       ConvertArgs a) {
   constexpr int Ld = 72;
   __shared__ __align__(16) _Float16 tile[64 * Ld];
-  const MuonTile t = a.tiles[blockIdx.x];
-  const MuonMat& mat = a.mats[t.mat];
+  const MuonConvertTile mat = a.tiles[blockIdx.x], &t = mat;
   const int64_t r0 = int64_t(t.i) * 64, c0 = int64_t(t.j) * 64;
   const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
   const int64_t r = r0 + lr, c = c0 + lc;
@@ -352,12 +361,13 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
 #pragma unroll
   for (int k = 0; k < 16; ++k) x[k] = static_cast<float>(static_cast<double>(x[k]) * scale);
   for (int low = 0; low < (a.xl ? 2 : 1); ++low) {
+    if (low && a.bytes) break;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       part.h[k] = static_cast<_Float16>(x[k]);
       x[k] -= static_cast<float>(part.h[k]);
     }
-    _Float16* out = (low ? a.xl : a.xh) + mat.off_x;
+    _Float16* out = (low ? static_cast<_Float16*>(a.xl) : a.xh) + mat.off_x;
     if (!mat.tall) {
       u4* d = reinterpret_cast<u4*>(out + r * mat.ldx + c);
       d[0] = part.v[0];
@@ -375,16 +385,40 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
       d[1] = part.v[1];
     }
   }
+  if (!a.xl || !a.bytes) return;
+  char* out = static_cast<char*>(a.xl) + mat.off_x;
+  u4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    v[k] = pack_bf8({x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
+  if (!mat.tall) {
+    *reinterpret_cast<u4*>(out + r * mat.ldx + c) = v;
+  } else {
+    char* bytes = reinterpret_cast<char*>(tile);  // rows of 64 and 16 between
+    __syncthreads();
+    *reinterpret_cast<u4*>(bytes + lr * 80 + lc) = v;
+    __syncthreads();
+    union {
+      char b[16];
+      u4 v;
+    } w;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w.b[k] = bytes[(lc + k) * 80 + lr];
+    *reinterpret_cast<u4*>(out + (c0 + lr) * mat.ldx + r0 + lc) = w.v;
+  }
 }
 
 // ---------------------------------------------------------------- products
 struct GemmArgs {
-  const MuonGemmTile* tiles;
   const float* coef;  // non-null: the first step's coefficients, per matrix
   float a, b, c;      // the other steps'
   float *adiag, *bdiag;  // the diagonals of A and B
-  const _Float16 *xh, *xl;  // X of this step (xl null in the first one: zeros)
-  _Float16 *yh, *yl;        // X of the next
+  // X of this step and of the next; the low parts in bf8 or, where they are
+  // operands, in fp16 (xl null in the first step of a bf16 update: zeros)
+  const _Float16* xh;
+  const void* xl;
+  _Float16* yh;
+  void* yl;
   _Float16 *ah, *al, *bh, *bl;
   void* ortho;
 };
@@ -415,11 +449,11 @@ __device__ __forceinline__ int place(int r, int c) {
 // The same for rows across the sum (BN entries): a transposing read takes 32
 // bytes of rows 0-3, 8-11, 16-19 and 24-27 (or 4-7, ...) of 32 at a time, so
 // the pairs of chunks move by bits 0, 1 and 3 of the row; rows of 128 bytes
-// alternate by themselves with bit 0.
+// alternate by themselves with bit 0, rows of 64 bytes with bits 0 and 1.
 template <int BN>
 __device__ __forceinline__ int place_across(int r, int c) {
   const int b = (r & 3) | ((r >> 1) & 4);
-  return c ^ (BN == 64 ? b & 6 : b << 1);
+  return c ^ (BN == 32 ? (b & 4) >> 1 : BN == 64 ? b & 6 : b << 1);
 }
 
 // 16 bytes per lane from global memory to LDS at a wave-uniform address, lane
@@ -438,6 +472,16 @@ __device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
 // counts on from it), then for the other waves.
 __device__ __forceinline__ void wait_lds() {
   __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+}
+// Wait until at most N of this wave's global accesses are under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64);
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
@@ -496,6 +540,21 @@ __device__ __forceinline__ void store_rows(char* lds, const u2 (&v)[FN], F store
   for (int k = 0; k < N; ++k) store(k * Rows + r, c, out[k]);
 }
 
+// The same for rows of bytes, 8 per lane: v[j] has the four of row lane % 16.
+template <int FN, typename F>
+__device__ __forceinline__ void store_byte_rows(char* lds, const uint32_t (&v)[FN], F store) {
+  constexpr int Ld = FN * 16 + 8;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    *reinterpret_cast<uint32_t*>(lds + (lane & 15) * Ld + j * 16 + (lane >> 4) * 4) = v[j];
+  constexpr int PerRow = FN * 2, Rows = 64 / PerRow, N = 16 / Rows;
+  const int r = lane / PerRow, c = lane % PerRow * 8;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    store(k * Rows + r, c, *reinterpret_cast<const u2*>(lds + (k * Rows + r) * Ld + c));
+}
+
 // The same values into a transposed image (columns as rows, ld bytes each).
 template <int FN>
 __device__ __forceinline__ void keep_transposed(char* lds, int ld, int i, const u2 (&v)[FN]) {
@@ -525,172 +584,151 @@ __device__ __forceinline__ void store_image(const char* lds, F store) {
   }
 }
 
-// One tile of a product.  A round's loads go straight to LDS, NS - 1 rounds
-// ahead.  The products of one part of a round (32 of the sum) are issued row
-// by row with the LDS reads of the next part and the loads of a later round
-// between them: issued in one go, those loads keep a wave from its products
-// for a thousand cycles.  Operand rows and columns past the plane's last are
-// read from the last ones; their results are not stored.
-template <typename S, Stage ST, bool SPLIT, typename O>
-__global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0)) void k_gemm(
-    GemmArgs g) {
-  constexpr int FM = S::FM, FN = S::FN, TM = S::TM, TN = S::TN, BK = S::BK, NS = S::NS;
-  constexpr int BM = S::BM, BN = S::BN, RB = S::RB, LP = S::LP, LQ = S::LQ;
-  constexpr bool kAcross = ST == kStep || ST == kLast;  // Q lies across the sum
-  constexpr bool kMirror = ST == kGram || ST == kPoly;
-  // a wave's part of LDS after the sums: 16 rows, and a transposed image
-  // (fp32 results: one of fp32, either way round)
-  constexpr int kRows = 16 * (TN + 8) * 2;
-  constexpr int kImage = ST == kStep ? 0 : TN * (TM + 8) * 2;
-  constexpr int kOut = ST == kLast && sizeof(O) == 4 ? (TM + 1) * (TN + 1) * 4 : kImage + kRows;
-  constexpr int kLds = S::RoundBytes * NS > kOut * S::NW ? S::RoundBytes * NS : kOut * S::NW;
-  __shared__ __align__(128) char lds[kLds];
-
-  const MuonGemmTile t = g.tiles[blockIdx.x];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  const int lr = lane & 15, lk = lane >> 4;
-
-  const int mp = t.mp, np = t.np;
+// The operands of one product: D (rows of P x rows or columns of Q).
+template <Stage ST, bool SPLIT>
+struct Operands {
+  static constexpr bool kAcross = ST == kStep || ST == kLast;  // Q lies across the sum
   const _Float16 *ph, *pl = nullptr, *qh, *ql = nullptr;
   int prows, qrows, depth;
-  int ld, lp, lq;  // of the result and of the operands
-  if constexpr (ST == kGram) {
-    ph = qh = g.xh + t.off_x;
-    if (SPLIT) pl = ql = g.xl + t.off_x;
-    prows = qrows = mp;
-    ld = t.lda;
-    lp = lq = t.ldx;
-    depth = np;
-  } else if constexpr (ST == kPoly) {
-    ph = qh = g.ah + t.off_a;
-    if (SPLIT) pl = ql = g.al + t.off_a;
-    prows = qrows = mp;
-    ld = lp = lq = t.lda;
-    depth = mp;
-  } else {
-    ph = g.bh + t.off_a;
-    qh = g.xh + t.off_x;
-    if (SPLIT) {
-      pl = g.bl + t.off_a;
-      ql = g.xl + t.off_x;
-    }
-    prows = mp;
-    qrows = np;
-    lp = t.lda;
-    ld = lq = t.ldx;
-    depth = mp;
-  }
-  const int i0 = t.i * BM, j0 = t.j * BN;
+  int ld, lp, lq;  // row pitch of the result and of the operands
 
-  // this lane's part of a round's loads, from the round's first element
-  int64_t po[LP], qo[LQ];
-  {
-    constexpr int PerRow = BK / 8;
-    const int r = lane / PerRow, c = place<BK>(r, lane % PerRow);
+  __device__ __forceinline__ Operands(const GemmArgs& g, const MuonGemmTile& t) {
+    if constexpr (ST == kGram) {
+      ph = qh = g.xh + t.off_x;
+      if (SPLIT) pl = ql = static_cast<const _Float16*>(g.xl) + t.off_x;
+      prows = qrows = t.mp;
+      ld = t.lda;
+      lp = lq = t.ldx;
+      depth = t.np;
+    } else if constexpr (ST == kPoly) {
+      ph = qh = g.ah + t.off_a;
+      if (SPLIT) pl = ql = g.al + t.off_a;
+      prows = qrows = t.mp;
+      ld = lp = lq = t.lda;
+      depth = t.mp;
+    } else {
+      ph = g.bh + t.off_a;
+      qh = g.xh + t.off_x;
+      if (SPLIT) {
+        pl = g.bl + t.off_a;
+        ql = static_cast<const _Float16*>(g.xl) + t.off_x;
+      }
+      prows = t.mp;
+      qrows = t.np;
+      lp = t.lda;
+      ld = lq = t.ldx;
+      depth = t.mp;
+    }
+  }
+};
+
+// Where a round begins in P and Q.
+struct From {
+  const _Float16 *p, *q;
+};
+
+// A workgroup's tile in one scalar load (its table's address is preloaded), and
+// the arguments asked for with it:
+// read where each is used they made a chain of round trips to memory, some
+// 10,000 cycles before the first operand was asked for.
+__device__ __forceinline__ MuonGemmTile tile_of(const MuonGemmTile* tiles, const GemmArgs& g) {
+  typedef int i16 __attribute__((ext_vector_type(16)));
+  union {
+    i16 v;
+    MuonGemmTile t;
+  } u;
+  u.v = *reinterpret_cast<const i16*>(tiles + blockIdx.x);
+  asm volatile("" ::"s"(u.v), "s"(g.coef), "s"(g.adiag), "s"(g.bdiag), "s"(g.xh), "s"(g.xl),
+               "s"(g.yh), "s"(g.yl), "s"(g.ah), "s"(g.bh), "s"(g.ortho));
+  return u.t;
+}
+template <int BK, Stage ST, bool SPLIT>
+__device__ __forceinline__ From from_round(const Operands<ST, SPLIT>& o, int it, int rounds) {
+  From f{o.ph, o.qh};
+  int k = it;
+  if constexpr (SPLIT) {  // the small products first: high low, low high, high high
+    const int part = it / rounds;
+    k = it - part * rounds;
+    if (part == 0) f.q = o.ql;
+    if (part == 1) f.p = o.pl;
+  }
+  f.p += int64_t(k) * BK;
+  f.q += Operands<ST, SPLIT>::kAcross ? int64_t(k) * BK * o.lq : int64_t(k) * BK;
+  return f;
+}
+
+// One lane's part of a round's loads, by wave `wave` of S::NW: LP pieces of
+// P, then LQ of Q, each 1024 bytes of the round's image in LDS.  Rows and
+// columns past the plane's last are read from the last ones; their results
+// are not stored.
+template <typename S, bool ACROSS>
+struct Loader {
+  int64_t po[S::LP], qo[S::LQ];
+  int wave;
+
+  __device__ __forceinline__ Loader(int wave_, int i0, int j0, int prows, int qrows, int lp,
+                                    int lq)
+      : wave(wave_) {
+    const int lane = threadIdx.x & 63;
+    constexpr int PerRow = S::BK / 8;
+    const int r = lane / PerRow, c = place<S::BK>(r, lane % PerRow);
 #pragma unroll
-    for (int k = 0; k < LP; ++k) {
-      const int row = i0 + (wave * LP + k) * S::RowsPerLoad + r;
+    for (int k = 0; k < S::LP; ++k) {
+      const int row = i0 + (wave * S::LP + k) * S::RowsPerLoad + r;
       po[k] = int64_t(row < prows ? row : prows - 1) * lp + c * 8;
     }
-    if constexpr (kAcross) {
-      constexpr int Chunks = BN / 8, Rows = 64 / Chunks;
+    if constexpr (ACROSS) {
+      constexpr int Chunks = S::BN / 8, Rows = 64 / Chunks;
 #pragma unroll
-      for (int k = 0; k < LQ; ++k) {
-        const int row = (wave * LQ + k) * Rows + lane / Chunks;
-        const int col = j0 + place_across<BN>(row, lane % Chunks) * 8;
-        qo[k] = int64_t(row) * lq + (col < np ? col : np - 8);
+      for (int k = 0; k < S::LQ; ++k) {
+        const int row = (wave * S::LQ + k) * Rows + lane / Chunks;
+        const int col = j0 + place_across<S::BN>(row, lane % Chunks) * 8;
+        qo[k] = int64_t(row) * lq + (col < qrows ? col : qrows - 8);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < LQ; ++k) {
-        const int row = j0 + (wave * LQ + k) * S::RowsPerLoad + r;
+      for (int k = 0; k < S::LQ; ++k) {
+        const int row = j0 + (wave * S::LQ + k) * S::RowsPerLoad + r;
         qo[k] = int64_t(row < qrows ? row : qrows - 1) * lq + c * 8;
       }
     }
   }
-  const int64_t qstep = kAcross ? int64_t(BK) * lq : BK;
-  const int rounds = depth / BK;
-  const int total = SPLIT ? 3 * rounds : rounds;
-  // where round `it` begins in P and Q
-  struct From {
-    const _Float16 *p, *q;
-  };
-  auto from = [&](int it) {
-    From f{ph, qh};
-    int k = it;
-    if constexpr (SPLIT) {  // the small products first: high low, low high, high high
-      const int part = it / rounds;
-      k = it - part * rounds;
-      if (part == 0) f.q = ql;
-      if (part == 1) f.p = pl;
-    }
-    f.p += int64_t(k) * BK;
-    f.q += k * qstep;
-    return f;
-  };
-  // load x of a round's LP + LQ
-  const uint32_t lds0 = static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-  auto load = [&](const From& f, int buf, int x) {
-    const uint32_t base = lds0 + buf * S::RoundBytes + (x < LP ? 0 : BM * RB);
-    const _Float16* from1 = x < LP ? f.p + po[x < LP ? x : 0] : f.q + qo[x < LP ? 0 : x - LP];
-    const int at = x < LP ? wave * LP + x : wave * LQ + x - LP;
-    load_to_lds(from1, base + at * 1024);
-  };
-
-  f4 acc[FM][FN];
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-
-  // Split operands: the matrix cores' sums go to a second set of
-  // accumulators every 128 of the depth.  One chain over a long positive sum
-  // (A's diagonal) loses 2^-24 of it at every link: 40 x 1025 measured
-  // 4.3e-6 off that way, three times what blocked fp32 sums are.
-  f4 sum[SPLIT ? FM : 1][SPLIT ? FN : 1];
-  auto flush = [&] {
-    if constexpr (SPLIT) {
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          sum[i][j] += acc[i][j];
-          acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-        }
-    }
-  };
-  if constexpr (SPLIT) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) sum[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  // piece x of the round at f into the image at `image`
+  __device__ __forceinline__ void load(const From& f, uint32_t image, int x) const {
+    if (x < S::LP)
+      load_to_lds(f.p + po[x < S::LP ? x : 0], image + (wave * S::LP + x) * 1024);
+    else
+      load_to_lds(f.q + qo[x < S::LP ? 0 : x - S::LP],
+                  image + S::BM * S::RB + (wave * S::LQ + x - S::LP) * 1024);
   }
+};
 
-  // ---- LDS to registers
-  constexpr int KK = BK / 32;
-  h8 p[2][FM], q[2][FN];
-  const int pat = (wm * TM + lr) * RB;
-  int qat[kAcross ? FN : 1];
-  if constexpr (kAcross) {
-    const int row = lk * 8 + (lr >> 2);  // and 4 more for the second half
+// LDS to registers: the 16 x 32 operands of wave (wm, wn).
+template <typename S, bool ACROSS>
+struct Fetcher {
+  int pat, qat[ACROSS ? S::FN : 1];
+
+  __device__ __forceinline__ Fetcher(int wm, int wn) {
+    const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
+    pat = (wm * S::TM + lr) * S::RB;
+    if constexpr (ACROSS) {
+      const int row = lk * 8 + (lr >> 2);  // and 4 more for the second half
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      qat[j] = BM * RB + row * BN * 2 +
-               place_across<BN>(row, wn * (TN / 8) + j * 2 + ((lr & 3) >> 1)) * 16 +
-               (lr & 1) * 8;
-  } else {
-    qat[0] = BM * RB + (wn * TN + lr) * RB;
+      for (int j = 0; j < S::FN; ++j)
+        qat[j] = S::BM * S::RB + row * S::BN * 2 +
+                 place_across<S::BN>(row, wn * (S::TN / 8) + j * 2 + ((lr & 3) >> 1)) * 16 +
+                 (lr & 1) * 8;
+    } else {
+      qat[0] = S::BM * S::RB + (wn * S::TN + lr) * S::RB;
+    }
   }
-  auto fetch_p = [&](int buf, int kk, int set, int i) {
-    p[set][i] = *reinterpret_cast<const h8*>(lds + buf * S::RoundBytes +
-                                             place<BK>(lr, kk * 4 + lk) * 16 + pat +
-                                             i * 16 * RB);
-  };
-  auto fetch_q = [&](int buf, int kk, int set, int j) {
-    if constexpr (kAcross) {
+  __device__ __forceinline__ h8 p(const char* image, int kk, int i) const {
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const h8*>(
+        image + place<S::BK>(lane & 15, kk * 4 + (lane >> 4)) * 16 + pat + i * 16 * S::RB);
+  }
+  __device__ __forceinline__ h8 q(const char* image, int kk, int j) const {
+    if constexpr (ACROSS) {
       typedef short s4 __attribute__((ext_vector_type(4)));
       union {
         s4 s[2];
@@ -699,32 +737,466 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
 #pragma unroll
       for (int half = 0; half < 2; ++half)
         v.s[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s4*)(lds + buf * S::RoundBytes + qat[j] +
-                                                    (kk * 32 + half * 4) * BN * 2));
-      q[set][j] = v.h;
+            (__attribute__((address_space(3))) s4*)(image + qat[j] +
+                                                    (kk * 32 + half * 4) * S::BN * 2));
+      return v.h;
     } else {
-      q[set][j] = *reinterpret_cast<const h8*>(lds + buf * S::RoundBytes +
-                                               place<BK>(lr, kk * 4 + lk) * 16 + qat[0] +
-                                               j * 16 * RB);
+      const int lane = threadIdx.x & 63;
+      return *reinterpret_cast<const h8*>(
+          image + place<S::BK>(lane & 15, kk * 4 + (lane >> 4)) * 16 + qat[0] + j * 16 * S::RB);
     }
-  };
+  }
+};
+
+// A wave's results, FM x FN parts of 16 x 16: acc[i][j][r] is row rb + 16 i +
+// lane % 16 of P, row or column cb + 16 j + 4 (lane / 16) + r of Q.  Planes
+// are padded to multiples of 64: whole parts are inside or outside.  AHEAD:
+// how many sets of 16 rows of what the results are added to (A's or X's own
+// entries) are in registers at once.  Loads and stores are waited for in
+// order: with one set ahead each set waited for the stores of the one before.
+// The sets come in whole rows, 16 bytes per lane, and reach the lanes of the
+// results through LDS: read as the results lie, 8 bytes of each of 16 rows
+// at a time, they took 20,000 of a 128 x 128 tile's 47,000 cycles (depth
+// 512).
+template <int FM, int FN, int AHEAD, Stage ST, bool SPLIT, typename O>
+struct Result {
+  static constexpr int TM = FM * 16, TN = FN * 16;
+  static constexpr bool kAcross = ST == kStep || ST == kLast;
+  static constexpr bool kMirror = ST == kGram || ST == kPoly;
+  // One part of 16 x 16 goes to memory from the registers; more by way of a
+  // wave's part of LDS: 16 rows, and a transposed image (fp32 results: one of
+  // fp32, either way round).
+  static constexpr bool kDirect = FM * FN == 1;
+  static constexpr int kRows = 16 * (TN + 8) * 2;
+  static constexpr int kImage = ST == kStep ? 0 : TN * (TM + 8) * 2;
+  static constexpr int kOut =
+      kRows + (ST == kLast && sizeof(O) == 4 ? ((TM + 1) * (TN + 1) * 4 + 15) / 16 * 16 : kImage);
+
+  static constexpr bool kOwnLow = kAcross || SPLIT;
+  static constexpr bool kBytes = kAcross && !SPLIT;  // low parts in bf8
+  static constexpr int kOwnLd = (TN + 8) * 2;  // of 16 rows in LDS
+  static constexpr int kPerRow = TN / 8, kStepRows = kDirect ? 16 : 64 / kPerRow;
+  static constexpr int kSets = kDirect ? 1 : 16 / kStepRows;
+  static_assert(64 % TN == 0);
+
+  int rb, cb, lr, lk;
+  u4 own_h[AHEAD][kSets], own_l[AHEAD][kSets];  // kDirect: in the first two words
+  float ca, cb1, cc, di[FM];
+  f4 dj[FN];
+
+  __device__ __forceinline__ void own_rows(const GemmArgs& g, const MuonGemmTile& t,
+                                           const Operands<ST, SPLIT>& o, int i) {
+    const _Float16* oh = ST == kPoly ? o.ph : o.qh;
+    const char* ol = ST == kPoly ? reinterpret_cast<const char*>(o.pl)
+                                 : static_cast<const char*>(g.xl);
+    if (ST != kPoly && ol) ol += t.off_x * (kBytes ? 1 : 2);
+    if constexpr (ST != kGram) {
+      const int lane = threadIdx.x & 63;
+      const int64_t at =
+          kDirect ? int64_t(rb + lr) * o.ld + cb + lk * 4
+                  : int64_t(rb + i * 16 + lane / kPerRow) * o.ld + cb + lane % kPerRow * 8;
+      const bool in = rb + i * 16 < o.prows && cb < o.qrows;  // uniform: TN divides 64
+#pragma unroll
+      for (int k = 0; k < kSets; ++k) {
+        u4 &h = own_h[i % AHEAD][k], &l = own_l[i % AHEAD][k];
+        h = l = u4{0, 0, 0, 0};
+        if (in) {
+          const int64_t e = at + int64_t(k) * kStepRows * o.ld;
+          if constexpr (kDirect) {
+            const u2 v = *reinterpret_cast<const u2*>(oh + e);
+            h.x = v.x;
+            h.y = v.y;
+            if (kOwnLow && ol) {
+              if constexpr (kBytes) {
+                l.x = *reinterpret_cast<const uint32_t*>(ol + e);
+              } else {
+                const u2 w = *reinterpret_cast<const u2*>(ol + e * 2);
+                l.x = w.x;
+                l.y = w.y;
+              }
+            }
+          } else {
+            h = *reinterpret_cast<const u4*>(oh + e);
+            if (kOwnLow && ol) {
+              if constexpr (kBytes) {
+                const u2 w = *reinterpret_cast<const u2*>(ol + e);
+                l.x = w.x;
+                l.y = w.y;
+              } else {
+                l = *reinterpret_cast<const u4*>(ol + e * 2);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // One plane of set i, as the results lie.
+  __device__ __forceinline__ void spread(char* rows16, const u4 (&from)[kSets],
+                                         h4 (&to)[FN]) const {
+    union {
+      u2 u;
+      h4 h;
+    } v;
+    if constexpr (kDirect) {
+      v.u = u2{from[0].x, from[0].y};
+      to[0] = v.h;
+    } else {
+      const int lane = threadIdx.x & 63;
+#pragma unroll
+      for (int k = 0; k < kSets; ++k)
+        *reinterpret_cast<u4*>(rows16 + (k * kStepRows + lane / kPerRow) * kOwnLd +
+                               lane % kPerRow * 16) = from[k];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        to[j] = *reinterpret_cast<const h4*>(rows16 + lr * kOwnLd + (j * 16 + lk * 4) * 2);
+    }
+  }
+
+  // The low parts of set i, likewise.
+  __device__ __forceinline__ void spread_low(char* rows16, const u4 (&from)[kSets],
+                                             f4 (&to)[FN]) const {
+    if constexpr (kBytes) {
+      if constexpr (kDirect) {
+        to[0] = unpack_bf8(from[0].x);
+      } else {
+        constexpr int Ld = TN + 8;
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int k = 0; k < kSets; ++k)
+          *reinterpret_cast<u2*>(rows16 + (k * kStepRows + lane / kPerRow) * Ld +
+                                 lane % kPerRow * 8) = u2{from[k].x, from[k].y};
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          to[j] = unpack_bf8(
+              *reinterpret_cast<const uint32_t*>(rows16 + lr * Ld + j * 16 + lk * 4));
+      }
+    } else {
+      h4 l[FN];
+      spread(rows16, from, l);
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[j][r] = static_cast<float>(l[j][r]);
+    }
+  }
+
+  // Ask for everything that is not a sum.
+  __device__ __forceinline__ void ask(const GemmArgs& g, const MuonGemmTile& t,
+                                      const Operands<ST, SPLIT>& o, int rb_, int cb_) {
+    const int lane = threadIdx.x & 63;
+    lr = lane & 15;
+    lk = lane >> 4;
+    rb = rb_;
+    cb = cb_;
+    ca = g.a;
+    cb1 = g.b;
+    cc = g.c;
+    if (g.coef) {
+      const int mat = t.mat & ~kMuonTall;
+      ca = g.coef[4 * mat];
+      cb1 = g.coef[4 * mat + 1];
+      cc = g.coef[4 * mat + 2];
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      dj[j] = f4{0.f, 0.f, 0.f, 0.f};
+      if (ST == kPoly && cb + j * 16 < o.qrows)
+        dj[j] = *reinterpret_cast<const f4*>(g.adiag + t.off_d + cb + j * 16 + lk * 4);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      di[i] = 0.f;
+      if (ST != kGram && rb + i * 16 < o.prows)
+        di[i] = (ST == kPoly ? g.adiag : g.bdiag)[t.off_d + rb + i * 16 + lr];
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) own_rows(g, t, o, i);
+  }
+
+  // Four results of a lane, columns col to col + 3 of a row.
+  __device__ __forceinline__ void direct(const GemmArgs& g, const MuonGemmTile& t,
+                                         const Operands<ST, SPLIT>& o, int row, int col,
+                                         float (&x)[4]) const {
+    if constexpr (ST == kLast) {
+      O* out = static_cast<O*>(g.ortho) + t.flat_off;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (row < t.m && col + r < t.n)
+          El<O>::store(out + (t.mat & kMuonTall ? int64_t(col + r) * t.m + row : int64_t(row) * t.n + col + r),
+                       x[r]);
+    } else {
+      _Float16* d[2] = {ST == kStep ? g.yh + t.off_x : (ST == kGram ? g.ah : g.bh) + t.off_a,
+                        ST == kStep ? static_cast<_Float16*>(g.yl) + t.off_x
+                               : (ST == kGram ? g.al : g.bl) + t.off_a};
+      const int lane = threadIdx.x & 63;
+      const uint32_t sel = lane & 1 ? 0x03020706u : 0x05040100u;
+#pragma unroll
+      for (int low = 0; low < (ST == kStep || SPLIT ? 2 : 1); ++low) {
+        union {
+          u2 u;
+          h4 h;
+        } v;
+        v.u = pack4(x);
+        if (kBytes && low) {
+          *reinterpret_cast<uint32_t*>(static_cast<char*>(g.yl) + t.off_x +
+                                       int64_t(row) * o.ld + col) = pack_bf8(x);
+          continue;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(v.h[r]);
+        *reinterpret_cast<u2*>(d[low] + int64_t(row) * o.ld + col) = v.u;
+        if (kMirror && t.i != t.j)
+          *reinterpret_cast<u2*>(d[low] + int64_t(col + (lr & 3)) * o.ld + row - (lr & 3)) =
+              transpose4(v.u, sel, lane & 2);
+      }
+    }
+  }
+
+  // The results to where they belong, through `lds` (kOut bytes of the
+  // wave's own).  acc is used up.
+  __device__ __forceinline__ void finish(const GemmArgs& g, const MuonGemmTile& t,
+                                         const Operands<ST, SPLIT>& o, f4 (&acc)[FM][FN],
+                                         char* lds) {
+    if (rb >= o.prows || cb >= o.qrows) return;
+    const int lane = threadIdx.x & 63;
+    char* rows16 = lds;
+    char* image = rows16 + kRows;
+    constexpr int kImageLd = (TM + 8) * 2;
+    const bool mirror = ST == kLast ? (t.mat & kMuonTall) != 0 : t.i != t.j;
+    O* out = static_cast<O*>(g.ortho) + t.flat_off;  // kLast
+    const bool tall = t.mat & kMuonTall;
+    const int64_t cols = tall ? t.m : t.n;
+    // 16 bytes of the result where the rows' and the base's alignment allow it
+    const bool vec = ((reinterpret_cast<uintptr_t>(out) | (cols * 2)) & 15) == 0;
+    auto put = [&](int64_t r, int64_t c, int64_t n_rows, u4 v) {
+      if (r >= n_rows || c >= cols) return;
+      u16* d = reinterpret_cast<u16*>(out) + r * cols + c;
+      if (vec && c + 8 <= cols) {
+        *reinterpret_cast<u4*>(d) = v;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c + k < cols) d[k] = static_cast<u16>(v[k / 2] >> (16 * (k & 1)));
+      }
+    };
+    // eight adjacent entries of a plane; it is padded to multiples of 64
+    const int ld = o.ld;
+    auto to = [&](_Float16* plane, int64_t first, int64_t second, int n_cols) {
+      return [=](int r, int c, u4 v) {
+        if (second + c < n_cols)
+          *reinterpret_cast<u4*>(plane + (first + r) * ld + second + c) = v;
+      };
+    };
+    _Float16* dh = ST == kStep ? g.yh + t.off_x : (ST == kGram ? g.ah : g.bh) + t.off_a;
+    _Float16* dl = ST == kStep ? static_cast<_Float16*>(g.yl) + t.off_x
+                               : (ST == kGram ? g.al : g.bl) + t.off_a;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (rb + i * 16 >= o.prows) break;
+      const int row = rb + i * 16 + lr;
+      u2 hi[FN], lo[FN];
+      uint32_t low8[FN];
+      h4 h[FN];
+      f4 l[FN];
+      if constexpr (ST != kGram) spread(rows16, own_h[i % AHEAD], h);
+      if constexpr (ST != kGram && kOwnLow) spread_low(rows16, own_l[i % AHEAD], l);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int col = cb + j * 16 + lk * 4;
+        float x[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float sum = acc[i][j][r];
+          float own = 0.f;
+          if constexpr (ST != kGram) own = static_cast<float>(h[j][r]);
+          if constexpr (ST != kGram && kOwnLow) own += l[j][r];
+          if constexpr (ST == kGram) {
+            x[r] = sum * (kSa / (kSx * kSx));
+          } else if constexpr (ST == kPoly) {
+            x[r] = fmaf(fmaf(cc, di[i] + dj[j][r], cb1), own, cc * (sum * (1.f / kSa)));
+          } else {
+            x[r] = fmaf(ca + di[i], own, sum * (1.f / kSa));
+            if (ST == kLast) x[r] *= 1.f / kSx;
+          }
+          if (kMirror && row == col + r) {
+            if (ST == kGram)
+              g.adiag[t.off_d + row] = x[r] * (1.f / kSa);
+            else
+              g.bdiag[t.off_d + row] = fmaf(di[i], fmaf(cc, di[i], cb1), x[r] * (1.f / kSa));
+            x[r] = 0.f;
+          }
+        }
+        if constexpr (kDirect) {
+          direct(g, t, o, row, col, x);
+        } else if constexpr (ST == kLast && sizeof(O) == 4) {
+          // in the parameter's orientation, one element at a time
+          float* f = reinterpret_cast<float*>(image);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int y = i * 16 + lr, z = j * 16 + lk * 4 + r;
+            f[tall ? z * (TM + 1) + y : y * (TN + 1) + z] = x[r];
+          }
+        } else if constexpr (ST == kLast) {
+          hi[j] = u2{f32_to_bf16(x[0]) | (f32_to_bf16(x[1]) << 16),
+                     f32_to_bf16(x[2]) | (f32_to_bf16(x[3]) << 16)};
+        } else {
+          union {
+            u2 u;
+            h4 h;
+          } v;
+          v.u = hi[j] = pack4(x);
+          if (ST == kStep || SPLIT) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(v.h[r]);
+            if (kBytes)
+              low8[j] = pack_bf8(x);
+            else
+              lo[j] = pack4(x);
+          }
+        }
+      }
+      if (i + AHEAD < FM) own_rows(g, t, o, i + AHEAD);
+      if constexpr (!kDirect && !(ST == kLast && sizeof(O) == 4)) {
+        const int r0 = rb + i * 16;
+        if constexpr (ST == kLast) {
+          if (!tall)
+            store_rows<FN>(rows16, hi, [&](int r, int c, u4 v) { put(r0 + r, cb + c, t.m, v); });
+        } else {
+          store_rows<FN>(rows16, hi, to(dh, r0, cb, o.qrows));
+          if constexpr (kBytes) {
+            char* plane = static_cast<char*>(g.yl) + t.off_x;
+            store_byte_rows<FN>(rows16, low8, [&](int r, int c, u2 v) {
+              *reinterpret_cast<u2*>(plane + int64_t(r0 + r) * ld + cb + c) = v;
+            });
+          } else if constexpr (ST == kStep || SPLIT) {
+            store_rows<FN>(rows16, lo, to(dl, r0, cb, o.qrows));
+          }
+        }
+        if (ST != kStep && mirror) keep_transposed<FN>(image, kImageLd, i, hi);
+        if constexpr (SPLIT && kMirror) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {  // for a second image: over the sums
+            acc[i][j][0] = __uint_as_float(lo[j].x);
+            acc[i][j][1] = __uint_as_float(lo[j].y);
+          }
+        }
+      }
+    }
+    if constexpr (kDirect) {
+      return;
+    } else if constexpr (ST == kLast && sizeof(O) == 4) {
+      const float* f = reinterpret_cast<const float*>(image);
+      const int n_rows = tall ? TN : TM, width = tall ? TM : TN;
+      const int64_t r0 = tall ? cb : rb, c0 = tall ? rb : cb, last = tall ? t.n : t.m;
+      for (int e = lane; e < n_rows * width; e += 64) {
+        const int r = e / width, c = e % width;
+        if (r0 + r < last && c0 + c < cols)
+          out[(r0 + r) * cols + c0 + c] = f[r * (width + 1) + c];
+      }
+    } else if constexpr (ST == kLast) {
+      if (mirror)
+        store_image<TN, TM>(image, [&](int r, int c, u4 v) { put(cb + r, rb + c, t.n, v); });
+    } else if constexpr (kMirror) {
+      if (mirror) {
+        // the image's rows are inside the plane: a tile below the diagonal
+        // has its columns before its rows
+        store_image<TN, TM>(image, to(dh, cb, rb, o.prows));
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int i = 0; i < FM; ++i) {
+            u2 lo[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+              lo[j] = u2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
+            keep_transposed<FN>(image, kImageLd, i, lo);
+          }
+          store_image<TN, TM>(image, to(dl, cb, rb, o.prows));
+        }
+      }
+    }
+  }
+};
+
+// Split operands: the matrix cores' sums go to a second set of accumulators
+// every 128 of the depth.  One chain over a long positive sum (A's diagonal)
+// loses 2^-24 of it at every link: 40 x 1025 measured 4.3e-6 off that way,
+// three times what blocked fp32 sums are.
+template <int FM, int FN>
+__device__ __forceinline__ void zero(f4 (&x)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) x[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+}
+template <int FM, int FN>
+__device__ __forceinline__ void flush(f4 (&sum)[FM][FN], f4 (&acc)[FM][FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sum[i][j] += acc[i][j];
+  zero(acc);
+}
+
+// One tile of a product, all waves on the same rounds.  A round's loads go
+// straight to LDS, NS - 1 rounds ahead.  The products of one part of a round
+// (32 of the sum) are issued row by row with the LDS reads of the next part
+// and the loads of a later round between them: issued in one go, those loads
+// keep a wave from its products for a thousand cycles.
+template <typename S, Stage ST, bool SPLIT, typename O>
+__global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0)) void k_gemm(
+    const MuonGemmTile* __restrict__ tiles, GemmArgs g) {
+  constexpr int FM = S::FM, FN = S::FN, TM = S::TM, TN = S::TN, BK = S::BK, NS = S::NS;
+  constexpr int LP = S::LP, LQ = S::LQ;
+  constexpr bool kAcross = ST == kStep || ST == kLast;
+  // what the results are added to is asked for before the sums, or, where
+  // there is no room in registers, after them
+  constexpr bool kEarly = S::BM <= 128;
+  using Res = Result<FM, FN, kEarly ? FM : FM / 2, ST, SPLIT, O>;
+  constexpr int kLds =
+      S::RoundBytes * NS > Res::kOut * S::NW ? S::RoundBytes * NS : Res::kOut * S::NW;
+  __shared__ __align__(128) char lds[kLds];
+
+  const MuonGemmTile t = tile_of(tiles, g);
+  if (t.mat < 0) return;  // filled up
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const Operands<ST, SPLIT> o(g, t);
+  const int i0 = t.i * S::BM, j0 = t.j * S::BN;
+  const Loader<S, kAcross> loader(wave, i0, j0, o.prows, o.qrows, o.lp, o.lq);
+  const Fetcher<S, kAcross> fetcher(wm, wn);
+  const int rounds = o.depth / BK;
+  const int total = SPLIT ? 3 * rounds : rounds;
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+
+  f4 acc[FM][FN], sum[SPLIT ? FM : 1][SPLIT ? FN : 1];
+  zero(acc);
+  zero(sum);
+  Res res;
+
+  constexpr int KK = BK / 32;
+  h8 p[2][FM], q[2][FN];
   // The products of operand set `set`, with the next operands (other set)
   // read from `buf`, part kk, and with LOADS the loads of round f into
   // buffer `into` between their rows.
   auto products = [&](int set, int buf, int kk, auto loads, const From& f, int into) {
     constexpr int kFetch = FM + FN, kLoad = LP + LQ;
+    const char* image = lds + buf * S::RoundBytes;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
       for (int x = i * kFetch / FM; x < (i + 1) * kFetch / FM; ++x) {
         if (x < FN)
-          fetch_q(buf, kk, set ^ 1, x);
+          q[set ^ 1][x] = fetcher.q(image, kk, x);
         else
-          fetch_p(buf, kk, set ^ 1, x - FN);
+          p[set ^ 1][x - FN] = fetcher.p(image, kk, x - FN);
       }
       if constexpr (decltype(loads)::value) {
 #pragma unroll
-        for (int x = i * kLoad / FM; x < (i + 1) * kLoad / FM; ++x) load(f, into, x);
+        for (int x = i * kLoad / FM; x < (i + 1) * kLoad / FM; ++x)
+          loader.load(f, lds0 + into * S::RoundBytes, x);
       }
 #pragma unroll
       for (int j = 0; j < FN; ++j)
@@ -734,270 +1206,163 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
     }
   };
 
-  // What the results are added to: A's or X's own entries, 16 rows at a time,
-  // Ahead sets of them in registers: all, asked for before the sums begin, or
-  // as many as fit after them.  Loads and stores are waited for in order, so
-  // with one set ahead each set waited for the stores of the one before.
-  const int rb = i0 + wm * TM, cb = j0 + wn * TN;
-  constexpr bool kEarly = S::BM <= 128;
-  constexpr int Ahead = kEarly ? FM : FM / 2;
-  const _Float16* oh = ST == kPoly ? ph : qh;
-  const _Float16* ol = ST == kPoly ? pl : (g.xl ? g.xl + t.off_x : nullptr);
-  h4 h[Ahead][FN], l[Ahead][FN];
-  auto own_rows = [&](int i) {
-    const int64_t at = int64_t(rb + i * 16 + lr) * ld + cb + lk * 4;
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      h[i % Ahead][j] = l[i % Ahead][j] = h4{0, 0, 0, 0};
-      if (ST != kGram && rb + i * 16 < prows && cb + j * 16 < qrows) {
-        h[i % Ahead][j] = *reinterpret_cast<const h4*>(oh + at + j * 16);
-        if ((kAcross || SPLIT) && ol)
-          l[i % Ahead][j] = *reinterpret_cast<const h4*>(ol + at + j * 16);
-      }
-    }
-  };
-  float ca = g.a, cb1 = g.b, cc = g.c, di[FM];
-  f4 dj[FN];
-  auto others = [&] {
-    if (g.coef) {
-      ca = g.coef[4 * t.mat];
-      cb1 = g.coef[4 * t.mat + 1];
-      cc = g.coef[4 * t.mat + 2];
-    }
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      dj[j] = f4{0.f, 0.f, 0.f, 0.f};
-      if (ST == kPoly && cb + j * 16 < qrows)
-        dj[j] = *reinterpret_cast<const f4*>(g.adiag + t.off_d + cb + j * 16 + lk * 4);
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      di[i] = 0.f;
-      if (ST != kGram && rb + i * 16 < prows)
-        di[i] = (ST == kPoly ? g.adiag : g.bdiag)[t.off_d + rb + i * 16 + lr];
-    }
-#pragma unroll
-    for (int i = 0; i < Ahead; ++i) own_rows(i);
-  };
-  if constexpr (kEarly) others();
-
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     if (s < total) {
-      const From f = from(s);
+      const From f = from_round<BK>(o, s, rounds);
 #pragma unroll
-      for (int x = 0; x < LP + LQ; ++x) load(f, s, x);
+      for (int x = 0; x < LP + LQ; ++x) loader.load(f, lds0 + s * S::RoundBytes, x);
     }
+  if constexpr (kEarly) res.ask(g, t, o, i0 + wm * TM, j0 + wn * TN);
   if (total >= NS)
     wait_and_meet<(NS - 1) * (LP + LQ)>();
   else
     wait_and_meet<0>();
 #pragma unroll
-  for (int j = 0; j < FN; ++j) fetch_q(0, 0, 0, j);
+  for (int j = 0; j < FN; ++j) q[0][j] = fetcher.q(lds, 0, j);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) fetch_p(0, 0, 0, i);
+  for (int i = 0; i < FM; ++i) p[0][i] = fetcher.p(lds, 0, i);
   // Before a round's last part: the next round has landed for every wave, and
   // every wave is done reading this one, whose buffer is loaded again.  The
   // last round reads operands that nothing uses: with a tail of its own the
   // accumulators were copied around in every round.
   int buf = 0;
-  // round `it`, its last part's operands in set `set`
-  auto one = [&](int it, auto set, auto loads) {
+  auto one = [&](int it, auto loads) {
     const int next = buf + 1 == NS ? 0 : buf + 1;
     constexpr int kWait = decltype(loads)::value ? (NS - 2) * (LP + LQ) : 0;
     From f{};
-    if constexpr (KK == 2) {
-      wait_lds();  // set 0: asked for half a round ago
-      products(0, buf, 1, std::false_type{}, f, 0);
-    }
+    static_assert(KK == 2);
+    wait_lds();  // set 0: asked for half a round ago
+    products(0, buf, 1, std::false_type{}, f, 0);
     wait_and_meet<kWait>();
-    if (decltype(loads)::value) f = from(it + NS);
-    products(set, next, 0, loads, f, buf);
+    if (decltype(loads)::value) f = from_round<BK>(o, it + NS, rounds);
+    products(1, next, 0, loads, f, buf);
+    if constexpr (SPLIT) {
+      if (it & 1) flush(sum, acc);
+    }
     buf = next;
   };
   int it = 0;
-  if constexpr (KK == 2) {
-    for (; it + NS < total; ++it) {
-      one(it, 1, std::true_type{});
-      if (SPLIT && (it & 1)) flush();
-    }
-    for (; it < total; ++it) {
-      one(it, 1, std::false_type{});
-      if (SPLIT && (it & 1)) flush();
-    }
-  } else {
-    // total is even: the depth is a multiple of 64
-    auto two = [&](auto first, auto second) {
-      one(it, 0, first);
-      one(it + 1, 1, second);
-      if (SPLIT && (it & 2)) flush();
-    };
-    for (; it + 1 + NS < total; it += 2) two(std::true_type{}, std::true_type{});
-    if (it + NS < total) {
-      two(std::true_type{}, std::false_type{});
-      it += 2;
-    }
-    for (; it < total; it += 2) two(std::false_type{}, std::false_type{});
-  }
+  for (; it + NS < total; ++it) one(it, std::true_type{});
+  for (; it < total; ++it) one(it, std::false_type{});
   if constexpr (SPLIT) {
-    flush();
+    flush(sum, acc);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = sum[i][j];
   }
 
-  // ---- the results: acc[i][j][r] is row rb + 16 i + lane % 16 of P, row or
-  // column cb + 16 j + 4 (lane / 16) + r of Q.  Planes are padded to
-  // multiples of 64: whole 16 x 16 parts are inside or outside.
-  char* rows16 = lds + wave * kOut;
-  char* image = rows16 + kRows;
-  constexpr int kImageLd = (TM + 8) * 2;
-  const bool mirror = ST == kLast ? t.tall : t.i != t.j;
-  O* out = static_cast<O*>(g.ortho) + t.flat_off;  // kLast
-  const int64_t cols = t.tall ? t.m : t.n;
-  // 16 bytes of the result where the rows' and the base's alignment allow it
-  const bool vec = ((reinterpret_cast<uintptr_t>(out) | (cols * 2)) & 15) == 0;
-  auto put = [&](int64_t r, int64_t c, int64_t n_rows, u4 v) {
-    if (r >= n_rows || c >= cols) return;
-    u16* d = reinterpret_cast<u16*>(out) + r * cols + c;
-    if (vec && c + 8 <= cols) {
-      *reinterpret_cast<u4*>(d) = v;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (c + k < cols) d[k] = static_cast<u16>(v[k / 2] >> (16 * (k & 1)));
-    }
-  };
-  // eight adjacent entries of a plane; it is padded to multiples of 64
-  auto to = [&](_Float16* plane, int64_t first, int64_t second, int n_cols) {
-    return [=](int r, int c, u4 v) {
-      if (second + c < n_cols)
-        *reinterpret_cast<u4*>(plane + (first + r) * ld + second + c) = v;
-    };
-  };
-  _Float16* dh = ST == kStep ? g.yh + t.off_x : (ST == kGram ? g.ah : g.bh) + t.off_a;
-  _Float16* dl = ST == kStep ? g.yl + t.off_x : (ST == kGram ? g.al : g.bl) + t.off_a;
-
-  if constexpr (!kEarly) others();
+  if constexpr (!kEarly) res.ask(g, t, o, i0 + wm * TM, j0 + wn * TN);
   __syncthreads();  // every wave is done with the operands in LDS
-  if (rb >= prows || cb >= qrows) return;
+  res.finish(g, t, o, acc, lds + wave * Res::kOut);
+}
+
+// A 32 x 32 tile with the sum dealt over 4 waves: wave w takes rounds w, w +
+// 4, ... with loads, LDS and accumulators of its own, so nothing is waited
+// for but its own loads until the four are added up, each wave one 16 x 16
+// part.  For few tiles: a compute unit takes in 46 bytes a cycle, so with 64
+// x 64 tiles the operands of a sum of 512 alone are 2,800 cycles (1.3 us of
+// a launch's 6), and most compute units have no tile.
+template <typename S, Stage ST, bool SPLIT, typename O>
+__global__ __launch_bounds__(256, S::Waves) void k_thin(
+    const MuonGemmTile* __restrict__ tiles, GemmArgs g) {
+  constexpr int BK = S::BK, NS = S::NS, kLoads = S::LP + S::LQ, KK = BK / 32;
+  constexpr int FM = S::FM, FN = S::FN;
+  static_assert(S::NW == 1 && FM * FN == 4);
+  constexpr bool kAcross = ST == kStep || ST == kLast;
+  constexpr int kOwn = S::RoundBytes * NS;
+  static_assert(kOwn >= FM * FN * 1024);
+  __shared__ __align__(128) char lds[4 * kOwn];
+
+  const MuonGemmTile t = tile_of(tiles, g);
+  if (t.mat < 0) return;  // filled up
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Operands<ST, SPLIT> o(g, t);
+  const int i0 = t.i * S::BM, j0 = t.j * S::BN;
+  const int rounds = o.depth / BK;
+  const int total = SPLIT ? 3 * rounds : rounds;
+  const int mine = (total - wave + 3) / 4;  // total > 0; none for wave >= total
+  char* own = lds + wave * kOwn;
+  const uint32_t own0 =
+      static_cast<uint32_t>(
+          reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds)) +
+      wave * kOwn;
+  Result<1, 1, 1, ST, SPLIT, O> res;
+  const Loader<S, kAcross> loader(0, i0, j0, o.prows, o.qrows, o.lp, o.lq);
+  const Fetcher<S, kAcross> fetcher(0, 0);
+  auto issue = [&](int r, int buf) {
+    const From f = from_round<BK>(o, wave + 4 * r, rounds);
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    if (rb + i * 16 >= prows) break;
-    const int row = rb + i * 16 + lr;
-    u2 hi[FN], lo[FN];
+    for (int x = 0; x < kLoads; ++x) loader.load(f, own0 + buf * S::RoundBytes, x);
+  };
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (s < mine) issue(s, s);
+  res.ask(g, t, o, i0 + wave / FN * 16, j0 + wave % FN * 16);
+
+  f4 acc[FM][FN], sum[SPLIT ? FM : 1][SPLIT ? FN : 1];
+  zero(acc);
+  zero(sum);
+  int buf = 0;
+  for (int r = 0; r < mine; ++r) {
+    if (r + NS <= mine)
+      wait_loads<(NS - 1) * kLoads>();
+    else
+      wait_loads<0>();
+    h8 p[KK][FM], q[KK][FN];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) q[kk][j] = fetcher.q(own + buf * S::RoundBytes, kk, j);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) p[kk][i] = fetcher.p(own + buf * S::RoundBytes, kk, i);
+    }
+    if (r + NS < mine) {
+      wait_lds();  // the buffer is read: load it again
+      asm volatile("" ::: "memory");
+      issue(r + NS, buf);
+    }
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] =
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(q[kk][j], p[kk][i], acc[i][j], 0, 0, 0);
+    if constexpr (SPLIT) flush(sum, acc);
+    buf = buf + 1 == NS ? 0 : buf + 1;
+  }
+  // the four waves' sums, in their order
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      const int col = cb + j * 16 + lk * 4;
-      float x[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float sum1 = acc[i][j][r];
-        const float own =
-            static_cast<float>(h[i % Ahead][j][r]) + static_cast<float>(l[i % Ahead][j][r]);
-        if constexpr (ST == kGram) {
-          x[r] = sum1 * (kSa / (kSx * kSx));
-        } else if constexpr (ST == kPoly) {
-          x[r] = fmaf(fmaf(cc, di[i] + dj[j][r], cb1), own, cc * (sum1 * (1.f / kSa)));
-        } else {
-          x[r] = fmaf(ca + di[i], own, sum1 * (1.f / kSa));
-          if (ST == kLast) x[r] *= 1.f / kSx;
-        }
-        if (kMirror && row == col + r) {
-          if (ST == kGram)
-            g.adiag[t.off_d + row] = x[r] * (1.f / kSa);
-          else
-            g.bdiag[t.off_d + row] = fmaf(di[i], fmaf(cc, di[i], cb1), x[r] * (1.f / kSa));
-          x[r] = 0.f;
-        }
-      }
-      if constexpr (ST == kLast && sizeof(O) == 4) {
-        // in the parameter's orientation, one element at a time
-        float* f = reinterpret_cast<float*>(rows16);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int y = i * 16 + lr, z = j * 16 + lk * 4 + r;
-          f[t.tall ? z * (TM + 1) + y : y * (TN + 1) + z] = x[r];
-        }
-      } else if constexpr (ST == kLast) {
-        hi[j] = u2{f32_to_bf16(x[0]) | (f32_to_bf16(x[1]) << 16),
-                   f32_to_bf16(x[2]) | (f32_to_bf16(x[3]) << 16)};
-      } else {
-        union {
-          u2 u;
-          h4 h;
-        } v;
-        v.u = hi[j] = pack4(x);
-        if (ST == kStep || SPLIT) {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[r] -= static_cast<float>(v.h[r]);
-          lo[j] = pack4(x);
-        }
-      }
+      if constexpr (SPLIT) acc[i][j] = sum[i][j];
+      *reinterpret_cast<f4*>(own + ((i * FN + j) * 64 + lane) * 16) = acc[i][j];
     }
-    if (i + Ahead < FM) own_rows(i + Ahead);
-    if constexpr (ST == kLast && sizeof(O) == 4) continue;
-    const int r0 = rb + i * 16;
-    if constexpr (ST == kLast) {
-      if (!t.tall)
-        store_rows<FN>(rows16, hi, [&](int r, int c, u4 v) { put(r0 + r, cb + c, t.m, v); });
-    } else {
-      store_rows<FN>(rows16, hi, to(dh, r0, cb, qrows));
-      if constexpr (ST == kStep || SPLIT) store_rows<FN>(rows16, lo, to(dl, r0, cb, qrows));
-    }
-    if (ST != kStep && mirror) keep_transposed<FN>(image, kImageLd, i, hi);
-    if constexpr (SPLIT && kMirror) {
+  __syncthreads();
+  f4 all[1][1];
+  all[0][0] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {  // for a second image: over the sums
-        acc[i][j][0] = __uint_as_float(lo[j].x);
-        acc[i][j][1] = __uint_as_float(lo[j].y);
-      }
-    }
-  }
-  if constexpr (ST == kLast && sizeof(O) == 4) {
-    const float* f = reinterpret_cast<const float*>(rows16);
-    const int n_rows = t.tall ? TN : TM, width = t.tall ? TM : TN;
-    const int64_t r0 = t.tall ? cb : rb, c0 = t.tall ? rb : cb, last = t.tall ? t.n : t.m;
-    for (int e = lane; e < n_rows * width; e += 64) {
-      const int r = e / width, c = e % width;
-      if (r0 + r < last && c0 + c < cols) out[(r0 + r) * cols + c0 + c] = f[r * (width + 1) + c];
-    }
-  } else if constexpr (ST == kLast) {
-    if (mirror)
-      store_image<TN, TM>(image, [&](int r, int c, u4 v) { put(cb + r, rb + c, t.n, v); });
-  } else if constexpr (kMirror) {
-    if (mirror) {
-      // rows of the image past the plane: tiles of the lower triangle have
-      // their columns inside wherever their rows are
-      store_image<TN, TM>(image, to(dh, cb, rb, prows));
-      if constexpr (SPLIT) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          u2 lo[FN];
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            lo[j] = u2{__float_as_uint(acc[i][j][0]), __float_as_uint(acc[i][j][1])};
-          keep_transposed<FN>(image, kImageLd, i, lo);
-        }
-        store_image<TN, TM>(image, to(dl, cb, rb, prows));
-      }
-    }
-  }
+  for (int w = 0; w < 4; ++w)
+    all[0][0] += *reinterpret_cast<const f4*>(lds + w * kOwn + (wave * 64 + lane) * 16);
+  res.finish(g, t, o, all, nullptr);
 }
 
 // `from`: which plane holds X.  Its low parts are replaced in place, by the
 // workgroup that reads them, unless they are an operand too.
-GemmArgs gemm_args(const MuonArgs& a, const MuonGemmTile* tiles, int from) {
+GemmArgs gemm_args(const MuonArgs& a, int from) {
   auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
   GemmArgs g{};
-  g.tiles = tiles;
   g.adiag = reinterpret_cast<float*>(a.ws + a.w.adiag);
   g.bdiag = reinterpret_cast<float*>(a.ws + a.w.bdiag);
   g.xh = half(a.w.xh[from]);
-  g.xl = half(a.w.xl[from]);
+  g.xl = a.ws + a.w.xl[from];
   g.yh = half(a.w.xh[1 - from]);
-  g.yl = half(a.w.xl[1 - from]);
+  g.yl = a.ws + a.w.xl[1 - from];
   g.ah = half(a.w.ah);
   g.al = half(a.w.al);
   g.bh = half(a.w.bh);
@@ -1005,33 +1370,46 @@ GemmArgs gemm_args(const MuonArgs& a, const MuonGemmTile* tiles, int from) {
   return g;
 }
 
+using Thin = Shape<32, 32, 1, 1, 64, 2, 2>;  // per wave
 using Small = Shape<64, 64, 2, 2, 64, 3, 2>;
 using Mid = Shape<128, 128, 2, 2, 64, 2, 2>;
 using Big = Shape<256, 256, 2, 4, 64, 2, 2>;
-static_assert(Small::BM == kMuonTiles[0] && Mid::BM == kMuonTiles[1] && Big::BM == kMuonTiles[2]);
+static_assert(Thin::BM == kMuonTiles[0] && Small::BM == kMuonTiles[1] &&
+              Mid::BM == kMuonTiles[2] && Big::BM == kMuonTiles[3]);
 
 template <typename S, Stage ST, bool SPLIT, typename O>
-hipError_t launch_shape(GemmArgs& g, int64_t n, const Sink& sink) {
-  void* p[] = {&g};
-  return sink.launch(reinterpret_cast<const void*>(&k_gemm<S, ST, SPLIT, O>),
-                     dim3(static_cast<unsigned>(n)), dim3(S::Threads), p, 0);
+hipError_t launch_shape(const MuonTiles& t, GemmArgs& g, const Sink& sink) {
+  const int64_t n = t.n;
+  const MuonGemmTile* tiles = t.tiles;
+  void* p[] = {&tiles, &g};
+  if constexpr (S::NW == 1)
+    return sink.launch(reinterpret_cast<const void*>(&k_thin<S, ST, SPLIT, O>),
+                       dim3(static_cast<unsigned>(n)), dim3(256), p, 0);
+  else
+    return sink.launch(reinterpret_cast<const void*>(&k_gemm<S, ST, SPLIT, O>),
+                       dim3(static_cast<unsigned>(n)), dim3(S::Threads), p, 0);
 }
 
 template <Stage ST, typename O>
 hipError_t launch_gemm(bool split, const MuonTiles& t, GemmArgs& g, const Sink& sink) {
   if (t.n <= 0) return hipErrorInvalidValue;
   if constexpr (!(ST == kLast && sizeof(O) == 2)) {
-    if (split)
-      return t.shape == 0 ? launch_shape<Small, ST, true, O>(g, t.n, sink)
-                          : launch_shape<Mid, ST, true, O>(g, t.n, sink);
+    if (split) {
+      switch (t.shape) {
+        case 0: return launch_shape<Thin, ST, true, O>(t, g, sink);
+        case 1: return launch_shape<Small, ST, true, O>(t, g, sink);
+        default: return launch_shape<Mid, ST, true, O>(t, g, sink);
+      }
+    }
   }
   if constexpr (ST == kLast && sizeof(O) == 4) {
     return hipErrorInvalidValue;  // fp32 results take split operands
   } else {
     switch (t.shape) {
-      case 0: return launch_shape<Small, ST, false, O>(g, t.n, sink);
-      case 1: return launch_shape<Mid, ST, false, O>(g, t.n, sink);
-      default: return launch_shape<Big, ST, false, O>(g, t.n, sink);
+      case 0: return launch_shape<Thin, ST, false, O>(t, g, sink);
+      case 1: return launch_shape<Small, ST, false, O>(t, g, sink);
+      case 2: return launch_shape<Mid, ST, false, O>(t, g, sink);
+      default: return launch_shape<Big, ST, false, O>(t, g, sink);
     }
   }
 }
@@ -1095,29 +1473,28 @@ hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* ma
   return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_norm(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+hipError_t launch_muon_norm(const MuonArgs& a, const MuonChunk* tiles, int64_t n,
                             const void* update, int dt, const Sink& sink) {
   if (n <= 0) return hipErrorInvalidValue;
-  const MuonMat* mats = a.mats;
   double* partial = reinterpret_cast<double*>(a.ws + a.w.partial);
-  void* p[] = {&mats, &tiles, &update, &partial};
+  void* p[] = {&tiles, &update, &partial};
   const void* fn = dt == FSDP_BF16 ? reinterpret_cast<const void*>(&k_norm<u16>)
                                    : reinterpret_cast<const void*>(&k_norm<float>);
   return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_convert(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, int64_t n,
                                const void* update, int dt, double eps, const double (&poly)[3],
                                const Sink& sink) {
   if (n <= 0) return hipErrorInvalidValue;
   auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
   ConvertArgs c{};
-  c.mats = a.mats;
   c.tiles = tiles;
   c.partial = reinterpret_cast<const double*>(a.ws + a.w.partial);
   c.coef = reinterpret_cast<float*>(a.ws + a.w.coef);
   c.xh = half(a.w.xh[0]);
-  c.xl = a.low ? half(a.w.xl[0]) : nullptr;
+  c.xl = a.low ? a.ws + a.w.xl[0] : nullptr;
+  c.bytes = !a.split;
   c.eps = eps;
   c.a = poly[0];
   c.b = poly[1];
@@ -1129,13 +1506,13 @@ hipError_t launch_muon_convert(const MuonArgs& a, const MuonTile* tiles, int64_t
 }
 
 hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, int from, const Sink& sink) {
-  GemmArgs g = gemm_args(a, t.tiles, from);
+  GemmArgs g = gemm_args(a, from);
   return launch_gemm<kGram, u16>(a.split, t, g, sink);
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
                             const double (&poly)[3], const Sink& sink) {
-  GemmArgs g = gemm_args(a, t.tiles, 0);
+  GemmArgs g = gemm_args(a, 0);
   g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
   g.b = static_cast<float>(poly[1]);
   g.c = static_cast<float>(poly[2]);
@@ -1145,7 +1522,7 @@ hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
 hipError_t launch_muon_step(const MuonArgs& a, const MuonTiles& t, int from, bool first,
                             bool last, const double (&poly)[3], void* ortho, int ortho_dt,
                             const Sink& sink) {
-  GemmArgs g = gemm_args(a, t.tiles, from);
+  GemmArgs g = gemm_args(a, from);
   g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
   g.a = static_cast<float>(poly[0]);
   if (first && !a.low) g.xl = nullptr;

@@ -40,23 +40,35 @@ constexpr int kMuonPad = 64;
 // apart (sides that are powers of two) all met on one channel.
 inline int64_t muon_pitch(int64_t cols) { return (cols + 127) / 128 * 128 + (((cols + 127) / 128) % 2 ? 0 : 128); }
 
-// A kernel's tile or chunk: which matrix, and where in it.
-struct MuonTile {
-  int32_t mat, i, j, unused;
+// The kernels' tiles hold all that a workgroup needs to know of its matrix:
+// one load at its start, where a tile naming a matrix took a chain of them.
+
+// A chunk of the update, [lo, hi) of the unit, for one partial sum.
+struct MuonChunk {
+  int64_t lo, hi;
+  int64_t to, unused;
 };
 
-// A product's tile, with all that its workgroup needs: one load at its start
-// instead of a chain of two.
-struct MuonGemmTile {
+// A 64 x 64 tile of the update, row and column i and j of those.
+struct alignas(64) MuonConvertTile {
+  int64_t flat_off, off_x;
+  int32_t rows, cols, ldx, i, j, mat;
+  int32_t norm_first, norm_count;
+  int32_t tall, unused[3];
+};
+
+// A product's tile.  mat < 0: none.  Bit 30 of mat: more rows than columns.
+struct alignas(64) MuonGemmTile {
   int64_t off_x, off_a, flat_off;
   int32_t off_d, i, j, mat;
   int32_t mp, np, m, n;
   int32_t ldx, lda;
-  int32_t tall, unused;
 };
+constexpr int32_t kMuonTall = 1 << 30;
+static_assert(sizeof(MuonConvertTile) == 64 && sizeof(MuonGemmTile) == 64);
 
 // Sides of the products' tiles.
-constexpr int kMuonTiles[3] = {64, 128, 256};
+constexpr int kMuonTiles[4] = {32, 64, 128, 256};
 
 // One kind of product's tiles on the device.
 struct MuonTiles {
@@ -75,8 +87,8 @@ struct MuonItem {
 // Device copies of the tables, one per device, in one allocation.
 struct MuonDevice {
   const MuonMat* mats;
-  const MuonTile* norm;       // chunks of the norm's partial sums
-  const MuonTile* convert;    // 64 x 64 tiles of the parameter's own orientation
+  const MuonChunk* norm;
+  const MuonConvertTile* convert;
   MuonTiles gram, poly, step;  // the lower triangles of A and of B, X
   const MuonItem* momentum;   // flat space
   const MuonItem* apply;      // shard space
@@ -92,7 +104,6 @@ struct MuonWorkspace {
 
 // Everything the launchers of the products need.
 struct MuonArgs {
-  const MuonMat* mats;
   char* ws;
   MuonWorkspace w;
   bool split;
@@ -105,7 +116,8 @@ struct fsdp_muon {
   int32_t R = 0;
   int64_t T = 0, S = 0;
   std::vector<fsdp::MuonMat> mats;
-  std::vector<fsdp::MuonTile> norm, convert;
+  std::vector<fsdp::MuonChunk> norm;
+  std::vector<fsdp::MuonConvertTile> convert;
   // the products' tiles for results in bf16, and for split operands
   struct Tiles {
     std::vector<fsdp::MuonGemmTile> gram, poly, step;
@@ -147,11 +159,11 @@ hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* ma
                              const void* ortho, int ortho_dt, float* master, void* param,
                              int param_dt, const MuonScalars& sc, bool vec, const Sink& sink);
 
-hipError_t launch_muon_norm(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+hipError_t launch_muon_norm(const MuonArgs& a, const MuonChunk* tiles, int64_t n,
                             const void* update, int dt, const Sink& sink);
 // The update into the planes of X, scaled by a power of
 // two, and the first step's coefficients with what is left of the norm.
-hipError_t launch_muon_convert(const MuonArgs& a, const MuonTile* tiles, int64_t n,
+hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, int64_t n,
                                const void* update, int dt, double eps, const double (&poly)[3],
                                const Sink& sink);
 // A = X X^T.

@@ -481,8 +481,8 @@ fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
  * (with X^T X on the right where rows > columns: the same matrix, smaller
  * products).  ortho gets the last X, in unit order.
  *   Products take operands of 11 significant bits (fp16, scaled by powers
- *   of two) and sum in fp32; the term a X and the diagonals of A and
- *   b A + c A A are kept in about 22 and 24 bits.  With ortho FSDP_BF16 the result is
+ *   of two) and sum in fp32; the term a X is kept in 14 bits, the diagonals
+ *   of A and b A + c A A in fp32.  With ortho FSDP_BF16 the result is
  *   within about the rounding to bf16 of the exact one.  With FSDP_F32
  *   every operand is kept as two fp16 parts and each product is the sum of
  *   three: an error near that of fp32 products, at three times the work.

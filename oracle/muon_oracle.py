@@ -93,13 +93,17 @@ def orthogonalize(u, steps=5, eps=1e-7, poly=POLY):
 def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
     """The definition with the library's documented precision: operands of
     11 bits (split: of 22) under power-of-two scales, fp32 sums, the residual
-    in two parts and the diagonals of A and B in fp32.  What it is off the definition by
+    of 14 bits (split: of 22) and the diagonals of A and B in fp32.  What it is off the definition by
     is what the kernels may be off by."""
     f32 = np.float32
 
     def parts(x, s):
         hi = (x * f32(s)).astype(np.float16).astype(f32)
-        lo = (x * f32(s) - hi).astype(np.float16).astype(f32)
+        lo = (x * f32(s) - hi).astype(np.float16)
+        if not split:   # 5 bits of exponent and 2 of mantissa: fp16's upper byte, rounded
+            b = lo.view(np.uint16)
+            lo = ((b + 0x7f + ((b >> 8) & 1)) & 0xff00).astype(np.uint16).view(np.float16)
+        lo = lo.astype(f32)
         return hi / f32(s), lo / f32(s)
 
     def prod(p, q):
