@@ -168,6 +168,9 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     mu->n_partial += t.norm_count;
     if (k >= kMuonTall - 1) return FSDP_ERR_UNSUPPORTED;
     mu->mats.push_back(t);
+    const double rows = static_cast<double>(t.rows), cols = static_cast<double>(t.cols);
+    mu->scales.push_back(MuonScale{std::sqrt(std::max(1.0, rows / cols)),
+                                   0.2 * std::sqrt(std::max(rows, cols))});
   }
   // grids first: a table that is refused is not built
   int64_t n_convert = 0, n_wide = 0, n_square = 0;
@@ -176,7 +179,8 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     const int64_t si = t.mp / kMuonTiles[0], sj = t.np / kMuonTiles[0];
     n_wide += si * sj;
     n_square += si * (si + 1) / 2;
-    if (n_convert > kMaxItems || n_wide > kMaxItems || n_square > kMaxItems)
+    // products have workgroups of up to 512 lanes
+    if (n_convert > kMaxItems || n_wide > kMaxItems / 2 || n_square > kMaxItems / 2)
       return FSDP_ERR_UNSUPPORTED;
   }
   if (mu->n_partial > kMaxItems || mu->nd > INT32_MAX) return FSDP_ERR_UNSUPPORTED;
@@ -255,6 +259,9 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     fill(to.gram, &to.gram_shape, true, true);
     fill(to.poly, &to.poly_shape, true, false);
     fill(to.step, &to.step_shape, false, false);
+    // (filling up may have made a table longer than its tiles)
+    for (const auto* t : {&to.gram, &to.poly, &to.step})
+      if (static_cast<int64_t>(t->size()) > kMaxItems / 2) return FSDP_ERR_UNSUPPORTED;
   }
   return FSDP_OK;
 }
@@ -314,11 +321,11 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
     bytes += (size[n] + 255) / 256 * 256;
     ++n;
   };
-  part(mats);
   part(norm);
   part(convert);
   part(momentum);
   part(apply);
+  part(scales);
   for (const Tiles& t : tiles) {
     part(t.gram);
     part(t.poly);
@@ -344,12 +351,12 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
     it = dev_.emplace(dev, mem).first;
   }
   const char* b = static_cast<const char*>(it->second);
-  out->mats = reinterpret_cast<const fsdp::MuonMat*>(b + at[0]);
-  out->norm = reinterpret_cast<const fsdp::MuonChunk*>(b + at[1]);
-  out->convert = reinterpret_cast<const fsdp::MuonConvertTile*>(b + at[2]);
-  out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[3]);
-  out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[4]);
+  out->norm = reinterpret_cast<const fsdp::MuonChunk*>(b + at[0]);
+  out->convert = reinterpret_cast<const fsdp::MuonConvertTile*>(b + at[1]);
+  out->momentum = reinterpret_cast<const fsdp::MuonItem*>(b + at[2]);
+  out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[3]);
   const Tiles& t = tiles[split ? 1 : 0];
+  out->scales = reinterpret_cast<const fsdp::MuonScale*>(b + at[4]);
   const int k = split ? 8 : 5;
   auto gemm = [&](int i, const std::vector<fsdp::MuonGemmTile>& v, int shape) {
     return fsdp::MuonTiles{reinterpret_cast<const fsdp::MuonGemmTile*>(b + at[i]),
@@ -567,7 +574,7 @@ fsdp_status fsdp_muon_apply(const fsdp_muon* mu, const fsdp_muon_hparams* hp, co
     fsdp::MuonDevice d;
     if ((st = mu->device(false, &d)) != FSDP_OK) return st;
     return fsdp::status_of(fsdp::launch_muon_apply(
-        d.apply, static_cast<int64_t>(mu->apply.size()), d.mats, ortho, ortho_dtype, master,
+        d.apply, static_cast<int64_t>(mu->apply.size()), d.scales, ortho, ortho_dtype, master,
         param_out, param_dtype, scalars(hp),
         aligned(ortho, 16) && aligned(master, 16) && aligned(param_out, 16),
         fsdp::StreamSink(stream)));
@@ -620,7 +627,7 @@ fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* h
                          static_cast<char*>(workspace) + update_bytes, sink);
     if (st == FSDP_OK)
       st = fsdp::status_of(fsdp::launch_muon_apply(
-          d.apply, static_cast<int64_t>(mu->apply.size()), d.mats, update, FSDP_BF16, master,
+          d.apply, static_cast<int64_t>(mu->apply.size()), d.scales, update, FSDP_BF16, master,
           param_out, param_dtype, ms, vec, sink));
     if (st == FSDP_OK && adamw && !mu->rest.host.empty())
       st = fsdp::status_of(fsdp::launch_fused(rest, static_cast<int64_t>(mu->rest.host.size()), g,

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(kThreads) void k_momentum(const MuonItem* __restric
 }
 
 struct ApplyArgs {
-  const MuonMat* mats;
+  const MuonScale* scales;
   const void* ortho;
   float* master;
   void* param;
@@ -212,13 +212,9 @@ __global__ __launch_bounds__(kThreads) void k_apply(const MuonItem* __restrict__
   P* param = static_cast<P*>(a.param);
   const int64_t s0 = w.src + (e0 - w.dst);
   // lr times the matrix's scale
-  const double rows = static_cast<double>(a.mats[w.mat].rows);
-  const double cols = static_cast<double>(a.mats[w.mat].cols);
   double rate = a.sc.lr;
-  if (a.sc.scale == FSDP_MUON_SCALE_ASPECT)
-    rate *= sqrt(fmax(1.0, rows / cols));
-  else if (a.sc.scale == FSDP_MUON_SCALE_RMS)
-    rate *= 0.2 * sqrt(fmax(rows, cols));
+  if (a.sc.scale == FSDP_MUON_SCALE_ASPECT) rate *= a.scales[w.mat].aspect;
+  if (a.sc.scale == FSDP_MUON_SCALE_RMS) rate *= a.scales[w.mat].rms;
   auto one = [&](float p, float x) {
     return static_cast<float>(static_cast<double>(p) * a.sc.decay -
                               rate * static_cast<double>(x));
@@ -310,39 +306,55 @@ struct ConvertArgs {
   double eps, a, b, c;
 };
 
+// Eight adjacent elements (aligned to 16 bytes) as floats.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  if constexpr (sizeof(T) == 2) {
+    const u4 v = __builtin_nontemporal_load(reinterpret_cast<const u4*>(p));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(v[k] << 16);
+      x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
+    }
+  } else {
+    float y[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      El<float>::load4(p + 4 * h, y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[4 * h + k] = y[k];
+    }
+  }
+}
+
 // 64 x 64 tiles of the update into X, transposed where the parameter has
 // more rows than columns.  With |U| + eps = N, the planes get U 2^-e with
 // 2^e <= N < 2^(e+1): exact for bf16 updates.  What is left, f = 2^e / N,
 // goes into the first step's coefficients: A is then A f^-2 and X is X f^-1.
-// A lane has 16 adjacent entries of a row.
+// A lane has 8 adjacent entries of each of two rows.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ update,
                                                       ConvertArgs a) {
   constexpr int Ld = 72;
   __shared__ __align__(16) _Float16 tile[64 * Ld];
-  const MuonConvertTile mat = a.tiles[blockIdx.x], &t = mat;
+  const MuonConvertTile t = a.tiles[blockIdx.x];
   const int64_t r0 = int64_t(t.i) * 64, c0 = int64_t(t.j) * 64;
-  const int lr = threadIdx.x >> 2, lc = (threadIdx.x & 3) * 16;
-  const int64_t r = r0 + lr, c = c0 + lc;
-  const T* u = update + mat.flat_off + r * mat.cols + c;
-  float x[16];
-  if (r < mat.rows && c + 16 <= mat.cols &&
-      (reinterpret_cast<uintptr_t>(u) & (4 * sizeof(T) - 1)) == 0) {
+  const int lr = threadIdx.x >> 3, lc = (threadIdx.x & 7) * 8;
+  float x[2][8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float y[4];
-      El<T>::load4(u + 4 * k, y);
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = r0 + lr + 32 * h, c = c0 + lc;
+    const T* u = update + t.flat_off + r * t.cols + c;
+    if (r < t.rows && c + 8 <= t.cols && (reinterpret_cast<uintptr_t>(u) & 15) == 0) {
+      load8(u, x[h]);
+    } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) x[4 * k + q] = y[q];
+      for (int k = 0; k < 8; ++k)
+        x[h][k] = r < t.rows && c + k < t.cols ? El<T>::load(u + k) : 0.f;
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      x[k] = r < mat.rows && c + k < mat.cols ? El<T>::load(u + k) : 0.f;
   }
   double s = 0;
-  for (int k = threadIdx.x; k < mat.norm_count; k += kThreads)
-    s += a.partial[mat.norm_first + k];
+  for (int k = threadIdx.x; k < t.norm_count; k += kThreads) s += a.partial[t.norm_first + k];
   const double norm = sqrt(block_sum(s)) + a.eps;
   const int e = ilogb(norm);
   const double scale = ldexp(static_cast<double>(kSx), -e);
@@ -354,58 +366,64 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
     k[1] = bad ? NAN : static_cast<float>(a.b * f * f * f);
     k[2] = bad ? NAN : static_cast<float>(a.c * f * f * f * f * f);
   }
+  // where a lane's entries go: rows of X, across them in a tall parameter
+  const int64_t to0 = t.tall ? (c0 + lr) * t.ldx + r0 + lc : (r0 + lr) * t.ldx + c0 + lc;
+  const int64_t to[2] = {t.off_x + to0, t.off_x + to0 + 32 * int64_t(t.ldx)};
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      x[h][k] = static_cast<float>(static_cast<double>(x[h][k]) * scale);
   union {
-    _Float16 h[16];
-    u4 v[2];
-  } part;
+    _Float16 h[8];
+    u4 v;
+  } part[2];
+  for (int low = 0; low < (a.xl && !a.bytes ? 2 : 1); ++low) {
 #pragma unroll
-  for (int k = 0; k < 16; ++k) x[k] = static_cast<float>(static_cast<double>(x[k]) * scale);
-  for (int low = 0; low < (a.xl ? 2 : 1); ++low) {
-    if (low && a.bytes) break;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      part.h[k] = static_cast<_Float16>(x[k]);
-      x[k] -= static_cast<float>(part.h[k]);
-    }
-    _Float16* out = (low ? static_cast<_Float16*>(a.xl) : a.xh) + mat.off_x;
-    if (!mat.tall) {
-      u4* d = reinterpret_cast<u4*>(out + r * mat.ldx + c);
-      d[0] = part.v[0];
-      d[1] = part.v[1];
-    } else {
-      __syncthreads();
-      u4* d = reinterpret_cast<u4*>(tile + lr * Ld + lc);
-      d[0] = part.v[0];
-      d[1] = part.v[1];
+      for (int k = 0; k < 8; ++k) {
+        part[h].h[k] = static_cast<_Float16>(x[h][k]);
+        x[h][k] -= static_cast<float>(part[h].h[k]);
+      }
+    if (t.tall) {
       __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) part.h[k] = tile[(lc + k) * Ld + lr];
-      d = reinterpret_cast<u4*>(out + (c0 + lr) * mat.ldx + r0 + lc);
-      d[0] = part.v[0];
-      d[1] = part.v[1];
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u4*>(tile + (lr + 32 * h) * Ld + lc) = part[h].v;
+      __syncthreads();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) part[h].h[k] = tile[(lc + k) * Ld + lr + 32 * h];
     }
+    _Float16* out = low ? static_cast<_Float16*>(a.xl) : a.xh;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<u4*>(out + to[h]) = part[h].v;
   }
   if (!a.xl || !a.bytes) return;
-  char* out = static_cast<char*>(a.xl) + mat.off_x;
-  u4 v;
+  union {
+    char b[8];
+    u2 v;
+  } low[2];
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    v[k] = pack_bf8({x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]});
-  if (!mat.tall) {
-    *reinterpret_cast<u4*>(out + r * mat.ldx + c) = v;
-  } else {
-    char* bytes = reinterpret_cast<char*>(tile);  // rows of 64 and 16 between
+  for (int h = 0; h < 2; ++h)
+    low[h].v = u2{pack_bf8({x[h][0], x[h][1], x[h][2], x[h][3]}),
+                  pack_bf8({x[h][4], x[h][5], x[h][6], x[h][7]})};
+  if (t.tall) {
+    char* bytes = reinterpret_cast<char*>(tile);
     __syncthreads();
-    *reinterpret_cast<u4*>(bytes + lr * 80 + lc) = v;
-    __syncthreads();
-    union {
-      char b[16];
-      u4 v;
-    } w;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) w.b[k] = bytes[(lc + k) * 80 + lr];
-    *reinterpret_cast<u4*>(out + (c0 + lr) * mat.ldx + r0 + lc) = w.v;
+    for (int h = 0; h < 2; ++h) *reinterpret_cast<u2*>(bytes + (lr + 32 * h) * Ld + lc) = low[h].v;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) low[h].b[k] = bytes[(lc + k) * Ld + lr + 32 * h];
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    *reinterpret_cast<u2*>(static_cast<char*>(a.xl) + to[h]) = low[h].v;
 }
 
 // ---------------------------------------------------------------- products
@@ -1459,11 +1477,11 @@ hipError_t launch_muon_momentum(const MuonItem* items, int64_t n, const PtrArray
   return momentum_r<float, float>(items, n, grads, R, replicas, m, update, sc, vec, sink);
 }
 
-hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* mats,
+hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonScale* scales,
                              const void* ortho, int ortho_dt, float* master, void* param,
                              int param_dt, const MuonScalars& sc, bool vec, const Sink& sink) {
   if (n <= 0) return hipErrorInvalidValue;
-  ApplyArgs a{mats, ortho, master, param, sc, vec};
+  ApplyArgs a{scales, ortho, master, param, sc, vec};
   const bool ob = ortho_dt == FSDP_BF16, pb = param_dt == FSDP_BF16;
   const void* fn = ob ? (pb ? reinterpret_cast<const void*>(&k_apply<u16, u16>)
                             : reinterpret_cast<const void*>(&k_apply<u16, float>))

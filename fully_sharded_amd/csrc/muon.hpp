@@ -84,14 +84,19 @@ struct MuonItem {
   int32_t len, mat;
 };
 
+// A matrix's scales.
+struct MuonScale {
+  double aspect, rms;
+};
+
 // Device copies of the tables, one per device, in one allocation.
 struct MuonDevice {
-  const MuonMat* mats;
   const MuonChunk* norm;
   const MuonConvertTile* convert;
   MuonTiles gram, poly, step;  // the lower triangles of A and of B, X
   const MuonItem* momentum;   // flat space
   const MuonItem* apply;      // shard space
+  const MuonScale* scales;    // per matrix
 };
 
 // Where each part of fsdp_orthogonalize's workspace begins, in bytes.
@@ -124,6 +129,7 @@ struct fsdp_muon {
     int gram_shape = 0, poly_shape = 0, step_shape = 0;
   } tiles[2];
   std::vector<fsdp::MuonItem> momentum, apply;
+  std::vector<fsdp::MuonScale> scales;
   fsdp::WorkTable rest;  // shard space: all that is not chosen, padding too
   int64_t nx = 0, na = 0, nd = 0, n_partial = 0;  // plane, diagonal and partial-sum sizes
 
@@ -155,7 +161,7 @@ hipError_t launch_muon_momentum(const MuonItem* items, int64_t n, const PtrArray
                                 int grad_dt, bool replicas, float* m, void* update, int update_dt,
                                 const MuonScalars& sc, bool vec, const Sink& sink);
 
-hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonMat* mats,
+hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonScale* scales,
                              const void* ortho, int ortho_dt, float* master, void* param,
                              int param_dt, const MuonScalars& sc, bool vec, const Sink& sink);
 

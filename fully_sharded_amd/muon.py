@@ -153,12 +153,31 @@ def _work(t):
     return ctypes.c_void_p(_dev(t, "workspace")), t.numel()
 
 
-def _bound(name, args, keep, tensors):
+def _caller(name, keep, tensors):
+    """(BoundCall, f(args, stream)): the library call on the given stream, or
+    on the current one of the tensors' device, which has to be the current
+    device at every call.  The handle is asked of torch directly: a Stream
+    object costs 2.7 us, a third of a small call."""
     _on_current_device(*tensors)
-    call = BoundCall(name, args, keep)
+    device = tensors[0].device.index
+    call = BoundCall(name, None, keep)
+    fn, current, raw = call._fn, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+    def go(args, stream):
+        if current() != device:
+            raise ValueError(f"the tensors are on cuda:{device}, the current device is "
+                             f"cuda:{current()}")
+        status = fn(*args, raw(device) if stream is None else _stream(stream))
+        if status != 0:
+            _check(name, status)
+    return call, go
+
+
+def _bound(name, args, keep, tensors):
+    call, go = _caller(name, keep, tensors)
 
     def run(stream=None):
-        call._run(*call._args, _stream(stream))
+        go(args, stream)
     run.call = call
     return run
 
@@ -227,11 +246,10 @@ def bind_muon_shard_step(mu: Muon, hp: dict, grads, master, m, param_out, worksp
             None if v is None else _shards(mu, v, "v"),
             _shards(mu, param_out, "param_out", False), _dtype_code(param_out), ws, n)
     state = (master, m, param_out, workspace) + (() if v is None else (v,))
-    _on_current_device(*gs, *state)
-    call = BoundCall("fsdp_muon_shard_step", None, (mu, h, a, gs, state))
+    call, go = _caller("fsdp_muon_shard_step", (mu, h, a, gs, state), (*gs, *state))
 
     def run(step=1, stream=None):
-        call._run(*head, int(step), *tail, _stream(stream))
+        go((*head, int(step), *tail), stream)
     run.call = call
     return run
 
