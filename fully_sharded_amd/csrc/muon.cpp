@@ -186,6 +186,11 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
   if (mu->n_partial > kMaxItems || mu->nd > INT32_MAX) return FSDP_ERR_UNSUPPORTED;
 
   // the per-element work: the plan's runs, cut where parameters end
+  int64_t elements = 0;
+  for (const MuonMat& t : mu->mats) elements += t.rows * t.cols;
+  mu->apply.reserve(static_cast<size_t>(elements / kItem + 1));
+  mu->momentum.reserve(static_cast<size_t>(elements / kItem + 1));
+  mu->convert.reserve(static_cast<size_t>(n_convert));
   std::vector<Work> rest;
   auto split = [&](int64_t shard, int64_t flat, int64_t len) {
     // first parameter that ends after `flat`
@@ -217,8 +222,10 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
       count_items(rest, kShardChunk) > kMaxItems)
     return FSDP_ERR_UNSUPPORTED;
   emit_items(rest, kShardChunk, mu->rest.host);
-  std::sort(mu->momentum.begin(), mu->momentum.end(),
-            [](const MuonItem& a, const MuonItem& b) { return a.dst < b.dst; });
+  // in the order of the flat space (the flat layout has them so already)
+  const auto before = [](const MuonItem& a, const MuonItem& b) { return a.dst < b.dst; };
+  if (!std::is_sorted(mu->momentum.begin(), mu->momentum.end(), before))
+    std::sort(mu->momentum.begin(), mu->momentum.end(), before);
 
   for (int32_t k = 0; k < n_params; ++k) {
     const MuonMat& t = mu->mats[k];
