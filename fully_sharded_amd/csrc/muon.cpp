@@ -113,7 +113,8 @@ int64_t count(const std::vector<MuonMat>& mats, int64_t tile, bool square) {
 // units without a tile: one 512 x 512 matrix (36 and 64 tiles of 64 x 64)
 // takes 62 us a pass with them and 90 without; of one block of hidden 512,
 // A (216 tiles, depth up to 2048) gains 6 us a pass, B (216) loses 5 and the
-// step (768) 45.
+// step (768) 45.  (build_muon takes 64 x 64 tiles for A all the same where
+// their sums, in parts, fill the compute units.)
 int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool split) {
   int64_t tiles = 0, rounds = 0;
   for (const MuonMat& t : mats) {
@@ -124,6 +125,59 @@ int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool spli
   if (!split && tiles >= 2 * kCus && rounds >= tiles * 1024) return 3;
   if (count(mats, 128, square) >= 2 * kCus) return 2;
   return count(mats, 64, square) <= (gram ? kCus : kCus / 2) ? 0 : 1;
+}
+
+// A's smaller tiles, where a few of them have long sums: these are cut into
+// parts, each a workgroup's, and joined by a second launch.  Parts are as
+// long as gives every compute unit two, kPart rounds at least, and are made
+// only where the longest sum gets kJoin rounds and a fifth shorter, so that
+// the second launch and the partial sums' way through memory pay.  Of one 32 x n matrix,
+// five steps, whole sums and parts: n = 4,096 77 us and 88 (so they stay
+// whole), 6,144 90 and 90, 16,384 152 and 91, 1M 7,020 and 860; fp32 results,
+// with three products 124 and 95 at 4,096; 1440 x 16384 (276 tiles of 64 x 64)
+// 1,013 and 935, 1800 x 32000 (435) 2,290 and 2,360.  Parts of 16 rounds
+// measured 5-10% longer, four per compute unit level.
+constexpr int64_t kPart = 32, kJoin = 64;
+
+int64_t rounds_of(const std::vector<MuonMat>& mats, int64_t side, int products) {
+  int64_t work = 0;
+  for (const MuonMat& t : mats)
+    work += count({t}, side, true) * products * (t.np / kMuonRound);
+  return work;
+}
+
+int64_t part_rounds(const std::vector<MuonMat>& mats, int64_t side, int products) {
+  const int64_t work = rounds_of(mats, side, products);
+  int64_t longest = 0;
+  for (const MuonMat& t : mats)
+    longest = std::max(longest, int64_t(products) * t.np / kMuonRound);
+  const int64_t len = std::max(kPart, (work + 2 * kCus - 1) / (2 * kCus));
+  return longest >= len + std::max(kJoin, len / 4) ? len : longest;
+}
+
+// `all`: rounds of the matrix's sums.  The same part of all tiles lies
+// together: they read the same columns.
+std::vector<MuonGemmTile> in_parts(const std::vector<MuonGemmTile>& tiles, int64_t all,
+                                   int64_t len, fsdp_muon::Tiles* to) {
+  std::vector<MuonGemmTile> out;
+  const int64_t parts = (all + len - 1) / len, n = static_cast<int64_t>(tiles.size());
+  for (int64_t p = 0; p < parts; ++p)
+    for (int64_t k = 0; k < n; ++k) {
+      MuonGemmTile t = tiles[k];
+      t.m = static_cast<int32_t>(all * p / parts);
+      t.n = static_cast<int32_t>(all * (p + 1) / parts) - t.m;
+      t.flat_off = parts > 1 ? to->n_sums + k * parts + p : -1;
+      out.push_back(t);
+    }
+  if (parts == 1) return out;
+  for (MuonGemmTile t : tiles) {
+    t.m = 0;
+    t.n = static_cast<int32_t>(parts);
+    t.flat_off = to->n_sums;
+    to->n_sums += parts;
+    to->join.push_back(t);
+  }
+  return out;
 }
 
 }  // namespace
@@ -246,6 +300,14 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     fsdp_muon::Tiles& to = mu->tiles[split];
     auto fill = [&](std::vector<MuonGemmTile>& out, int* shape, bool square, bool gram) {
       *shape = shape_of(mu->mats, square, gram, split != 0);
+      const int products = split ? 3 : 1;
+      // 64 x 64 tiles read half as much, where their parts are as many and
+      // no tile has more than 32 to join: 1024 x 32000 takes 882 us with
+      // them and 1,133 in parts of 32 x 32 (whole sums: 1,154), 512 x 32000
+      // 337 and 367 (426); one tile of 32 x 1M in 512 parts took 1,920
+      if (gram && *shape == 0 && count(mu->mats, kMuonTiles[1], true) >= kCus / 16 &&
+          rounds_of(mu->mats, kMuonTiles[1], products) >= 2 * kCus * kPart)
+        *shape = 1;
       auto depth = [gram](const MuonMat& t) { return int64_t(gram ? t.np : t.mp); };
       const int64_t side = kMuonTiles[*shape];
       std::vector<int32_t> order(n_params);
@@ -256,10 +318,20 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
       int64_t all = 0;
       for (const MuonMat& t : mu->mats) all += count({t}, side, square) * depth(t);
       Deal deal(all);
+      const int64_t len = part_rounds(mu->mats, side, products);
       for (int32_t k : order) {
         const MuonMat& t = mu->mats[k];
         const int64_t si = (t.mp + side - 1) / side, sj = (t.np + side - 1) / side;
-        deal.add(square ? grid(t, k, si, si, true) : grid(t, k, si, sj, false), depth(t));
+        const std::vector<MuonGemmTile> tiles =
+            square ? grid(t, k, si, si, true) : grid(t, k, si, sj, false);
+        if (gram && side <= kMuonPartTile) {
+          const int64_t rounds = int64_t(products) * t.np / kMuonRound;
+          const std::vector<MuonGemmTile> parts = in_parts(tiles, rounds, len, &to);
+          deal.add(parts, depth(t) * static_cast<int64_t>(tiles.size()) /
+                              static_cast<int64_t>(parts.size()));
+        } else {
+          deal.add(tiles, depth(t));
+        }
       }
       out = deal.dealt();
     };
@@ -296,6 +368,8 @@ MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split) {
   w.bh = take(a);
   w.al = split ? take(a) : 0;
   w.bl = split ? take(a) : 0;
+  const fsdp_muon::Tiles& t = mu->tiles[split ? 1 : 0];
+  w.sums = take(t.n_sums * kMuonTiles[t.gram_shape] * kMuonTiles[t.gram_shape] * 4);
   w.bytes = at;
   return w;
 }
@@ -317,7 +391,7 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
     (void)hipGetLastError();
     return FSDP_ERR_HIP;
   }
-  constexpr int kParts = 11;
+  constexpr int kParts = 13;
   const void* from[kParts];
   int64_t size[kParts], at[kParts], bytes = 0;
   int n = 0;
@@ -337,8 +411,9 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
     part(t.gram);
     part(t.poly);
     part(t.step);
+    part(t.join);
   }
-  static_assert(kParts == 5 + 2 * 3);
+  static_assert(kParts == 5 + 2 * 4);
   std::lock_guard<std::mutex> lock(mu_);
   auto it = dev_.find(dev);
   if (it == dev_.end()) {
@@ -364,7 +439,7 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
   out->apply = reinterpret_cast<const fsdp::MuonItem*>(b + at[3]);
   const Tiles& t = tiles[split ? 1 : 0];
   out->scales = reinterpret_cast<const fsdp::MuonScale*>(b + at[4]);
-  const int k = split ? 8 : 5;
+  const int k = split ? 9 : 5;
   auto gemm = [&](int i, const std::vector<fsdp::MuonGemmTile>& v, int shape) {
     return fsdp::MuonTiles{reinterpret_cast<const fsdp::MuonGemmTile*>(b + at[i]),
                            static_cast<int64_t>(v.size()), shape};
@@ -372,6 +447,7 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
   out->gram = gemm(k, t.gram, t.gram_shape);
   out->poly = gemm(k + 1, t.poly, t.poly_shape);
   out->step = gemm(k + 2, t.step, t.step_shape);
+  out->join = gemm(k + 3, t.join, t.gram_shape);
   return FSDP_OK;
 }
 
@@ -440,7 +516,7 @@ fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
     e = fsdp::launch_muon_convert(a, d.convert, static_cast<int64_t>(mu->convert.size()), update,
                                   update_dt, hp->eps, poly, sink);
   for (int s = 0; s < hp->ns_steps && e == hipSuccess; ++s) {
-    e = fsdp::launch_muon_gram(a, d.gram, s & 1, sink);
+    e = fsdp::launch_muon_gram(a, d.gram, d.join, s & 1, sink);
     if (e == hipSuccess) e = fsdp::launch_muon_poly(a, d.poly, s == 0, poly, sink);
     if (e == hipSuccess)
       e = fsdp::launch_muon_step(a, d.step, s & 1, s == 0, s == hp->ns_steps - 1, poly, ortho,

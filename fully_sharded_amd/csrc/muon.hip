@@ -445,6 +445,7 @@ struct GemmArgs {
   void* yl;
   _Float16 *ah, *al, *bh, *bl;
   void* ortho;
+  float* sums;  // A's partial sums
 };
 
 enum Stage { kGram, kPoly, kStep, kLast };
@@ -1196,8 +1197,11 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
   const int i0 = t.i * S::BM, j0 = t.j * S::BN;
   const Loader<S, kAcross> loader(wave, i0, j0, o.prows, o.qrows, o.lp, o.lq);
   const Fetcher<S, kAcross> fetcher(wm, wn);
+  static_assert(BK == kMuonRound);
   const int rounds = o.depth / BK;
-  const int total = SPLIT ? 3 * rounds : rounds;
+  constexpr bool kParts = ST == kGram && S::BM == 64;
+  const int first = kParts ? t.m : 0;
+  const int total = kParts ? t.n : SPLIT ? 3 * rounds : rounds;
   const uint32_t lds0 = static_cast<uint32_t>(
       reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
 
@@ -1239,7 +1243,7 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
 #pragma unroll
   for (int s = 0; s < NS; ++s)
     if (s < total) {
-      const From f = from_round<BK>(o, s, rounds);
+      const From f = from_round<BK>(o, first + s, rounds);
 #pragma unroll
       for (int x = 0; x < LP + LQ; ++x) loader.load(f, lds0 + s * S::RoundBytes, x);
     }
@@ -1265,7 +1269,7 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
     wait_lds();  // set 0: asked for half a round ago
     products(0, buf, 1, std::false_type{}, f, 0);
     wait_and_meet<kWait>();
-    if (decltype(loads)::value) f = from_round<BK>(o, it + NS, rounds);
+    if (decltype(loads)::value) f = from_round<BK>(o, first + it + NS, rounds);
     products(1, next, 0, loads, f, buf);
     if constexpr (SPLIT) {
       if (it & 1) flush(sum, acc);
@@ -1283,6 +1287,16 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
       for (int j = 0; j < FN; ++j) acc[i][j] = sum[i][j];
   }
 
+  if constexpr (kParts) {
+    if (t.flat_off >= 0) {  // a part
+      f4* to = reinterpret_cast<f4*>(g.sums) + t.flat_off * (FM * FN * S::Threads) + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) to[(i * FN + j) * S::Threads] = acc[i][j];
+      return;
+    }
+  }
   if constexpr (!kEarly) res.ask(g, t, o, i0 + wm * TM, j0 + wn * TN);
   __syncthreads();  // every wave is done with the operands in LDS
   res.finish(g, t, o, acc, lds + wave * Res::kOut);
@@ -1293,7 +1307,8 @@ __global__ __launch_bounds__(S::Threads, S::Waves - (SPLIT && S::BM > 64 ? 1 : 0
 // for but its own loads until the four are added up, each wave one 16 x 16
 // part.  For few tiles: a compute unit takes in 46 bytes a cycle, so with 64
 // x 64 tiles the operands of a sum of 512 alone are 2,800 cycles (1.3 us of
-// a launch's 6), and most compute units have no tile.
+// a launch's 6), and most compute units have no tile.  A's may be parts of a
+// sum (k_join).
 template <typename S, Stage ST, bool SPLIT, typename O>
 __global__ __launch_bounds__(256, S::Waves) void k_thin(
     const MuonGemmTile* __restrict__ tiles, GemmArgs g) {
@@ -1311,8 +1326,10 @@ __global__ __launch_bounds__(256, S::Waves) void k_thin(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Operands<ST, SPLIT> o(g, t);
   const int i0 = t.i * S::BM, j0 = t.j * S::BN;
+  static_assert(BK == kMuonRound);
   const int rounds = o.depth / BK;
-  const int total = SPLIT ? 3 * rounds : rounds;
+  const int first = ST == kGram ? t.m : 0;
+  const int total = ST == kGram ? t.n : SPLIT ? 3 * rounds : rounds;
   const int mine = (total - wave + 3) / 4;  // total > 0; none for wave >= total
   char* own = lds + wave * kOwn;
   const uint32_t own0 =
@@ -1323,7 +1340,7 @@ __global__ __launch_bounds__(256, S::Waves) void k_thin(
   const Loader<S, kAcross> loader(0, i0, j0, o.prows, o.qrows, o.lp, o.lq);
   const Fetcher<S, kAcross> fetcher(0, 0);
   auto issue = [&](int r, int buf) {
-    const From f = from_round<BK>(o, wave + 4 * r, rounds);
+    const From f = from_round<BK>(o, first + wave + 4 * r, rounds);
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) loader.load(f, own0 + buf * S::RoundBytes, x);
   };
@@ -1379,7 +1396,48 @@ __global__ __launch_bounds__(256, S::Waves) void k_thin(
 #pragma unroll
   for (int w = 0; w < 4; ++w)
     all[0][0] += *reinterpret_cast<const f4*>(lds + w * kOwn + (wave * 64 + lane) * 16);
-  res.finish(g, t, o, all, nullptr);
+  if (ST == kGram && t.flat_off >= 0)  // a part
+    reinterpret_cast<f4*>(g.sums)[t.flat_off * 256 + threadIdx.x] = all[0][0];
+  else
+    res.finish(g, t, o, all, nullptr);
+}
+
+// A's tiles whose sums came in parts: the parts in their order, four chains
+// of them, and to where k_thin's (F = 1) or k_gemm's (F = 2) own go.  A lane
+// has F x F f4's of each part.  8.5 us for 36 tiles of 15 parts (512 x 32000,
+// the parts 17.7), 23 us for 3 of 171 (32 x 1M, the parts 32: a workgroup
+// reads 700 KB alone).
+template <int F, bool SPLIT>
+__global__ __launch_bounds__(256) void k_join(const MuonGemmTile* __restrict__ tiles, GemmArgs g) {
+  const MuonGemmTile t = tile_of(tiles, g);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Operands<kGram, SPLIT> o(g, t);
+  using Res = Result<F, F, F, kGram, SPLIT, u16>;
+  __shared__ __align__(16) char lds[F == 1 ? 16 : 4 * Res::kOut];
+  Res res;
+  res.ask(g, t, o, (t.i * 2 + wave / 2) * 16 * F, (t.j * 2 + wave % 2) * 16 * F);
+  constexpr int N = F * F;
+  const f4* from = reinterpret_cast<const f4*>(g.sums) + t.flat_off * (N * 256) + threadIdx.x;
+  f4 chain[4][N];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int x = 0; x < N; ++x) chain[k][x] = f4{0.f, 0.f, 0.f, 0.f};
+  int p = 0;
+#pragma unroll 2
+  for (; p + 4 <= t.n; p += 4)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < N; ++x) chain[k][x] += from[((p + k) * N + x) * 256];
+  for (; p < t.n; ++p)
+#pragma unroll
+    for (int x = 0; x < N; ++x) chain[0][x] += from[(p * N + x) * 256];
+  f4 all[F][F];
+#pragma unroll
+  for (int x = 0; x < N; ++x)
+    all[x / F][x % F] = (chain[0][x] + chain[1][x]) + (chain[2][x] + chain[3][x]);
+  res.finish(g, t, o, all, F == 1 ? nullptr : lds + wave * Res::kOut);
 }
 
 // `from`: which plane holds X.  Its low parts are replaced in place, by the
@@ -1397,6 +1455,7 @@ GemmArgs gemm_args(const MuonArgs& a, int from) {
   g.al = half(a.w.al);
   g.bh = half(a.w.bh);
   g.bl = half(a.w.bl);
+  g.sums = reinterpret_cast<float*>(a.ws + a.w.sums);
   return g;
 }
 
@@ -1535,9 +1594,18 @@ hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, 
   return sink.launch(fn, dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
-hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, int from, const Sink& sink) {
+hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, const MuonTiles& join, int from,
+                            const Sink& sink) {
   GemmArgs g = gemm_args(a, from);
-  return launch_gemm<kGram, u16>(a.split, t, g, sink);
+  const hipError_t e = launch_gemm<kGram, u16>(a.split, t, g, sink);
+  if (e != hipSuccess || join.n == 0) return e;
+  const MuonGemmTile* tiles = join.tiles;
+  void* p[] = {&tiles, &g};
+  const void* fn = t.shape == 0 ? (a.split ? reinterpret_cast<const void*>(&k_join<1, true>)
+                                           : reinterpret_cast<const void*>(&k_join<1, false>))
+                                : (a.split ? reinterpret_cast<const void*>(&k_join<2, true>)
+                                           : reinterpret_cast<const void*>(&k_join<2, false>));
+  return sink.launch(fn, dim3(static_cast<unsigned>(join.n)), dim3(256), p, 0);
 }
 
 hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,

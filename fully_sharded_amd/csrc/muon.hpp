@@ -58,6 +58,9 @@ struct alignas(64) MuonConvertTile {
 };
 
 // A product's tile.  mat < 0: none.  Bit 30 of mat: more rows than columns.
+// A's tiles of up to kMuonPartTile, which write nothing to the unit, may be a
+// part of the sum: n rounds from round m on, into partial sum flat_off (-1:
+// the whole sum, straight into A); in `join`, n partial sums from flat_off on.
 struct alignas(64) MuonGemmTile {
   int64_t off_x, off_a, flat_off;
   int32_t off_d, i, j, mat;
@@ -65,6 +68,8 @@ struct alignas(64) MuonGemmTile {
   int32_t ldx, lda;
 };
 constexpr int32_t kMuonTall = 1 << 30;
+constexpr int kMuonRound = 64;  // of the sum, loaded at once
+constexpr int kMuonPartTile = 64;
 static_assert(sizeof(MuonConvertTile) == 64 && sizeof(MuonGemmTile) == 64);
 
 // Sides of the products' tiles.
@@ -94,6 +99,7 @@ struct MuonDevice {
   const MuonChunk* norm;
   const MuonConvertTile* convert;
   MuonTiles gram, poly, step;  // the lower triangles of A and of B, X
+  MuonTiles join;              // those of A's tiles that come in parts
   const MuonItem* momentum;   // flat space
   const MuonItem* apply;      // shard space
   const MuonScale* scales;    // per matrix
@@ -104,6 +110,7 @@ struct MuonDevice {
 struct MuonWorkspace {
   int64_t partial, coef, adiag, bdiag;
   int64_t xh[2], xl[2], ah, al, bh, bl;
+  int64_t sums;  // A's partial sums
   int64_t bytes;
 };
 
@@ -125,8 +132,9 @@ struct fsdp_muon {
   std::vector<fsdp::MuonConvertTile> convert;
   // the products' tiles for results in bf16, and for split operands
   struct Tiles {
-    std::vector<fsdp::MuonGemmTile> gram, poly, step;
+    std::vector<fsdp::MuonGemmTile> gram, poly, step, join;
     int gram_shape = 0, poly_shape = 0, step_shape = 0;
+    int64_t n_sums = 0;  // A's partial sums, a tile of fp32 each
   } tiles[2];
   std::vector<fsdp::MuonItem> momentum, apply;
   std::vector<fsdp::MuonScale> scales;
@@ -172,8 +180,9 @@ hipError_t launch_muon_norm(const MuonArgs& a, const MuonChunk* tiles, int64_t n
 hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, int64_t n,
                                const void* update, int dt, double eps, const double (&poly)[3],
                                const Sink& sink);
-// A = X X^T.
-hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, int from, const Sink& sink);
+// A = X X^T; join: the tiles of it that t has in parts (none: no launch).
+hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, const MuonTiles& join, int from,
+                            const Sink& sink);
 // B = b A + c A A.
 hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
                             const double (&poly)[3], const Sink& sink);

@@ -20,7 +20,8 @@ hipError_t launch_muon_convert(const MuonArgs&, const MuonConvertTile*, int64_t,
                                double, const double (&)[3], const Sink&) {
   return hipErrorNoDevice;
 }
-hipError_t launch_muon_gram(const MuonArgs&, const MuonTiles&, int, const Sink&) {
+hipError_t launch_muon_gram(const MuonArgs&, const MuonTiles&, const MuonTiles&, int,
+                            const Sink&) {
   return hipErrorNoDevice;
 }
 hipError_t launch_muon_poly(const MuonArgs&, const MuonTiles&, bool, const double (&)[3],

@@ -23,9 +23,10 @@ static int failures = 0;
 // Every tile of every matrix once, each with its matrix's own numbers; tables
 // that mix empty tiles in keep them behind a die's own.
 static void check_tiles(const fsdp_muon& mu, const std::vector<fsdp::MuonGemmTile>& tiles,
-                        int shape, bool square) {
+                        int shape, bool square, bool parts = false) {
   const int64_t side = fsdp::kMuonTiles[shape];
-  std::set<std::tuple<int, int, int>> seen;
+  std::set<std::tuple<int, int, int, int>> seen;
+  size_t whole = 0;
   bool ended[8] = {};
   for (size_t p = 0; p < tiles.size(); ++p) {
     const fsdp::MuonGemmTile& t = tiles[p];
@@ -39,11 +40,13 @@ static void check_tiles(const fsdp_muon& mu, const std::vector<fsdp::MuonGemmTil
     const fsdp::MuonMat& m = mu.mats[k];
     CHECK(((t.mat & fsdp::kMuonTall) != 0) == (m.rows > m.cols));
     CHECK(t.off_x == m.off_x && t.off_a == m.off_a && t.off_d == m.off_d);
-    CHECK(t.flat_off == m.flat_off && t.mp == m.mp && t.np == m.np && t.m == m.m && t.n == m.n);
+    CHECK(t.mp == m.mp && t.np == m.np);
+    CHECK(parts || (t.flat_off == m.flat_off && t.m == m.m && t.n == m.n));
     CHECK(t.ldx == m.ldx && t.lda == m.lda);
     CHECK(t.i >= 0 && t.j >= 0 && t.i * side < m.mp && t.j * side < (square ? m.mp : m.np));
     CHECK(!square || t.i >= t.j);
-    CHECK(seen.insert({k, t.i, t.j}).second);
+    CHECK(seen.insert({k, t.i, t.j, parts ? t.m : 0}).second);
+    whole += !parts || t.m == 0;  // first parts stand for their tiles
   }
   CHECK(tiles.empty() || tiles.back().mat >= 0);
   size_t want = 0;
@@ -51,8 +54,58 @@ static void check_tiles(const fsdp_muon& mu, const std::vector<fsdp::MuonGemmTil
     const int64_t si = (m.mp + side - 1) / side, sj = (m.np + side - 1) / side;
     want += square ? si * (si + 1) / 2 : si * sj;
   }
-  CHECK(seen.size() == want);
+  CHECK(whole == want);
 }
+
+// A's smaller tiles: the parts of a tile's sum follow each other from its
+// first round to its last, each with a partial sum of its own, which the
+// tile's join reads in that order; a sum in one piece has neither.  A join is
+// worth 64 rounds at least, and parts give every compute unit two at most.
+static int check_parts(const fsdp_muon& mu, const fsdp_muon::Tiles& t, int products) {
+  if (t.gram_shape > 1) {
+    CHECK(t.join.empty() && t.n_sums == 0);
+    check_tiles(mu, t.gram, t.gram_shape, true);
+    return 0;
+  }
+  std::map<std::tuple<int, int, int>, std::map<int, const fsdp::MuonGemmTile*>> tiles;
+  std::map<std::tuple<int, int, int>, const fsdp::MuonGemmTile*> joins;
+  for (const fsdp::MuonGemmTile& g : t.gram)
+    if (g.mat >= 0) CHECK((tiles[{g.mat, g.i, g.j}].insert({g.m, &g}).second));
+  for (const fsdp::MuonGemmTile& g : t.join) CHECK((joins.insert({{g.mat, g.i, g.j}, &g}).second));
+  std::set<int64_t> used;
+  int longest = 0, whole = 0, in_parts = 0;
+  for (const auto& [key, list] : tiles) {
+    const int all = products * (list.begin()->second->np / 64);
+    int at = 0, k = 0;
+    const auto join = joins.find(key);
+    CHECK((join != joins.end()) == (list.size() > 1));
+    for (const auto& [first, g] : list) {
+      CHECK(first == at && g->n > 0);
+      at += g->n;
+      longest = std::max<int>(longest, g->n);
+      if (join == joins.end()) {
+        CHECK(g->flat_off == -1);
+      } else {
+        CHECK(g->flat_off == join->second->flat_off + k && used.insert(g->flat_off).second);
+        CHECK(g->flat_off >= 0 && g->flat_off < t.n_sums);
+      }
+      ++k;
+    }
+    CHECK(at == all);
+    whole = std::max(whole, all);
+    if (join != joins.end()) {
+      CHECK(join->second->n == k);
+      in_parts += k;
+    }
+  }
+  CHECK(static_cast<int64_t>(used.size()) == t.n_sums && in_parts == t.n_sums);
+  CHECK(t.n_sums == 0 || whole >= longest + 64);
+  CHECK(in_parts <= 512 + static_cast<int>(tiles.size()));
+  check_tiles(mu, t.gram, t.gram_shape, true, true);
+  return t.n_sums > 0;
+}
+
+static int parted = 0;
 
 static void check_unit(const fsdp_muon& mu) {
   int64_t x = 0, a = 0, d = 0;
@@ -69,7 +122,7 @@ static void check_unit(const fsdp_muon& mu) {
   }
   CHECK(mu.nx == x && mu.na == a && mu.nd == d);
   for (const auto& t : mu.tiles) {
-    check_tiles(mu, t.gram, t.gram_shape, true);
+    parted += check_parts(mu, t, &t == mu.tiles ? 1 : 3);
     check_tiles(mu, t.poly, t.poly_shape, true);
     check_tiles(mu, t.step, t.step_shape, false);
   }
@@ -106,7 +159,7 @@ static void check_unit(const fsdp_muon& mu) {
         {w.adiag, d * 4},              {w.bdiag, d * 4},
         {w.xh[0], 2 * x},              {w.xh[1], 2 * x},
         {w.xl[0], lo},                 {w.ah, 2 * a},
-        {w.bh, 2 * a}};
+        {w.bh, 2 * a},                 {w.sums, mu.tiles[split].n_sums * (mu.tiles[split].gram_shape ? 16384 : 4096)}};
     if (split) {
       parts.push_back({w.xl[1], lo});
       parts.push_back({w.al, 2 * a});
@@ -128,12 +181,13 @@ int main(int argc, char** argv) {
   for (int u = 0; u < n; ++u) {
     const int k = pick(1, u % 10 == 0 ? 60 : 8);
     const int most = u % 7 == 0 ? 2500 : 300;
+    const int wide = u % 11 == 0 ? 100 : 1;  // second dimensions
     std::vector<int32_t> nd;
     std::vector<int64_t> dims;
     for (int p = 0; p < k; ++p) {
       const int dd = pick(1, 3);
       nd.push_back(dd);
-      for (int q = 0; q < dd; ++q) dims.push_back(q < 2 ? pick(1, most) : pick(1, 4));
+      for (int q = 0; q < dd; ++q) dims.push_back(q < 2 ? pick(1, most) * (q ? wide : 1) : pick(1, 4));
     }
     fsdp_plan* plan = nullptr;
     CHECK(fsdp_plan_layout(k, nd.data(), dims.data(), pick(1, 9), pick(0, 1), &plan) == FSDP_OK);
@@ -189,6 +243,7 @@ int main(int argc, char** argv) {
                                step, nullptr) == FSDP_ERR_INVALID_ARG);
     fsdp_muon_destroy(mu);
   }
+  CHECK(n < 100 || parted >= 10);
   std::printf("checked %d random units, failures %d\n", n, failures);
   return failures != 0;
 }

@@ -204,6 +204,18 @@ def test_one_matrix(r, c, udt, odt, kind):
     check(got, u, odt, what=kind)
 
 
+@pytest.mark.parametrize("udt,odt", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("shapes", [[(3, 9001)], [(20000, 70)], [(130, 12345)], [(25000, 300)], [(512, 29200), (60, 200)],
+                                    [(40, 300), (17,), (64, 30000), (90, 80)]])
+def test_long_sums_in_parts(shapes, udt, odt):
+    """A's few tiles have their sums cut into parts, beside others that do not."""
+    rng = np.random.default_rng(sum(s[0] for s in shapes))
+    us = [rng.standard_normal(s) for s in shapes]
+    for off in (0, 1):
+        for u, got in run_ortho(shapes, us, udt, odt, off=off):
+            check(got, u, odt, what=f"{udt} {odt}")
+
+
 @pytest.mark.parametrize("udt,odt,in_place", [("bf16", "bf16", False), ("bf16", "bf16", True),
                                               ("f32", "f32", True), ("f32", "bf16", False)])
 def test_unit_of_many_matrices(udt, odt, in_place):
