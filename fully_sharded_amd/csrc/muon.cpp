@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 #include <new>
 
 #include "checks.hpp"
@@ -417,19 +418,20 @@ fsdp_status fsdp_muon::device(bool split, fsdp::MuonDevice* out) const {
   std::lock_guard<std::mutex> lock(mu_);
   auto it = dev_.find(dev);
   if (it == dev_.end()) {
+    // one copy: a small unit's tables are 13 of a few KB
+    std::vector<char> all(static_cast<size_t>(bytes));
+    for (int k = 0; k < kParts; ++k)
+      if (size[k]) std::memcpy(all.data() + at[k], from[k], static_cast<size_t>(size[k]));
     void* mem = nullptr;
     if (hipMalloc(&mem, static_cast<size_t>(bytes)) != hipSuccess) {
       (void)hipGetLastError();
       return FSDP_ERR_OUT_OF_MEMORY;
     }
-    for (int k = 0; k < kParts; ++k)
-      if (size[k] && hipMemcpy(static_cast<char*>(mem) + at[k], from[k],
-                               static_cast<size_t>(size[k]),
-                               hipMemcpyHostToDevice) != hipSuccess) {
-        (void)hipGetLastError();
-        (void)hipFree(mem);
-        return FSDP_ERR_HIP;
-      }
+    if (hipMemcpy(mem, all.data(), all.size(), hipMemcpyHostToDevice) != hipSuccess) {
+      (void)hipGetLastError();
+      (void)hipFree(mem);
+      return FSDP_ERR_HIP;
+    }
     it = dev_.emplace(dev, mem).first;
   }
   const char* b = static_cast<const char*>(it->second);
