@@ -417,6 +417,39 @@ def test_captured_and_replayed():
         assert_bitexact(to_host(o), to_host(o2), f"ortho, replay {t}")
 
 
+@pytest.mark.parametrize("odt", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(20000, 70), (512, 29200)])
+def test_sums_in_parts_captured_and_on_two_streams(shape, odt):
+    rng = np.random.default_rng(24)
+    plan = F.Plan([shape], 1, "flat")
+    mu = F.Muon(plan)
+    mu.prepare()
+    dt = TORCH[odt]
+    sets = [(torch.zeros(plan.T, dtype=dt, device=DEV), torch.zeros(plan.T, dtype=dt, device=DEV),
+             mu.workspace(dt, dt)) for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    s = torch.cuda.Stream()
+    calls = [F.bind_orthogonalize(mu, F.MUON, *x) for x in sets]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        calls[0]()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for t in range(3):
+        u = to_dev(values(rng, plan.T, 1e-3, odt))
+        for x in sets:
+            x[0].copy_(u)
+            x[2].fill_(0xff)
+        torch.cuda.synchronize()
+        graph.replay()
+        for c, st in zip(calls[1:], streams):
+            c(st)
+        torch.cuda.synchronize()
+        want = to_host(sets[1][1])
+        assert np.isfinite(M.widen(want)).all()
+        assert_bitexact(to_host(sets[0][1]), want, f"replay {t}")
+        assert_bitexact(to_host(sets[2][1]), want, f"stream {t}")
+
+
 def test_other_devices_and_bad_workspaces_are_refused():
     plan = F.Plan([(8, 8)], 1, "flat")
     mu = F.Muon(plan)
