@@ -356,7 +356,7 @@ MuonWorkspace muon_workspace(const fsdp_muon* mu, bool split) {
   };
   const int64_t x = mu->nx * 2, a = mu->na * 2;
   w.partial = take(mu->n_partial * 8);
-  w.coef = take(static_cast<int64_t>(mu->mats.size()) * 16);
+  w.coef = take(static_cast<int64_t>(mu->mats.size() * kMuonSteps * sizeof(MuonCoef)));
   w.adiag = take(mu->nd * 4);
   w.bdiag = take(mu->nd * 4);
   w.xh[0] = take(x);
@@ -467,7 +467,7 @@ fsdp_status check(const fsdp_muon_hparams* hp) {
     if (!std::isfinite(x)) return FSDP_ERR_INVALID_ARG;
   if (hp->lr < 0 || !(hp->momentum >= 0 && hp->momentum < 1) || hp->weight_decay < 0 ||
       !(hp->eps >= 1e-300) || std::fabs(hp->ns_a) > 16 || std::fabs(hp->ns_b) > 16 ||
-      std::fabs(hp->ns_c) > 16 || hp->ns_steps < 1 || hp->ns_steps > 16 ||
+      std::fabs(hp->ns_c) > 16 || hp->ns_steps < 1 || hp->ns_steps > fsdp::kMuonSteps ||
       (hp->nesterov != 0 && hp->nesterov != 1) || hp->scale < FSDP_MUON_SCALE_NONE ||
       hp->scale > FSDP_MUON_SCALE_RMS)
     return FSDP_ERR_INVALID_ARG;
@@ -511,6 +511,7 @@ fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
   a.split = ortho_dt == FSDP_F32;
   a.low = a.split || update_dt == FSDP_F32;
   a.w = fsdp::muon_workspace(mu, a.split);
+  a.steps = hp->ns_steps;
   const double poly[3] = {hp->ns_a, hp->ns_b, hp->ns_c};
   hipError_t e = fsdp::launch_muon_norm(a, d.norm, static_cast<int64_t>(mu->norm.size()), update,
                                         update_dt, sink);
@@ -518,6 +519,7 @@ fsdp_status orthogonalize(const fsdp_muon* mu, const fsdp::MuonDevice& d,
     e = fsdp::launch_muon_convert(a, d.convert, static_cast<int64_t>(mu->convert.size()), update,
                                   update_dt, hp->eps, poly, sink);
   for (int s = 0; s < hp->ns_steps && e == hipSuccess; ++s) {
+    a.step = s;
     e = fsdp::launch_muon_gram(a, d.gram, d.join, s & 1, sink);
     if (e == hipSuccess) e = fsdp::launch_muon_poly(a, d.poly, s == 0, poly, sink);
     if (e == hipSuccess)

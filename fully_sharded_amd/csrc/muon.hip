@@ -44,7 +44,9 @@ constexpr int kThreads = 256;
 // Planes hold X * kSx and A * kSa, B * kSa: |X| < 2 before the first step
 // (its norm is in [1, 2)) and about 1.2 after it, |A| < 4, |B| < 12, each
 // at least 8 times below fp16's largest value, and an entry 2^-16 of the
-// largest still keeps all its bits.
+// largest still keeps all its bits.  Where X itself is small, as for an
+// update far below eps, the planes hold X 2^-q with a q per matrix and step
+// (k_convert): the same sizes, and the same bits kept.
 constexpr float kSx = 4096.f;
 constexpr float kSa = 1024.f;
 
@@ -304,7 +306,8 @@ __device__ __forceinline__ f4 unpack_bf8(uint32_t v) {
 struct ConvertArgs {
   const MuonConvertTile* tiles;
   const double* partial;
-  float* coef;  // per matrix: a f, b f^3, c f^5
+  MuonCoef* coef;  // per matrix and step
+  int steps;
   _Float16* xh;
   void* xl;    // null: the low parts are not wanted
   bool bytes;  // they are wanted in bf8
@@ -333,9 +336,18 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
 }
 
 // 64 x 64 tiles of the update into X, transposed where the parameter has
-// more rows than columns.  With |U| + eps = N, the planes get U 2^-e with
-// 2^e <= N < 2^(e+1): exact for bf16 updates.  What is left, f = 2^e / N,
-// goes into the first step's coefficients: A is then A f^-2 and X is X f^-1.
+// more rows than columns.  The planes get U 2^-e with 2^e <= |U| < 2^(e+1):
+// exact for bf16 updates, but for entries below 2^-29 of |U|.  What is left,
+// f = 2^e / N with N = |U| + eps, goes into the first step's coefficients: A
+// is then A f^-2 and X is X f^-1.  Where eps is not small beside |U|, X is:
+// at fixed scales an |X| of 1e-8 was 13-51% off for want of bits in fp16.  So
+// the planes hold X 2^-q after a step, 2^q the power of two below what X's
+// singular values can be, 1 at most: s = |U| / N before the first step, and
+// |a| s + |b| s^3 + |c| s^5 after each.  P = X 2^-q steps by
+//   P' = a 2^(q-q') P + b 2^(3q-q') P^3 + c 2^(5q-q') P^5
+// where no coefficient is above 2 for q' < 0; at q = q' = 0, as everywhere
+// that eps does not matter, these are a, b and c.  q stops at -400: X is then
+// 0 in fp32, and no 16 steps of coefficients up to 16 make it anything else.
 // A lane has 8 adjacent entries of each of two rows.  196 us for 218M bf16
 // elements (4.5 TB/s read and written).
 template <typename T>
@@ -361,16 +373,35 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
   }
   double s = 0;
   for (int k = threadIdx.x; k < t.norm_count; k += kThreads) s += a.partial[t.norm_first + k];
-  const double norm = sqrt(block_sum(s)) + a.eps;
-  const int e = ilogb(norm);
+  const double mass = sqrt(block_sum(s)), norm = mass + a.eps;
+  const bool bad = !(norm < INFINITY), some = !bad && mass > 0;
+  const int e = some ? ilogb(mass) : 0;
   const double scale = ldexp(static_cast<double>(kSx), -e);
-  if (t.i == 0 && t.j == 0 && threadIdx.x == 0) {
-    const double f = ldexp(1.0, e) / norm;
-    const bool bad = !(norm < INFINITY);
-    float* k = a.coef + 4 * t.mat;
-    k[0] = bad ? NAN : static_cast<float>(a.a * f);
-    k[1] = bad ? NAN : static_cast<float>(a.b * f * f * f);
-    k[2] = bad ? NAN : static_cast<float>(a.c * f * f * f * f * f);
+  if (t.i == 0 && t.j == 0 && threadIdx.x < a.steps) {
+    // lane n: of step n, which goes from q to `to`
+    const bool grows = fabs(a.a) + fabs(a.b) + fabs(a.c) >= 1;
+    double most = some ? mass / norm : 0;  // of X's singular values
+    int q = 0, to = 0;
+    for (int n = 0; n <= static_cast<int>(threadIdx.x) && !bad; ++n) {
+      q = to;
+      if (grows && most >= 1) {  // and so from here on
+        to = 0;
+        break;
+      }
+      const double most2 = most * most;
+      most *= fabs(a.a) + most2 * (fabs(a.b) + most2 * fabs(a.c));
+      to = most > 0 ? max(min(ilogb(most), 0), -400) : -400;
+      most = min(most, 16.0);
+    }
+    MuonCoef k{1.f, 1.f, 1.f, q - to, 3 * q - to, 5 * q - to, to, 0};
+    if (threadIdx.x == 0) {
+      k.ea = k.eb = k.ec = 0;
+      const double f = some ? ldexp(1.0, e) / norm : 0;
+      k.a = bad ? NAN : static_cast<float>(ldexp(a.a * f, -to));
+      k.b = bad ? NAN : static_cast<float>(ldexp(a.b * f * f * f, -to));
+      k.c = bad ? NAN : static_cast<float>(ldexp(a.c * f * f * f * f * f, -to));
+    }
+    a.coef[t.mat * kMuonSteps + threadIdx.x] = k;
   }
   // where a lane's entries go: rows of X, across them in a tall parameter
   const int64_t to0 = t.tall ? (c0 + lr) * t.ldx + r0 + lc : (r0 + lr) * t.ldx + c0 + lc;
@@ -434,8 +465,8 @@ __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ upda
 
 // ---------------------------------------------------------------- products
 struct GemmArgs {
-  const float* coef;  // non-null: the first step's coefficients, per matrix
-  float a, b, c;      // the other steps'
+  const MuonCoef* coef;  // per matrix and step, from this step's first on
+  float a, b, c;         // the step's; the first's are in coef, these 1
   float *adiag, *bdiag;  // the diagonals of A and B
   // X of this step and of the next; the low parts in bf8 or, where they are
   // operands, in fp16 (xl null in the first step of a bf16 update: zeros)
@@ -806,7 +837,8 @@ struct Result {
 
   int rb, cb, lr, lk;
   u4 own_h[AHEAD][kSets], own_l[AHEAD][kSets];  // kDirect: in the first two words
-  float ca, cb1, cc, di[FM];
+  float di[FM];
+  MuonCoef coef;
   f4 dj[FN];
 
   __device__ __forceinline__ void own_rows(const GemmArgs& g, const MuonGemmTile& t,
@@ -915,15 +947,8 @@ struct Result {
     lk = lane >> 4;
     rb = rb_;
     cb = cb_;
-    ca = g.a;
-    cb1 = g.b;
-    cc = g.c;
-    if (g.coef) {
-      const int mat = t.mat & ~kMuonTall;
-      ca = g.coef[4 * mat];
-      cb1 = g.coef[4 * mat + 1];
-      cc = g.coef[4 * mat + 2];
-    }
+    // (used in finish: a product here would be waited for before the sums)
+    if constexpr (ST != kGram) coef = g.coef[(t.mat & ~kMuonTall) * kMuonSteps];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       dj[j] = f4{0.f, 0.f, 0.f, 0.f};
@@ -986,6 +1011,12 @@ struct Result {
                                          char* lds) {
     if (rb >= o.prows || cb >= o.qrows) return;
     const int lane = threadIdx.x & 63;
+    float ca = 0.f, cb1 = 0.f, cc = 0.f;
+    if constexpr (ST != kGram) {
+      ca = __builtin_amdgcn_ldexpf(g.a * coef.a, coef.ea);
+      cb1 = __builtin_amdgcn_ldexpf(g.b * coef.b, coef.eb);
+      cc = __builtin_amdgcn_ldexpf(g.c * coef.c, coef.ec);
+    }
     char* rows16 = lds;
     char* image = rows16 + kRows;
     constexpr int kImageLd = (TM + 8) * 2;
@@ -1043,7 +1074,8 @@ struct Result {
             x[r] = fmaf(fmaf(cc, di[i] + dj[j][r], cb1), own, cc * (sum * (1.f / kSa)));
           } else {
             x[r] = fmaf(ca + di[i], own, sum * (1.f / kSa));
-            if (ST == kLast) x[r] *= 1.f / kSx;
+            static_assert(kSx == 4096.f);
+            if (ST == kLast) x[r] = __builtin_amdgcn_ldexpf(x[r], coef.q - 12);
           }
           if (kMirror && row == col + r) {
             if (ST == kGram)
@@ -1445,6 +1477,7 @@ __global__ __launch_bounds__(256) void k_join(const MuonGemmTile* __restrict__ t
 GemmArgs gemm_args(const MuonArgs& a, int from) {
   auto half = [&](int64_t off) { return reinterpret_cast<_Float16*>(a.ws + off); };
   GemmArgs g{};
+  g.coef = reinterpret_cast<const MuonCoef*>(a.ws + a.w.coef) + a.step;
   g.adiag = reinterpret_cast<float*>(a.ws + a.w.adiag);
   g.bdiag = reinterpret_cast<float*>(a.ws + a.w.bdiag);
   g.xh = half(a.w.xh[from]);
@@ -1580,7 +1613,8 @@ hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, 
   ConvertArgs c{};
   c.tiles = tiles;
   c.partial = reinterpret_cast<const double*>(a.ws + a.w.partial);
-  c.coef = reinterpret_cast<float*>(a.ws + a.w.coef);
+  c.coef = reinterpret_cast<MuonCoef*>(a.ws + a.w.coef);
+  c.steps = a.steps;
   c.xh = half(a.w.xh[0]);
   c.xl = a.low ? a.ws + a.w.xl[0] : nullptr;
   c.bytes = !a.split;
@@ -1611,9 +1645,8 @@ hipError_t launch_muon_gram(const MuonArgs& a, const MuonTiles& t, const MuonTil
 hipError_t launch_muon_poly(const MuonArgs& a, const MuonTiles& t, bool first,
                             const double (&poly)[3], const Sink& sink) {
   GemmArgs g = gemm_args(a, 0);
-  g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
-  g.b = static_cast<float>(poly[1]);
-  g.c = static_cast<float>(poly[2]);
+  g.b = first ? 1.f : static_cast<float>(poly[1]);
+  g.c = first ? 1.f : static_cast<float>(poly[2]);
   return launch_gemm<kPoly, u16>(a.split, t, g, sink);
 }
 
@@ -1621,8 +1654,7 @@ hipError_t launch_muon_step(const MuonArgs& a, const MuonTiles& t, int from, boo
                             bool last, const double (&poly)[3], void* ortho, int ortho_dt,
                             const Sink& sink) {
   GemmArgs g = gemm_args(a, from);
-  g.coef = first ? reinterpret_cast<const float*>(a.ws + a.w.coef) : nullptr;
-  g.a = static_cast<float>(poly[0]);
+  g.a = first ? 1.f : static_cast<float>(poly[0]);
   if (first && !a.low) g.xl = nullptr;
   g.ortho = ortho;
   if (!last) return launch_gemm<kStep, u16>(a.split, t, g, sink);

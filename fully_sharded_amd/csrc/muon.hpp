@@ -89,6 +89,16 @@ struct MuonItem {
   int32_t len, mat;
 };
 
+// One step's numbers for one matrix, made with the planes of its update.  Its
+// coefficients are a 2^ea, b 2^eb and c 2^ec, with a, b and c from here in the
+// first step and the optimiser's in the others (from here: 1); q: the planes
+// hold X 2^-q after it.
+struct alignas(32) MuonCoef {
+  float a, b, c;
+  int32_t ea, eb, ec, q, unused;
+};
+constexpr int kMuonSteps = 16;  // the most; a matrix has that many MuonCoef
+
 // A matrix's scales.
 struct MuonScale {
   double aspect, rms;
@@ -120,6 +130,7 @@ struct MuonArgs {
   MuonWorkspace w;
   bool split;
   bool low;  // the update has low parts: fp32, or split operands
+  int32_t steps, step;  // how many, and the one that is launched
 };
 
 }  // namespace fsdp
@@ -175,8 +186,8 @@ hipError_t launch_muon_apply(const MuonItem* items, int64_t n, const MuonScale* 
 
 hipError_t launch_muon_norm(const MuonArgs& a, const MuonChunk* tiles, int64_t n,
                             const void* update, int dt, const Sink& sink);
-// The update into the planes of X, scaled by a power of
-// two, and the first step's coefficients with what is left of the norm.
+// The update into the planes of X, scaled by a power of two, the first step's
+// coefficients with what is left of the norm, and all steps' exponents.
 hipError_t launch_muon_convert(const MuonArgs& a, const MuonConvertTile* tiles, int64_t n,
                                const void* update, int dt, double eps, const double (&poly)[3],
                                const Sink& sink);

@@ -486,6 +486,8 @@ fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
  *   within about the rounding to bf16 of the exact one.  With FSDP_F32
  *   every operand is kept as two fp16 parts and each product is the sum of
  *   three: an error near that of fp32 products, at three times the work.
+ *   Both hold however small |U|_F is beside eps: the operands' powers of two
+ *   follow X, per matrix and step.
  *   The steps' intermediate values must stay below 16 (X) and 64 (A and
  *   b A + c A A): so they do for coefficients that map [0, 1.3] into
  *   itself.  A matrix of zeros gives zeros.  One that holds an infinity

@@ -3,6 +3,8 @@ the library's contract rounds.  Test infrastructure only."""
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 from oracle import fsdp_oracle as O
@@ -90,6 +92,18 @@ def orthogonalize(u, steps=5, eps=1e-7, poly=POLY):
     return x.T if t else x
 
 
+def plane_exponents(sigma, steps, poly):
+    """The exponents q of the steps' results, whose planes hold X 2^-q: X's
+    singular values are at most sigma before the first step and at most
+    |a| s + |b| s^3 + |c| s^5 after one that began with at most s."""
+    out = []
+    for _ in range(steps):
+        bound = sum(abs(k) * sigma ** p for k, p in zip(poly, (1, 3, 5)))
+        out.append(max(min(math.frexp(bound)[1] - 1 if bound > 0 else -400, 0), -400))
+        sigma = min(bound, 16.0)
+    return out
+
+
 def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
     """The definition with the library's documented precision: operands of
     11 bits (split: of 22) under power-of-two scales, fp32 sums, the residual
@@ -110,15 +124,20 @@ def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
         r = p[0] @ q[0]
         return r + (p[0] @ q[1] + p[1] @ q[0]) if split else r
 
-    norm = np.sqrt((u.astype(np.float64) ** 2).sum()) + eps
-    e = int(np.floor(np.log2(norm)))
-    f = 2.0 ** e / norm
+    mass = float(np.sqrt((u.astype(np.float64) ** 2).sum()))
+    norm = mass + eps
+    e = math.frexp(mass)[1] - 1 if mass > 0 else 0
+    f = math.ldexp(1.0, e) / norm if mass > 0 else 0.0
+    exps = plane_exponents(mass / norm, steps, poly)
     x = (u.astype(np.float64) * 2.0 ** -e).astype(f32)
     t = x.shape[0] > x.shape[1]
     x = np.ascontiguousarray(x.T if t else x)
     for s in range(steps):
-        a, b, c = [f32(k) for k in ((poly[0] * f, poly[1] * f ** 3, poly[2] * f ** 5)
-                                    if s == 0 else poly)]
+        if s == 0:
+            scales = [f ** p * 2.0 ** -exps[0] for p in (1, 3, 5)]
+        else:
+            scales = [2.0 ** (p * exps[s - 1] - exps[s]) for p in (1, 3, 5)]
+        a, b, c = [f32(k * z) for k, z in zip(poly, scales)]
         x = parts(x, 4096)
         g = prod(x, (x[0].T, x[1].T))
         d = np.diag(g).copy()
@@ -129,4 +148,5 @@ def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
         np.fill_diagonal(y, 0)
         y = parts(y, 1024)
         x = (a + d)[:, None] * (x[0] + x[1]) + prod(y, x)
+    x = (x.astype(np.float64) * 2.0 ** exps[-1]).astype(f32)
     return x.T if t else x
