@@ -1,0 +1,59 @@
+"""Which tiles the products of a unit get, and how many parts A's sums come in
+(no GPU): the rules that choose between the kernels' forms."""
+
+import os
+import subprocess
+from collections import namedtuple
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+CSRC = os.path.join(ROOT, "fully_sharded_amd", "csrc")
+SOURCES = [os.path.join(CSRC, f) for f in ("plan.cpp", "abi.cpp", "graph.cpp", "muon.cpp")] + \
+    [os.path.join(ROOT, "tests", "c", f)
+     for f in ("launch_stub.cpp", "muon_launch_stub.cpp", "muon_tables.cpp")]
+Choice = namedtuple("Choice", "gram poly step longest parts")
+
+
+@pytest.fixture(scope="module")
+def choices(tmp_path_factory):
+    """f([(rows, columns), ...]) -> the Choice for bf16 results, for fp32 ones."""
+    if not os.path.exists(HIPCC):
+        pytest.skip("no hipcc")
+    exe = str(tmp_path_factory.mktemp("tables") / "muon_tables")
+    subprocess.run([HIPCC, "-x", "hip", "--offload-arch=gfx950", "-O1", "-std=c++17", "-I",
+                    os.path.join(ROOT, "include"), "-I", CSRC, *SOURCES, "-o", exe,
+                    "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib"],
+                   check=True, capture_output=True)
+
+    def f(shapes):
+        out = subprocess.run([exe], input=" ".join(f"{r} {c}" for r, c in shapes) + "\n",
+                             capture_output=True, text=True, check=True, timeout=120).stdout
+        v = [int(x) for x in out.split()]
+        return Choice(*v[:5]), Choice(*v[5:])
+    return f
+
+
+LONG = 1 << 20
+
+
+@pytest.mark.parametrize("shapes", [
+    [(64, LONG), (1024, 1024)], [(32, LONG), (1024, 1024)], [(LONG, 40), (700, 700), (700, 900)],
+    [(64, LONG // 2), (64, LONG // 2)] + [(512, 512)] * 2, [(100, 400000), (900, 900)]])
+def test_a_long_matrix_beside_square_ones(choices, shapes):
+    """A tile's parts are added up by one workgroup of 64 x 64 tiles, or three
+    and more of 32 x 32: at most 32 parts for the larger ones, whatever else is
+    in the unit."""
+    for c in choices(shapes):
+        assert c.gram == 32 or c.parts <= 32, c
+
+
+@pytest.mark.parametrize("shapes,gram,parts", [
+    ([(512, 29200)], 64, 15), ([(512, 32000)], 64, 16), ([(1024, 32000)], 64, 4),
+    ([(32, LONG)], 32, 171), ([(64, LONG)], 32, 171), ([(512, 512)], 32, 1)])
+def test_matrices_of_one_kind(choices, shapes, gram, parts):
+    """Choices that were measured, each with its parts (two per compute unit
+    at most, 32 rounds or more)."""
+    bf16, _ = choices(shapes)
+    assert bf16.gram == gram and bf16.parts <= parts and (bf16.parts > 1) == (parts > 1), bf16
