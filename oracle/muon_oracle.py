@@ -104,11 +104,14 @@ def plane_exponents(sigma, steps, poly):
     return out
 
 
-def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
+def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False, diagonals=True,
+                          low=True):
     """The definition with the library's documented precision: operands of
     11 bits (split: of 22) under power-of-two scales, fp32 sums, the residual
     of 14 bits (split: of 22) and the diagonals of A and B in fp32.  What it is off the definition by
-    is what the kernels may be off by."""
+    is what the kernels may be off by.  Without diagonals or low, those of A and
+    B are in the planes, or the residual has 11 bits: what a kernel that lost
+    them would compute."""
     f32 = np.float32
 
     def parts(x, s):
@@ -139,13 +142,16 @@ def orthogonalize_rounded(u, steps=5, eps=1e-7, poly=POLY, split=False):
             scales = [2.0 ** (p * exps[s - 1] - exps[s]) for p in (1, 3, 5)]
         a, b, c = [f32(k * z) for k, z in zip(poly, scales)]
         x = parts(x, 4096)
+        if not low:
+            x = (x[0], np.zeros_like(x[1]))
         g = prod(x, (x[0].T, x[1].T))
-        d = np.diag(g).copy()
+        d = np.diag(g).copy() if diagonals else np.zeros(len(g), f32)
         g = parts(g - np.diag(d), 1024)
         own = g[0] + g[1] if split else g[0]
         y = (b + c * (d[:, None] + d[None])) * own + c * prod(g, g)
-        d = d * (b + c * d) + np.diag(y)
-        np.fill_diagonal(y, 0)
+        if diagonals:
+            d = d * (b + c * d) + np.diag(y)
+            np.fill_diagonal(y, 0)
         y = parts(y, 1024)
         x = (a + d)[:, None] * (x[0] + x[1]) + prod(y, x)
     x = (x.astype(np.float64) * 2.0 ** exps[-1]).astype(f32)

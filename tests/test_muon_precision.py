@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 from oracle import muon_oracle as M
+from tests import muon_check as C
 
 
 @pytest.mark.parametrize("split", [False, True])
@@ -41,3 +42,40 @@ def test_steps_that_shrink_the_update():
         off = np.linalg.norm(got - want) / np.linalg.norm(want)
         assert off < 16 * (4 * 2.0 ** -23 if split else 2.0 ** -14), off
         assert (M.orthogonalize_rounded(u, 8, poly=(0.0, 1.0, 0.0), split=split) == 0).all()
+
+
+SIDES = [(63, 64), (65, 191), (333, 100), (129, 129), (257, 255), (40, 1025), (320, 960)]
+
+
+def rounded(u, dtype, **what):
+    return M.cast(M.orthogonalize_rounded(u, split=dtype == "f32", **what).astype(np.float32),
+                  dtype)
+
+
+@pytest.mark.parametrize("r,c", SIDES)
+def test_the_check_takes_results_of_the_documented_precision(r, c):
+    """Rows and columns in another order and the matrix half as large again:
+    the same value with other roundings."""
+    for kind in ("white", "low", "steep"):
+        rng = np.random.default_rng(r * 1000 + c)
+        u = M.widen(M.cast((C.spectrum(rng, r, c, kind) * 1e-3).astype(np.float32), "bf16"))
+        want = M.orthogonalize(u)
+        p, q = rng.permutation(r), rng.permutation(c)
+        for dtype in ("bf16", "f32"):
+            off = C.rms(M.orthogonalize_rounded(u, split=dtype == "f32") - want)
+            other = rounded(u[p][:, q] * np.float32(1.5), dtype)
+            C.check(other, M.orthogonalize(u[p][:, q] * np.float32(1.5)), off, dtype, kind)
+
+
+@pytest.mark.parametrize("r,c", SIDES)
+def test_the_check_refuses_lost_diagonals_and_low_parts(r, c):
+    """The diagonals of A and B rounded with their planes, and the residual a
+    X in 11 bits, in the spectra where each matters."""
+    for kind, lost, dtypes in (("white", "diagonals", ("bf16",)), ("low", "low", ("bf16", "f32"))):
+        rng = np.random.default_rng(r * 1000 + c)
+        u = M.widen(M.cast((C.spectrum(rng, r, c, kind) * 1e-3).astype(np.float32), "bf16"))
+        want = M.orthogonalize(u)
+        for dtype in dtypes:
+            off = C.rms(M.orthogonalize_rounded(u, split=dtype == "f32") - want)
+            with pytest.raises(AssertionError):
+                C.check(rounded(u, dtype, **{lost: False}), want, off, dtype, kind)
