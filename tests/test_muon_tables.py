@@ -7,6 +7,8 @@ from collections import namedtuple
 
 import pytest
 
+from tests.muon_units import UNITS
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CSRC = os.path.join(ROOT, "fully_sharded_amd", "csrc")
@@ -57,3 +59,18 @@ def test_matrices_of_one_kind(choices, shapes, gram, parts):
     at most, 32 rounds or more)."""
     bf16, _ = choices(shapes)
     assert bf16.gram == gram and bf16.parts <= parts and (bf16.parts > 1) == (parts > 1), bf16
+
+
+@pytest.mark.parametrize("name", UNITS)
+def test_units_that_take_each_tile(choices, name):
+    """The units by which the kernels of every tile are tested get those tiles."""
+    shapes, bf16, f32 = UNITS[name]
+    got = choices(shapes)
+    assert got[0][:3] == bf16 and got[1][:3] == f32
+    assert got[0].parts <= 3
+
+
+def test_every_tile_of_every_product_is_in_some_unit():
+    for k in range(3):
+        assert {u[1][k] for u in UNITS.values()} == {64, 128, 256}
+        assert {u[2][k] for u in UNITS.values()} == {64, 128}
