@@ -513,19 +513,19 @@ __device__ __forceinline__ int place_across(int r, int c) {
 }
 
 // 16 bytes per lane from global memory to LDS at a wave-uniform address, lane
-// after lane.  An asm statement (it writes no register): of the builtin the
-// compiler waits for all loads under way before every transposing LDS read,
-// which it cannot tell from a read of the bytes being loaded.  Waited for by
+// after lane.  An asm statement (it writes no register; the address is an
+// operand in M0, so that the compiler knows what is there): of the builtin it
+// waits for all loads under way before every transposing LDS read, which it
+// cannot tell from a read of the bytes being loaded.  Waited for by
 // wait_and_meet.
 __device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
-               "s"(__builtin_amdgcn_readfirstlane(to))
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from),
+               "{m0}"(__builtin_amdgcn_readfirstlane(to))
                : "memory");
 }
 
-// Wait until at most N of this wave's global accesses are under way and all
-// its LDS reads are done (the builtin, not an asm statement: the compiler
-// counts on from it), then for the other waves.
+// Wait until all of this wave's LDS reads are done (the builtin, not an asm
+// statement: the compiler counts on from it).
 __device__ __forceinline__ void wait_lds() {
   __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
 }
@@ -539,6 +539,7 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
+// The same and for all its LDS reads, then for the other waves.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
   static_assert(N < 64);
