@@ -220,7 +220,6 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     t.off_x = mu->nx;
     t.off_a = mu->na;
     t.off_d = mu->nd;
-    t.index = p;
     mu->nx += int64_t(t.mp) * t.ldx;
     mu->na += int64_t(t.mp) * t.lda;
     mu->nd += t.mp;

@@ -29,7 +29,6 @@ struct MuonMat {
   int32_t m, n, mp, np;
   int32_t ldx, lda;
   int32_t tall;  // rows > cols
-  int32_t index;  // of the parameter in the plan
 };
 
 constexpr int kMuonPad = 64;
