@@ -89,10 +89,11 @@ class Muon:
     def workspace_bytes(self, update_dtype=torch.bfloat16, ortho_dtype=torch.bfloat16):
         """(bytes of fsdp_orthogonalize's workspace, bytes of
         fsdp_muon_shard_step's)."""
-        code = {torch.float32: _b.F32, torch.bfloat16: _b.BF16}
+        def code(dtype):
+            return _dtype_code(torch.empty(0, dtype=dtype))
         one, step = ctypes.c_int64(), ctypes.c_int64()
         _check("fsdp_muon_workspace",
-               lib().fsdp_muon_workspace(self._h, code[update_dtype], code[ortho_dtype],
+               lib().fsdp_muon_workspace(self._h, code(update_dtype), code(ortho_dtype),
                                          ctypes.byref(one), ctypes.byref(step)))
         return one.value, step.value
 

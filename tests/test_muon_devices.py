@@ -56,3 +56,18 @@ def test_a_stream_of_another_device_is_refused(current):
             go((None,), s)
     with pytest.raises(ValueError, match="stream"):
         go((None,), stream(0))
+
+
+def test_workspace_types_are_those_of_the_tensors():
+    """bf16 bits in 16-bit integers are taken wherever tensors of them are;
+    anything else is refused as such a tensor is."""
+    mu = F.Muon(F.Plan([(60, 70)], 2, "flat"))
+    want = mu.workspace_bytes(torch.bfloat16, torch.bfloat16)
+    for t in (torch.int16, torch.uint16):
+        assert mu.workspace_bytes(t, t) == want
+        assert mu.workspace(t, t, device="cpu").numel() == want[0]
+    for t in (torch.float16, torch.float64, torch.int32):
+        with pytest.raises(TypeError, match="dtype"):
+            mu.workspace_bytes(t, torch.bfloat16)
+        with pytest.raises(TypeError, match="dtype"):
+            mu.workspace(torch.float32, t, device="cpu")
