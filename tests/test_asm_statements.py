@@ -26,14 +26,15 @@ def statements(text):
 
 @pytest.mark.parametrize("path", SOURCES, ids=os.path.basename)
 def test_special_registers_are_declared(path):
-    """A statement that writes M0, VCC or EXEC names it among its clobbers, or
-    the compiler may keep a value of its own there across it."""
+    """A statement that writes M0, VCC or EXEC names it among its outputs or
+    clobbers, or the compiler may keep a value of its own there across it."""
     with open(path) as f:
         for body in statements(f.read()):
             parts = body.split(":")
             for reg in ("m0", "vcc", "exec"):
                 if re.search(rf"\b[sv]_\w+ {reg}\b", parts[0]):
-                    assert len(parts) > 3 and f'"{reg}"' in parts[-1], body
+                    assert len(parts) > 1 and f"{{{reg}}}" in parts[1] or \
+                        len(parts) > 3 and f'"{reg}"' in parts[-1], body
 
 
 def test_statements_are_found():
