@@ -100,9 +100,9 @@ struct El<u16> {
 // lanes on multiples of four of the destination space.  Where the source
 // space is not on the same grid (shards that begin at odd places) it is
 // read element by element, which the first-level cache turns into the same
-// lines.  Bound by HBM; measured: momentum 9.4 us (6.0 TB/s) on 3.1M
+// lines.  Bound by HBM; measured: momentum 9.9 us (5.7 TB/s) on 3.1M
 // parameters, R = 4, and 0.92 ms (6.2 TB/s) on 218M, R = 8, both bf16; apply
-// 6.3 us (6.0 TB/s) and 0.41 ms (6.4 TB/s).  Items of 512 or 2,048 elements
+// 6.7 us (5.6 TB/s) and 0.42 ms (6.2 TB/s).  Items of 512 or 2,048 elements
 // measured level.
 template <int N>
 struct MomentumArgs {
@@ -348,8 +348,8 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
 // where no coefficient is above 2 for q' < 0; at q = q' = 0, as everywhere
 // that eps does not matter, these are a, b and c.  q stops at -400: X is then
 // 0 in fp32, and no 16 steps of coefficients up to 16 make it anything else.
-// A lane has 8 adjacent entries of each of two rows.  196 us for 218M bf16
-// elements (4.5 TB/s read and written).
+// A lane has 8 adjacent entries of each of two rows.  198 us for 218M bf16
+// elements (4.4 TB/s read and written).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_convert(const T* __restrict__ update,
                                                       ConvertArgs a) {
@@ -1205,9 +1205,9 @@ __device__ __forceinline__ void flush(f4 (&sum)[FM][FN], f4 (&acc)[FM][FN]) {
 // and the loads of a later round between them: issued in one go, those loads
 // keep a wave from its products for a thousand cycles.
 //
-// Measured on the hidden-4096 block (7 matrices, 256 x 256 tiles): A 729 us
-// (1,270 TFLOP/s, diagonal tiles whole), B 321 (1,170), the step 1,506
-// (1,140); alone, so without the clock's fall under load, the matrix cores are
+// Measured on the hidden-4096 block (7 matrices, 256 x 256 tiles): A 736 us
+// (1,260 TFLOP/s, diagonal tiles whole), B 325 (1,155), the step 1,527
+// (1,125); alone, so without the clock's fall under load, the matrix cores are
 // 73, 67 and 63% busy.  The rest is a tile's start and end (12% of 64 rounds)
 // and the rounds' loads.
 template <typename S, Stage ST, bool SPLIT, typename O>
@@ -1439,7 +1439,7 @@ __global__ __launch_bounds__(256, S::Waves) void k_thin(
 
 // A's tiles whose sums came in parts: the parts in their order, four chains
 // of them, and to where k_thin's (F = 1) or k_gemm's (F = 2) own go.  A lane
-// has F x F f4's of each part.  8.5 us for 36 tiles of 15 parts (512 x 32000,
+// has F x F f4's of each part.  8.4 us for 36 tiles of 15 parts (512 x 32000,
 // the parts 17.7), 23 us for 3 of 171 (32 x 1M, the parts 32: a workgroup
 // reads 700 KB alone).
 template <int F, bool SPLIT>

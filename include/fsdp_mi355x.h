@@ -487,7 +487,10 @@ fsdp_status fsdp_muon_momentum(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
  *   every operand is kept as two fp16 parts and each product is the sum of
  *   three: an error near that of fp32 products, at three times the work.
  *   Both hold however small |U|_F is beside eps: the operands' powers of two
- *   follow X, per matrix and step.
+ *   follow X, per matrix and step, by what its singular values can be: s =
+ *   |U|_F / (|U|_F + eps) before the first step, |a| s + |b| s^3 + |c| s^5
+ *   after each, 1 at most.  (Coefficients that take them far below that, as
+ *   a = 0 does, leave fewer bits.)
  *   The steps' intermediate values must stay below 16 (X) and 64 (A and
  *   b A + c A A): so they do for coefficients that map [0, 1.3] into
  *   itself.  A matrix of zeros gives zeros.  One that holds an infinity
@@ -527,7 +530,9 @@ fsdp_status fsdp_muon_apply(const fsdp_muon* mu, const fsdp_muon_hparams* hp, co
  *   for the chosen parameters and AdamW's first moment for the others.
  *   master, m, v, param_out, gradients and workspace are pairwise disjoint
  *   (two gradients may be the same).  workspace: step_bytes of
- *   fsdp_muon_workspace, 256-byte aligned, used as fsdp_orthogonalize's. */
+ *   fsdp_muon_workspace, 256-byte aligned, used as fsdp_orthogonalize's.
+ *   A captured call replays the hyper-parameters and the step counter that it
+ *   was captured with; where these change, capture again. */
 fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* hp,
                                  const fsdp_adamw_hparams* adamw, int64_t step,
                                  const void* const* grads, int32_t grad_dtype, float* master,
