@@ -138,7 +138,7 @@ int shape_of(const std::vector<MuonMat>& mats, bool square, bool gram, bool spli
 // with three products 124 and 95 at 4,096; 1440 x 16384 (276 tiles of 64 x 64)
 // 1,013 and 935, 1800 x 32000 (435) 2,290 and 2,360.  Parts of 16 rounds
 // measured 5-10% longer, four per compute unit level.
-constexpr int64_t kPart = 32, kJoin = 64, kJoined = 32;
+constexpr int64_t kPart = 32, kJoin = 64;
 
 int64_t rounds_of(const std::vector<MuonMat>& mats, int64_t side, int products) {
   int64_t work = 0;
@@ -156,13 +156,25 @@ int64_t part_rounds(const std::vector<MuonMat>& mats, int64_t side, int products
   return longest >= len + std::max(kJoin, len / 4) ? len : longest;
 }
 
-// Most parts that a tile of this side is joined from.
-int64_t most_parts(const std::vector<MuonMat>& mats, int64_t side, int products) {
-  const int64_t len = part_rounds(mats, side, products);
-  int64_t most = 1;
-  for (const MuonMat& t : mats)
+// Whether A in 64 x 64 tiles gains more by reading half as much than it loses
+// by joining: one workgroup adds up a tile's parts, 0.4 us each.  To 32 parts
+// it does; beyond, where the reading saved is 12 MB a part or more.  Measured
+// by MB a part, us a step against 32 x 32 tiles: 0.4 (64 x 1M beside 1024 x
+// 1024, 443 parts) 185 more, 1.5 (100 x 400000, 900 x 900) 67, 5.6 (192 x
+// 400000, 600 x 600) 19, 8.4 (256 x 200000, 600 x 600) 9; 12 (64 x 1M, 320 x
+// 300000) 7 less, 14 (320 x 150000, 300 x 300) 12, 20 (256 x 500000, 600 x 600)
+// 47, 40 (256 x 1M, 600 x 600) 217; fp32 results 6.6 21 more, 14 4 more, 13 3
+// less, 17 36 less.
+bool larger_pay(const std::vector<MuonMat>& mats, int products) {
+  const int64_t len = part_rounds(mats, kMuonTiles[1], products);
+  int64_t most = 1, saved = 0;
+  for (const MuonMat& t : mats) {
     most = std::max(most, (int64_t(products) * t.np / kMuonRound + len - 1) / len);
-  return most;
+    // two operands of `side` rows a tile, in fp16
+    saved += (count({t}, kMuonTiles[0], true) * kMuonTiles[0] -
+              count({t}, kMuonTiles[1], true) * kMuonTiles[1]) * 4 * products * t.np;
+  }
+  return most <= 32 || saved >= most * 12000000;
 }
 
 // `all`: rounds of the matrix's sums.  The same part of all tiles lies
@@ -310,16 +322,13 @@ fsdp_status build_muon(const fsdp_plan* plan, int32_t n_params, const int32_t* p
     auto fill = [&](std::vector<MuonGemmTile>& out, int* shape, bool square, bool gram) {
       *shape = shape_of(mu->mats, square, gram, split != 0);
       const int products = split ? 3 : 1;
-      // 64 x 64 tiles read half as much, where their parts are as many and
-      // no tile has more than 32 to join: 1024 x 32000 takes 882 us with
-      // them and 1,133 in parts of 32 x 32 (whole sums: 1,154), 512 x 32000
-      // 337 and 367 (426); one tile of 32 x 1M in 512 parts took 1,920.  The
-      // tiles and the rounds may be different matrices': 64 x 1M beside 1024 x
-      // 1024, 443 parts, took 1,865 us, 939 in parts of 32 x 32; 100 x 400000
-      // beside 900 x 900, 153 parts, 903 and 567
+      // 64 x 64 tiles read half as much, where their parts are as many and not
+      // too many of one tile: 1024 x 32000 takes 882 us with them and 1,133 in
+      // parts of 32 x 32 (whole sums: 1,154), 512 x 32000 337 and 367 (426);
+      // one tile of 32 x 1M in 512 parts took 1,920
       if (gram && *shape == 0 && count(mu->mats, kMuonTiles[1], true) >= kCus / 16 &&
           rounds_of(mu->mats, kMuonTiles[1], products) >= 2 * kCus * kPart &&
-          most_parts(mu->mats, kMuonTiles[1], products) <= kJoined)
+          larger_pay(mu->mats, products))
         *shape = 1;
       auto depth = [gram](const MuonMat& t) { return int64_t(gram ? t.np : t.mp); };
       const int64_t side = kMuonTiles[*shape];

@@ -15,8 +15,9 @@ or as one call, with AdamW on the unit's other parameters:
 
 Hyper-parameters are a dict like MUON.  Every call runs on the GPU that holds
 its tensors, which has to be the current one, and on the current stream
-unless another is given.  The bind_* forms check the tensors and marshal the
-pointers once, for loops.
+unless another is given; tensors and workspaces of a call on another stream
+have to live until it is done there.  The bind_* forms check the tensors and
+marshal the pointers once, for loops, the hyper-parameters with them.
 """
 
 from __future__ import annotations

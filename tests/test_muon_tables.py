@@ -74,3 +74,13 @@ def test_every_tile_of_every_product_is_in_some_unit():
     for k in range(3):
         assert {u[1][k] for u in UNITS.values()} == {64, 128, 256}
         assert {u[2][k] for u in UNITS.values()} == {64, 128}
+
+
+@pytest.mark.parametrize("shapes", [
+    [(256, 500000), (600, 600)], [(320, 150000), (300, 300)], [(320, 600000), (300, 300)],
+    [(256, LONG), (600, 600)], [(64, LONG), (320, 300000)]])
+def test_long_matrices_whose_reading_outweighs_the_joining(choices, shapes):
+    """64 x 64 tiles read A's operands half as often: with long matrices of
+    more rows that is more than adding up a few dozen parts."""
+    for c in choices(shapes)[0 if shapes[0][0] > 64 else 1:]:
+        assert c.gram == 64, c
