@@ -46,6 +46,14 @@ class MuonHParams(ctypes.Structure):
                 ("scale", ctypes.c_int32)]
 
 
+class MatmulShape(ctypes.Structure):
+    _fields_ = [("op", ctypes.c_int32), ("groups", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("lda", ctypes.c_int64),
+                ("ldb", ctypes.c_int64), ("ldc", ctypes.c_int64),
+                ("group_stride", ctypes.c_int64), ("accumulate", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("numel_full", ctypes.c_int64), ("shard_numel", ctypes.c_int64),
                 ("world", ctypes.c_int32), ("n_params", ctypes.c_int32),
@@ -89,6 +97,39 @@ _SIGS = {
                                                      ctypes.c_void_p, ctypes.c_void_p,
                                                      ctypes.c_void_p, ctypes.c_void_p,
                                                      ctypes.c_int32, ctypes.c_void_p]),
+    "fsdp_grouped_matmul_workspace": (ctypes.c_int, [ctypes.POINTER(MatmulShape),
+                                                     ctypes.c_int32,
+                                                     ctypes.POINTER(ctypes.c_int64)]),
+    "fsdp_grouped_matmul": (ctypes.c_int, [ctypes.POINTER(MatmulShape), ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                           ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                           ctypes.c_int64, ctypes.c_void_p]),
+    "fsdp_grouped_matmul_i8": (ctypes.c_int, [ctypes.POINTER(MatmulShape), ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                              ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                              ctypes.c_int32, ctypes.c_void_p]),
+    "fsdp_quantize_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                                          ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32,
+                                          ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                          ctypes.c_void_p]),
+    "fsdp_quant_plan": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
+                                       ctypes.POINTER(ctypes.c_int32),
+                                       ctypes.POINTER(ctypes.c_void_p)]),
+    "fsdp_quant_destroy": (None, [ctypes.c_void_p]),
+    "fsdp_quant_prepare": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p]),
+    "fsdp_quant_sizes": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int64)]),
+    "fsdp_quant_param": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
+                                        ctypes.POINTER(ctypes.c_int64)]),
+    "fsdp_gather_quantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                            ctypes.POINTER(ctypes.c_void_p),
+                                            ctypes.POINTER(ctypes.c_void_p),
+                                            ctypes.POINTER(ctypes.c_void_p), ctypes.c_void_p]),
+    "fsdp_dequantize": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p),
+                                       ctypes.POINTER(ctypes.c_void_p),
+                                       ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32,
+                                       ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32,
+                                       ctypes.c_void_p]),
     "fsdp_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fsdp_plan_work_items": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32,
                                             ctypes.POINTER(ctypes.c_int64), ctypes.c_int64,

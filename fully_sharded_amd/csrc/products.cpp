@@ -1,0 +1,245 @@
+// Host side of the unit's matrix products: the C entry points' checks, the
+// rule that chooses a tile, and the launches.
+#include "products.hpp"
+
+#include <algorithm>
+
+#include "checks.hpp"
+#include "ops.hpp"
+
+namespace fsdp {
+namespace {
+
+constexpr int64_t kCus = 256;      // compute units
+constexpr int64_t kXcds = 8;
+constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
+constexpr int64_t kMaxGroups = 65536;
+// Rows that go straight to LDS: 256 of them within 2^31 bytes.
+constexpr int64_t kMaxPitch = (int64_t(1) << 23) - 1;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
+  ProductRule r{};
+  const bool weight = m.op == FSDP_MATMUL_TN;
+  const int64_t met = std::max<int64_t>(1, std::min<int64_t>(m.groups, m.rows));
+  // tiles about as many as there will be: every group's last row of tiles is
+  // half empty
+  auto tiles = [&](int64_t side) {
+    return weight ? m.groups * ceil_div(m.n, side) * ceil_div(m.k, side)
+                  : (met == 1 ? ceil_div(m.rows, side) : m.rows / side + (met + 1) / 2) *
+                        ceil_div(m.n, side);
+  };
+  r.direct = direct && type != kProductF32;
+  r.tile = 0;
+  if (type != kProductF32) {
+    if (r.direct && tiles(256) >= kCus)
+      r.tile = 2;
+    else if (tiles(128) >= kCus)
+      r.tile = 1;
+  }
+  const int64_t side = kProductTiles[r.tile];
+  r.n_parts = 1;
+  if (weight) {
+    const int64_t per_group = ceil_div(m.n, side) * ceil_div(m.k, side);
+    const int64_t all = per_group * m.groups;
+    // long sums of few tiles in parts, eight rounds of 64 rows or more each
+    if (type == kProductBf16 && all < kCus)
+      r.n_parts = static_cast<int>(std::max<int64_t>(
+          1, std::min<int64_t>({2 * kCus / all, m.rows / met / 512, 64})));
+    r.grid = kXcds * ceil_div(per_group * r.n_parts, kXcds) * m.groups;
+    r.join = all;
+    if (r.n_parts > 1) r.workspace = all * r.n_parts * side * side * 4;
+  } else {
+    const int64_t down = m.groups == 1 ? ceil_div(m.rows, side) : m.rows / side + met;
+    r.grid = kXcds * ceil_div(down * ceil_div(m.n, side), kXcds);
+  }
+  return r;
+}
+
+namespace {
+
+struct Extents {
+  int64_t a, b, c;  // elements from the first to behind the last
+};
+
+// Sizes and strides, without the pointers.
+fsdp_status check_sizes(const fsdp_matmul* m, bool codes) {
+  if (!m) return FSDP_ERR_INVALID_ARG;
+  if (m->op < FSDP_MATMUL_NT || m->op > FSDP_MATMUL_TN || (codes && m->op == FSDP_MATMUL_TN) ||
+      m->groups < 1 || m->rows < 0 || m->n < 1 || m->k < 1 ||
+      (m->accumulate != 0 && m->accumulate != 1))
+    return FSDP_ERR_INVALID_ARG;
+  const int64_t most = INT32_MAX / 2;
+  if (m->groups > kMaxGroups || m->rows > most || m->n > most || m->k > most)
+    return FSDP_ERR_UNSUPPORTED;
+  const int64_t a_cols = m->op == FSDP_MATMUL_TN ? m->n : m->k;
+  const int64_t b_cols = m->op == FSDP_MATMUL_NN ? m->n : m->k;
+  const int64_t c_cols = m->op == FSDP_MATMUL_TN ? m->k : m->n;
+  const int64_t far = int64_t(1) << 40;
+  if (m->lda < a_cols || m->ldb < b_cols || m->ldc < c_cols || m->group_stride < 0)
+    return FSDP_ERR_INVALID_ARG;
+  if (m->lda > far || m->ldb > far || m->ldc > far || m->group_stride > far)
+    return FSDP_ERR_UNSUPPORTED;
+  // a group's gradient must not meet the next one's
+  if (m->op == FSDP_MATMUL_TN && m->groups > 1 &&
+      m->group_stride < (m->n - 1) * m->ldc + m->k)
+    return FSDP_ERR_INVALID_ARG;
+  if (codes && m->k > kMaxSum) return FSDP_ERR_UNSUPPORTED;
+  return FSDP_OK;
+}
+
+Extents extents(const fsdp_matmul& m) {
+  const int64_t behind = m.rows > 0 ? m.rows - 1 : 0;
+  Extents e{};
+  if (m.op == FSDP_MATMUL_TN) {
+    e.a = m.rows ? behind * m.lda + m.n : 0;
+    e.b = m.rows ? behind * m.ldb + m.k : 0;
+    e.c = (m.groups - 1) * m.group_stride + (m.n - 1) * m.ldc + m.k;
+  } else {
+    const int64_t rows = m.op == FSDP_MATMUL_NT ? m.n : m.k;
+    const int64_t cols = m.op == FSDP_MATMUL_NT ? m.k : m.n;
+    e.a = m.rows ? behind * m.lda + m.k : 0;
+    e.b = (m.groups - 1) * m.group_stride + (rows - 1) * m.ldb + cols;
+    e.c = m.rows ? behind * m.ldc + m.n : 0;
+  }
+  return e;
+}
+
+// Whether bf16 operands can go straight to LDS: every 16-byte piece of a row
+// is aligned and inside the row.
+bool pieces(const fsdp_matmul& m, const void* a, const void* b) {
+  const int64_t a_cols = m.op == FSDP_MATMUL_TN ? m.n : m.k;
+  const int64_t b_cols = m.op == FSDP_MATMUL_NN ? m.n : m.k;
+  return aligned(a, 16) && aligned(b, 16) && a_cols % 8 == 0 && b_cols % 8 == 0 &&
+         m.lda % 8 == 0 && m.ldb % 8 == 0 && 2 * m.lda <= kMaxPitch && 2 * m.ldb <= kMaxPitch &&
+         (m.op == FSDP_MATMUL_TN || m.groups == 1 || m.group_stride % 8 == 0);
+}
+
+ProductArgs product_args(const fsdp_matmul& m, const int32_t* offsets, const void* a,
+                         const void* b, void* c, int32_t out_dtype) {
+  ProductArgs p{};
+  p.a = a;
+  p.b = b;
+  p.c = c;
+  p.offsets = offsets;
+  p.lda = m.lda;
+  p.ldb = m.ldb;
+  p.ldc = m.ldc;
+  p.group_stride = m.group_stride;
+  p.rows = static_cast<int32_t>(m.rows);
+  p.groups = m.groups;
+  p.n = static_cast<int32_t>(m.n);
+  p.k = static_cast<int32_t>(m.k);
+  p.accumulate = m.accumulate;
+  p.out_f32 = out_dtype == FSDP_F32;
+  p.n_parts = 1;
+  return p;
+}
+
+bool fits(const ProductRule& r) {
+  // workgroups of up to 512 lanes
+  return r.grid <= kMaxItems / 2 && r.join <= kMaxItems / 2;
+}
+
+}  // namespace
+}  // namespace fsdp
+
+using namespace fsdp;
+
+extern "C" {
+
+fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, int64_t* bytes) {
+  if (!bytes || !valid_dtype(dtype)) return FSDP_ERR_INVALID_ARG;
+  const fsdp_status st = check_sizes(m, false);
+  if (st != FSDP_OK) return st;
+  // whichever way the operands turn out to be aligned
+  const ProductType type = static_cast<ProductType>(dtype);
+  *bytes = std::max(product_rule(*m, type, true).workspace,
+                    product_rule(*m, type, false).workspace);
+  return FSDP_OK;
+}
+
+fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, const void* a,
+                                const void* b, int32_t dtype, void* c, int32_t out_dtype,
+                                void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&]() -> fsdp_status {
+    if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check_sizes(m, false);
+    if (st != FSDP_OK) return st;
+    if (!offsets && m->groups != 1) return FSDP_ERR_INVALID_ARG;
+    const bool reads_b = m->op != FSDP_MATMUL_TN || m->rows > 0;
+    // (an array of nothing may be at NULL)
+    if ((m->rows > 0 && !a) || (reads_b && !b) || ((m->op == FSDP_MATMUL_TN || m->rows > 0) && !c))
+      return FSDP_ERR_INVALID_ARG;
+    const int64_t es = dtype_size(dtype), ces = dtype_size(out_dtype);
+    if (!aligned(a, es) || !aligned(b, es) || !aligned(c, ces) || !aligned(offsets, 4))
+      return FSDP_ERR_INVALID_ARG;
+    const ProductType type = static_cast<ProductType>(dtype);
+    const ProductRule rule = product_rule(*m, type, pieces(*m, a, b));
+    if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
+    const Extents e = extents(*m);
+    Ranges reads, writes;
+    reads.push_back(range_of(a, e.a * es));
+    reads.push_back(range_of(b, reads_b ? e.b * es : 0));
+    reads.push_back(range_of(offsets, offsets ? (int64_t(m->groups) + 1) * 4 : 0));
+    writes.push_back(range_of(c, e.c * ces));
+    if (rule.workspace) {
+      if (!workspace || workspace_bytes < rule.workspace || !aligned(workspace, 256))
+        return FSDP_ERR_INVALID_ARG;
+      writes.push_back(range_of(workspace, rule.workspace));
+    }
+    for (const Range& w : writes)
+      for (const Range& r : reads)
+        if (overlap(w, r)) return FSDP_ERR_INVALID_ARG;
+    if (any_overlap(writes)) return FSDP_ERR_INVALID_ARG;
+    if (m->op != FSDP_MATMUL_TN && m->rows == 0) return FSDP_OK;
+    ProductArgs p = product_args(*m, offsets, a, b, c, out_dtype);
+    p.parts = static_cast<float*>(workspace);
+    p.n_parts = rule.n_parts;
+    return status_of(launch_product(p, type, m->op, rule, StreamSink(stream)));
+  });
+}
+
+fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets, const int8_t* a,
+                                   const float* a_scale, const int8_t* b, const float* b_scale,
+                                   int64_t b_scale_stride, void* c, int32_t out_dtype,
+                                   void* stream) {
+  return guarded([&]() -> fsdp_status {
+    if (!valid_dtype(out_dtype) || !b) return FSDP_ERR_INVALID_ARG;
+    fsdp_status st = check_sizes(m, true);
+    if (st != FSDP_OK) return st;
+    if (!offsets && m->groups != 1) return FSDP_ERR_INVALID_ARG;
+    if (m->rows > 0 && (!a || !a_scale || !c)) return FSDP_ERR_INVALID_ARG;
+    const int64_t ces = dtype_size(out_dtype);
+    if (!aligned(a, 16) || !aligned(b, 16) || m->lda % 16 || m->ldb % 16 ||
+        (m->groups > 1 && m->group_stride % 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
+        !aligned(c, ces) || !aligned(offsets, 4) || b_scale_stride < 0)
+      return FSDP_ERR_INVALID_ARG;
+    if (m->lda > kMaxPitch || m->ldb > kMaxPitch || b_scale_stride > (int64_t(1) << 40))
+      return FSDP_ERR_UNSUPPORTED;
+    const ProductRule rule = product_rule(*m, kProductI8, true);
+    if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
+    Extents e = extents(*m);
+    // rows of codes are read to the next multiple of 16
+    e.a = (e.a + 15) / 16 * 16;
+    e.b = (e.b + 15) / 16 * 16;
+    const Range w = range_of(c, e.c * ces);
+    const Range reads[] = {
+        range_of(a, e.a), range_of(b, e.b), range_of(a_scale, m->rows * 4),
+        range_of(b_scale, b_scale ? ((m->groups - 1) * b_scale_stride + m->n) * 4 : 0),
+        range_of(offsets, offsets ? (int64_t(m->groups) + 1) * 4 : 0)};
+    for (const Range& r : reads)
+      if (overlap(w, r)) return FSDP_ERR_INVALID_ARG;
+    if (m->rows == 0) return FSDP_OK;
+    ProductArgs p = product_args(*m, offsets, a, b, c, out_dtype);
+    p.sa = a_scale;
+    p.sb = b_scale;
+    p.sb_stride = b_scale_stride;
+    return status_of(launch_product(p, kProductI8, m->op, rule, StreamSink(stream)));
+  });
+}
+
+}  // extern "C"

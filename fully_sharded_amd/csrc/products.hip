@@ -1,0 +1,780 @@
+// gfx950 kernels of the unit's matrix products: the linear layers of a gathered
+// unit, grouped by expert, and their gradients.
+//
+//   NT  C[t, n] = sum_k A[t, k] B_g[n, k]     forward, weights [out, in]
+//   NN  C[t, n] = sum_k A[t, k] B_g[k, n]     input gradient
+//   TN  C_g[n, k] = sum_t A[t, n] B[t, k]     weight gradient, t over g's rows
+//
+// with g the group of row t.  Operands are bf16, 8-bit codes with a scale per
+// row (NT and NN), or fp32, and sums fp32 (codes: 32-bit integers, exact).
+//
+// One tile loop serves bf16 and codes: both take 16 bytes per lane and matrix
+// instruction, which are 8 or 16 entries of the sum.  An operand whose rows lie
+// along the sum is kept in LDS as rows of 128 bytes and read as it is; one
+// whose rows lie across it as its rows are, and transposed by the LDS read (of
+// 16- or 8-bit entries).  So no operand is ever written transposed.
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "device.hpp"
+#include "products.hpp"
+
+namespace fsdp {
+namespace {
+
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef int i2 __attribute__((ext_vector_type(2)));
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+
+struct Bf16 {
+  static constexpr int kBytes = 2;
+  using Acc = f4;
+  __device__ __forceinline__ static Acc mma(u4 q, u4 p, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, q),
+                                                   __builtin_bit_cast(b8, p), c, 0, 0, 0);
+  }
+};
+struct I8 {
+  static constexpr int kBytes = 1;
+  using Acc = i4;
+  __device__ __forceinline__ static Acc mma(u4 q, u4 p, Acc c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i4, q),
+                                                 __builtin_bit_cast(i4, p), c, 0, 0, 0);
+  }
+};
+
+constexpr int kRow = 128;  // bytes of the sum per round, of a row along it
+
+// A BM x BN tile by WM x WN waves, NS rounds in LDS, registers for WPS waves
+// per SIMD.
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int WPS_>
+struct Tile {
+  static constexpr int Waves = WPS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int NW = WM * WN, Threads = 64 * NW;
+  static constexpr int TM = BM / WM, TN = BN / WN;  // a wave's tile
+  static constexpr int FM = TM / 16, FN = TN / 16;  // its 16 x 16 parts
+  static constexpr int LP = BM * kRow / 1024 / NW, LQ = BN * kRow / 1024 / NW;
+  static constexpr int RoundBytes = (BM + BN) * kRow;
+};
+
+// The place of 16-byte piece c of row r along the sum: the 16 rows that a wave
+// reads at one piece spread over all banks.
+__device__ __forceinline__ int place(int r, int c) { return c ^ (r & 7); }
+// The same for rows across the sum, BM entries of BYTES each: a transposing
+// read takes 32 bytes of rows 0-3, 8-11, 16-19 and 24-27 (or 4-7, ...) of 32 at
+// a time of 16-bit entries, and 16 bytes of rows 0-7 and 16-23 (or 8-15, ...)
+// of 64 of 8-bit ones.  The row's bits that tell those apart move the piece,
+// but for the ones that the length of a row moves by itself (256 bytes are all
+// banks once).
+template <int BM, int BYTES>
+__device__ __forceinline__ int place_across(int r, int c) {
+  if constexpr (BYTES == 2) {
+    const int b = (r & 3) | ((r >> 1) & 4);
+    return c ^ (BM == 32 ? (b & 4) >> 1 : BM == 64 ? b & 6 : b << 1);
+  } else {
+    return c ^ (BM == 256  ? (r & 7) | ((r >> 1) & 8)
+                : BM == 128 ? ((r >> 1) & 3) | ((r >> 2) & 4)
+                            : ((r >> 2) & 1) | ((r >> 3) & 2));
+  }
+}
+
+// 16 bytes per lane from a buffer to LDS at a wave-uniform address, lane after
+// lane; zeros for offsets from kOutside on.  An asm statement for the reason
+// given at load_to_lds, and waited for as those are.
+constexpr uint32_t kOutside = 0x80000000u;
+__device__ __forceinline__ void buffer_to_lds(u4 buffer, uint32_t offset, uint32_t to) {
+  uint32_t m0;
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               : "=&{m0}"(m0)
+               : "v"(offset), "s"(buffer), "s"(to)
+               : "memory");
+}
+// A raw buffer of kOutside bytes.
+__device__ __forceinline__ u4 buffer_at(const char* p) {
+  const uint64_t x = reinterpret_cast<uint64_t>(p);
+  return u4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x))),
+            static_cast<uint32_t>(
+                __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(x >> 32) & 0xffffu)),
+            kOutside, 0x00020000u};
+}
+
+// An operand of a tile: where its first entry is, and how much of it there is.
+struct Operand {
+  const char* p;   // entry (first row or column of the tile, first of the sum)
+  int64_t ld;      // bytes from one row to the next
+  int side;        // rows (along) or columns (across) from there on that exist
+  int sum;         // entries of the sum
+};
+
+// This wave's pieces of an operand's round, L of 1024 bytes each.  ROUND: bytes
+// of an along row or entries of an across column per round.
+template <typename T, int SIDE, int L, bool ACROSS>
+struct Pieces {
+  static constexpr int kEach = 16 / T::kBytes;     // entries of a piece
+  static constexpr int kSum = kRow / T::kBytes;    // of the sum per round
+  static constexpr int kPerRow = ACROSS ? SIDE / kEach : kRow / 16;
+  static constexpr int kRows = 64 / kPerRow;       // rows that a wave's load fills
+  static_assert(kPerRow <= 64);
+
+  // Row and first entry (in the row) of this lane's piece x.
+  __device__ __forceinline__ static int row(int wave, int x) {
+    return (wave * L + x) * kRows + (static_cast<int>(threadIdx.x) & 63) / kPerRow;
+  }
+  __device__ __forceinline__ static int col(int wave, int x) {
+    const int r = row(wave, x), c = (threadIdx.x & 63) % kPerRow;
+    return (ACROSS ? place_across<SIDE, T::kBytes>(r, c) : place(r, c)) * kEach;
+  }
+};
+
+// Pieces that go straight to LDS.  Rows and columns that do not exist, and the
+// sum's entries behind its end, are zeros.  (Codes along the sum: a piece that
+// the end cuts is read whole; its row is padded with zeros.)
+template <typename T, int SIDE, int L, bool ACROSS>
+struct Direct {
+  using P = Pieces<T, SIDE, L, ACROSS>;
+  uint32_t off[L];
+  const char* p;
+  int64_t step;
+  int sum, wave;
+
+  __device__ __forceinline__ void begin(const Operand& o, int wave_) {
+    wave = wave_;
+    p = o.p;
+    sum = o.sum;
+    step = ACROSS ? P::kSum * o.ld : kRow;
+#pragma unroll
+    for (int x = 0; x < L; ++x) {
+      const int r = P::row(wave, x), c = P::col(wave, x);
+      off[x] = static_cast<uint32_t>(r) * static_cast<uint32_t>(o.ld) + c * T::kBytes;
+      if ((ACROSS ? c : r) >= o.side) off[x] = kOutside;
+    }
+  }
+  __device__ __forceinline__ void load(int round, uint32_t image, int x) const {
+    const int left = sum - round * P::kSum;
+    const int at = ACROSS ? P::row(wave, x) : P::col(wave, x);
+    buffer_to_lds(buffer_at(p + round * step), at < left ? off[x] : kOutside,
+                  __builtin_amdgcn_readfirstlane(image + (wave * L + x) * 1024));
+  }
+};
+
+// Pieces that pass through registers: for rows that begin anywhere.
+template <typename T, int SIDE, int L, bool ACROSS>
+struct Staged {
+  using P = Pieces<T, SIDE, L, ACROSS>;
+  Operand o;
+  u4 v[L];
+  int wave;
+
+  __device__ __forceinline__ void begin(const Operand& o_, int wave_) {
+    o = o_;
+    wave = wave_;
+  }
+  __device__ __forceinline__ void fetch(int round) {
+#pragma unroll
+    for (int x = 0; x < L; ++x) {
+      const int r = P::row(wave, x), c = P::col(wave, x);
+      const int s = round * P::kSum + (ACROSS ? r : c);  // of the sum
+      const int left = o.sum - s, side = o.side - (ACROSS ? c : r);
+      const int have = ACROSS ? (left > 0 ? side : 0) : (side > 0 ? left : 0);
+      const char* from =
+          o.p + (ACROSS ? s * o.ld + int64_t(c) * T::kBytes : r * o.ld + int64_t(s) * T::kBytes);
+      u4 w = {0, 0, 0, 0};
+      if (have >= P::kEach) {
+        typedef u4 any __attribute__((aligned(2)));
+        w = *reinterpret_cast<const any*>(from);
+      } else {
+        static_assert(T::kBytes == 2);
+        const u16* h = reinterpret_cast<const u16*>(from);
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+          if (e < have) w[e / 2] |= static_cast<uint32_t>(h[e]) << (e % 2 * 16);
+      }
+      v[x] = w;
+    }
+  }
+  __device__ __forceinline__ void put(char* image) const {
+#pragma unroll
+    for (int x = 0; x < L; ++x)
+      *reinterpret_cast<u4*>(image + (wave * L + x) * 1024 + (threadIdx.x & 63) * 16) = v[x];
+  }
+};
+
+// LDS to registers: the matrix instruction's operands, 16 rows (columns of an
+// across operand) by 64 bytes of the sum, COUNT of them from row `from` on.
+template <typename T, int SIDE, int COUNT, bool ACROSS>
+struct Fetch {
+  int at[ACROSS ? COUNT : 1];
+
+  __device__ __forceinline__ explicit Fetch(int from) {
+    const int lane = threadIdx.x & 63, lr = lane & 15, lk = lane >> 4;
+    if constexpr (!ACROSS) {
+      at[0] = (from + lr) * kRow;
+    } else {
+      const int row = T::kBytes == 2 ? lk * 8 + (lr >> 2) : lk * 16 + (lr >> 1);
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i) {
+        const int c = T::kBytes == 2 ? (from + i * 16) / 8 + ((lr & 3) >> 1) : (from + i * 16) / 16;
+        at[i] = row * SIDE * T::kBytes + place_across<SIDE, T::kBytes>(row, c) * 16 + (lr & 1) * 8;
+      }
+    }
+  }
+  __device__ __forceinline__ u4 get(const char* image, int kk, int i) const {
+    if constexpr (!ACROSS) {
+      const int lane = threadIdx.x & 63;
+      return *reinterpret_cast<const u4*>(image + place(lane & 15, kk * 4 + (lane >> 4)) * 16 +
+                                          at[0] + i * 16 * kRow);
+    } else if constexpr (T::kBytes == 2) {
+      union {
+        s4 s[2];
+        u4 u;
+      } v;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        v.s[half] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s4*)(image + at[i] +
+                                                    (kk * 32 + half * 4) * SIDE * 2));
+      return v.u;
+    } else {
+      union {
+        i2 s[2];
+        u4 u;
+      } v;
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        v.s[half] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i2*)(image + at[i] + (kk * 64 + half * 8) * SIDE));
+      return v.u;
+    }
+  }
+};
+
+// ------------------------------------------------------- which tile is whose
+struct Place {
+  int group;       // < 0: none
+  int lo, hi;      // its rows
+  int i, j, part;  // the tile
+};
+
+__device__ __forceinline__ int clamp_to(int x, int lo, int hi) {
+  return x < lo ? lo : x > hi ? hi : x;
+}
+// Rows of group g.  Offsets that do not ascend or leave [0, rows] give wrong
+// results, but no row outside.
+__device__ __forceinline__ void rows_of(const ProductArgs& a, int g, int* lo, int* hi) {
+  if (!a.offsets) {
+    *lo = 0;
+    *hi = a.rows;
+    return;
+  }
+  *lo = clamp_to(a.offsets[g], 0, a.rows);
+  *hi = clamp_to(a.offsets[g + 1], *lo, a.rows);
+}
+
+// Tiles are numbered along bands of 8 tiles down, column by column, and each of
+// the 8 dies, to which workgroups go in turn, takes a contiguous range: the 32
+// tiles that a die has in flight share 8 panels of A and 4 of B in its L2.
+constexpr int kBand = 8, kXcds = 8;
+__device__ __forceinline__ bool in_band(int id, int ni, int nj, int* i, int* j) {
+  const int band = id / (kBand * nj), first = band * kBand;
+  const int high = ni - first < kBand ? ni - first : kBand;
+  const int in = id - first * nj;
+  *i = first + in % high;
+  *j = in / high;
+  return *i < ni && *j < nj;
+}
+
+// Tiles of NT and NN: every group's rows in tiles of BM, which a wave counts
+// with one group per lane.
+template <int BM>
+__device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
+  const int lane = threadIdx.x & 63;
+  Place t{-1, 0, 0, 0, 0, 0};
+  int ni = 0, lo = 0, hi = 0, incl = 0;
+  auto scan = [&](int base) {  // inclusive count over 64 groups from base on
+    lo = hi = 0;
+    if (base + lane < a.groups) rows_of(a, base + lane, &lo, &hi);
+    incl = (hi - lo + BM - 1) / BM;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int x = __shfl_up(incl, d);
+      if (lane >= d) incl += x;
+    }
+    return __builtin_amdgcn_readlane(incl, 63);
+  };
+  for (int base = 0; base < a.groups; base += 64) ni += scan(base);
+  const int total = ni * nj, per = (total + kXcds - 1) / kXcds;
+  const int id = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
+  if (static_cast<int>(blockIdx.x / kXcds) >= per || id >= total) return t;
+  int i, j;
+  if (!in_band(id, ni, nj, &i, &j)) return t;
+  for (int base = 0, before = 0; base < a.groups; base += 64) {
+    const int here = a.groups > 64 ? scan(base) : ni;
+    const uint64_t past = __ballot(before + incl > i);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      t.lo = __builtin_amdgcn_readlane(lo, l);
+      t.hi = __builtin_amdgcn_readlane(hi, l);
+      const int tiles = (t.hi - t.lo + BM - 1) / BM;
+      t.i = i - before - (__builtin_amdgcn_readlane(incl, l) - tiles);
+      t.j = j;
+      if (t.i >= 0 && t.i < tiles) t.group = base + l;
+      return t;
+    }
+    before += here;
+  }
+  return t;
+}
+
+// Tiles of TN: ni x nj of every group, each in a.n_parts parts.  The dies share
+// every group, as groups differ in length.
+__device__ __forceinline__ Place weight_tile(const ProductArgs& a, int ni, int nj) {
+  Place t{-1, 0, 0, 0, 0, 0};
+  const int tiles = ni * nj, all = tiles * a.n_parts, per = (all + kXcds - 1) / kXcds;
+  const int q = blockIdx.x / kXcds, g = q / per;
+  if (g >= a.groups) return t;
+  const int die = (blockIdx.x + static_cast<uint32_t>(g) * static_cast<uint32_t>(all)) % kXcds;
+  const int id = die * per + q % per;
+  if (id >= all) return t;
+  t.part = id / tiles;
+  if (!in_band(id % tiles, ni, nj, &t.i, &t.j)) return t;
+  rows_of(a, g, &t.lo, &t.hi);
+  t.group = g;
+  return t;
+}
+
+// ------------------------------------------------------------------ results
+// Four adjacent results of a row, as they are and with what is there.
+template <bool F32>
+__device__ __forceinline__ void store4(void* c, int64_t at, f4 x, int have, bool add) {
+  if constexpr (F32) {
+    typedef f4 any __attribute__((aligned(4)));
+    float* p = static_cast<float*>(c) + at;
+    if (have >= 4) {
+      if (add) x += *reinterpret_cast<const any*>(p);
+      *reinterpret_cast<any*>(p) = x;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 3; ++r)
+        if (r < have) p[r] = add ? p[r] + x[r] : x[r];
+    }
+  } else {
+    typedef u2 any __attribute__((aligned(2)));
+    u16* p = static_cast<u16*>(c) + at;
+    if (have >= 4) {
+      if (add) {
+        const u2 o = *reinterpret_cast<const any*>(p);
+        x += f4{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xffff0000u),
+                __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xffff0000u)};
+      }
+      *reinterpret_cast<any*>(p) = __builtin_bit_cast(u2, __builtin_convertvector(x, b4));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 3; ++r)
+        if (r < have)
+          p[r] = static_cast<u16>(f32_to_bf16(add ? x[r] + bf16_to_f32(p[r]) : x[r]));
+    }
+  }
+}
+__device__ __forceinline__ void store4(const ProductArgs& a, int64_t at, f4 x, int have) {
+  if (a.out_f32)
+    store4<true>(a.c, at, x, have, a.accumulate);
+  else
+    store4<false>(a.c, at, x, have, a.accumulate);
+}
+
+// A wave's results: acc[i][j][r] is row r0 + 16 i + lane % 16, column c0 + 16 j
+// + 4 (lane / 16) + r of what begins at `to`; rows x cols of it exist.
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void finish(const ProductArgs& a, const typename T::Acc (&acc)[FM][FN],
+                                       int64_t to, int r0, int c0, int rows, int cols,
+                                       const float* sa, const float* sb) {
+  const int lane = threadIdx.x & 63;
+  const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 4;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (r + i * 16 >= rows) continue;
+    float s = 1.f;
+    if constexpr (T::kBytes == 1) s = sa[r + i * 16];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const int have = cols - (c + j * 16);
+      if (have <= 0) continue;
+      f4 x;
+      if constexpr (T::kBytes == 1) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = static_cast<float>(acc[i][j][e]) * s;
+          if (sb) x[e] *= sb[c + j * 16 + (e < have ? e : 0)];
+        }
+      } else {
+        x = acc[i][j];
+      }
+      store4(a, to + (r + i * 16) * a.ldc + c + j * 16, x, have);
+    }
+  }
+}
+
+// ------------------------------------------------------------- the tile loop
+// One tile, all waves on the same rounds of 128 bytes of the sum.  The products
+// of one half of a round are issued row by row with the LDS reads of the next
+// half and the loads of a later round between them.
+template <typename T, typename S, int OP, bool DIRECT>
+__global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a) {
+  constexpr int FM = S::FM, FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
+  constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
+  constexpr int kSum = kRow / T::kBytes;
+  using Acc = typename T::Acc;
+  __shared__ __align__(1024) char lds[S::RoundBytes * NS];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  // P's rows and Q's are the result's rows and columns
+  const int prows = OP == FSDP_MATMUL_TN ? a.n : 0, qrows = OP == FSDP_MATMUL_TN ? a.k : a.n;
+  const int nj = (qrows + S::BN - 1) / S::BN;
+  const Place t = OP == FSDP_MATMUL_TN ? weight_tile(a, (prows + S::BM - 1) / S::BM, nj)
+                                       : ragged_tile<S::BM>(a, nj);
+  if (t.group < 0) return;
+  const int i0 = t.i * S::BM, j0 = t.j * S::BN;
+
+  Operand po, qo;
+  int64_t to;
+  const char* ab = static_cast<const char*>(a.a);
+  const char* bb = static_cast<const char*>(a.b);
+  constexpr int B = T::kBytes;
+  if constexpr (OP == FSDP_MATMUL_TN) {
+    // this part's rows of the group, whole rounds but for the last
+    const int rounds = (t.hi - t.lo + kSum - 1) / kSum;
+    const int from = static_cast<int>(int64_t(rounds) * t.part / a.n_parts) * kSum;
+    int end = static_cast<int>(int64_t(rounds) * (t.part + 1) / a.n_parts) * kSum;
+    if (end > t.hi - t.lo) end = t.hi - t.lo;
+    const int64_t row = t.lo + from;
+    po = Operand{ab + (row * a.lda + i0) * B, a.lda * B, a.n - i0, end - from};
+    qo = Operand{bb + (row * a.ldb + j0) * B, a.ldb * B, a.k - j0, end - from};
+    to = t.group * a.group_stride + i0 * a.ldc + j0;
+  } else {
+    const int64_t row = t.lo + i0;
+    po = Operand{ab + row * a.lda * B, a.lda * B, t.hi - t.lo - i0, a.k};
+    const char* b = bb + t.group * a.group_stride * B;
+    if constexpr (OP == FSDP_MATMUL_NT)
+      qo = Operand{b + j0 * a.ldb * B, a.ldb * B, a.n - j0, a.k};
+    else
+      qo = Operand{b + int64_t(j0) * B, a.ldb * B, a.n - j0, a.k};
+    to = row * a.ldc + j0;
+  }
+  const int total = (po.sum + kSum - 1) / kSum;
+  if (OP == FSDP_MATMUL_TN && total == 0 && a.accumulate && a.n_parts == 1) return;
+
+  std::conditional_t<DIRECT, Direct<T, S::BM, LP, PA>, Staged<T, S::BM, LP, PA>> pl;
+  std::conditional_t<DIRECT, Direct<T, S::BN, LQ, QA>, Staged<T, S::BN, LQ, QA>> ql;
+  pl.begin(po, wave);
+  ql.begin(qo, wave);
+  const Fetch<T, S::BM, FM, PA> pf(wm * S::TM);
+  const Fetch<T, S::BN, FN, QA> qf(wn * S::TN);
+  const uint32_t lds0 = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+
+  Acc acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
+
+  auto load = [&](int round, int buf, int x) {
+    if constexpr (DIRECT) {
+      if (x < LP)
+        pl.load(round, lds0 + buf * S::RoundBytes, x < LP ? x : 0);
+      else
+        ql.load(round, lds0 + buf * S::RoundBytes + S::BM * kRow, x < LP ? 0 : x - LP);
+    }
+  };
+  u4 p[2][FM], q[2][FN];
+  auto products = [&](int set, int buf, int kk, auto loads, int round, int into) {
+    constexpr int kFetch = FM + FN, kLoad = LP + LQ;
+    const char* image = lds + buf * S::RoundBytes;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int x = i * kFetch / FM; x < (i + 1) * kFetch / FM; ++x) {
+        if (x < FN)
+          q[set ^ 1][x] = qf.get(image + S::BM * kRow, kk, x);
+        else
+          p[set ^ 1][x - FN] = pf.get(image, kk, x - FN);
+      }
+      if constexpr (decltype(loads)::value) {
+#pragma unroll
+        for (int x = i * kLoad / FM; x < (i + 1) * kLoad / FM; ++x) load(round, into, x);
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = T::mma(q[set][j], p[set][i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  if (total > 0) {
+    if constexpr (DIRECT) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        if (s < total) {
+#pragma unroll
+          for (int x = 0; x < LP + LQ; ++x) load(s, s, x);
+        }
+      if (total >= NS)
+        wait_and_meet<(NS - 1) * (LP + LQ)>();
+      else
+        wait_and_meet<0>();
+    } else {
+      for (int s = 0; s < NS; ++s) {
+        pl.fetch(s);
+        ql.fetch(s);
+        pl.put(lds + s * S::RoundBytes);
+        ql.put(lds + s * S::RoundBytes + S::BM * kRow);
+      }
+      __syncthreads();
+      pl.fetch(NS);
+      ql.fetch(NS);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) q[0][j] = qf.get(lds + S::BM * kRow, 0, j);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) p[0][i] = pf.get(lds, 0, i);
+    // Before a round's last half: the next round has landed for every wave, and
+    // every wave is done reading this one, whose buffer is loaded again.  The
+    // last round reads operands that nothing uses.
+    int buf = 0;
+    auto one = [&](int it, auto loads) {
+      const int next = buf + 1 == NS ? 0 : buf + 1;
+      wait_lds();  // set 0: asked for half a round ago
+      products(0, buf, 1, std::false_type{}, 0, 0);
+      if constexpr (DIRECT) {
+        wait_and_meet<decltype(loads)::value ? (NS - 2) * (LP + LQ) : 0>();
+        products(1, next, 0, loads, it + NS, buf);
+      } else {
+        __syncthreads();
+        if (decltype(loads)::value) {
+          pl.put(lds + buf * S::RoundBytes);
+          ql.put(lds + buf * S::RoundBytes + S::BM * kRow);
+          pl.fetch(it + NS + 1);
+          ql.fetch(it + NS + 1);
+        }
+        products(1, next, 0, std::false_type{}, 0, 0);
+      }
+      buf = next;
+    };
+    int it = 0;
+    for (; it + NS < total; ++it) one(it, std::true_type{});
+    for (; it < total; ++it) one(it, std::false_type{});
+  }
+
+  if constexpr (OP == FSDP_MATMUL_TN) {
+    if (a.n_parts > 1) {
+      const int tiles = ((prows + S::BM - 1) / S::BM) * nj;
+      const int64_t at =
+          ((int64_t(t.group) * tiles + t.i * nj + t.j) * a.n_parts + t.part) * (FM * FN * S::Threads);
+      f4* part = reinterpret_cast<f4*>(a.parts) + at + threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) part[(i * FN + j) * S::Threads] = acc[i][j];
+      return;
+    }
+  }
+  if constexpr (T::kBytes == 1) {
+    finish<T>(a, acc, to, wm * S::TM, wn * S::TN, po.side, qo.side, a.sa + t.lo + i0,
+              a.sb ? a.sb + t.group * a.sb_stride + j0 : nullptr);
+  } else {
+    finish<T>(a, acc, to, wm * S::TM, wn * S::TN, po.side, qo.side, nullptr, nullptr);
+  }
+}
+
+// A weight gradient's tiles that came in parts, added up in their order.
+template <typename S>
+__global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
+  constexpr int FM = S::FM, FN = S::FN;
+  const int ni = (a.n + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
+  const int g = blockIdx.x / (ni * nj), id = blockIdx.x % (ni * nj);
+  const int i0 = id / nj * S::BM, j0 = id % nj * S::BN;
+  const int wave = threadIdx.x >> 6;
+  const f4* part = reinterpret_cast<const f4*>(a.parts) +
+                   int64_t(blockIdx.x) * a.n_parts * (FM * FN * S::Threads) + threadIdx.x;
+  f4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = part[(i * FN + j) * S::Threads];
+  for (int p = 1; p < a.n_parts; ++p) {
+    part += FM * FN * S::Threads;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] += part[(i * FN + j) * S::Threads];
+  }
+  finish<Bf16>(a, acc, g * a.group_stride + int64_t(i0) * a.ldc + j0, wave / S::WN * S::TM,
+               wave % S::WN * S::TN, a.n - i0, a.k - j0, nullptr, nullptr);
+}
+
+// ---------------------------------------------------------------------- fp32
+// fp32 operands, one 64 x 64 tile by four waves of 32 x 32, 16 of the sum per
+// round.  Both operands are kept in LDS as rows across the sum, which is how
+// the matrix instruction reads single entries.
+template <int OP>
+__global__ __launch_bounds__(256) void k_product_f32(ProductArgs a) {
+  constexpr int BM = 64, BK = 16, LD = BM + 16;
+  __shared__ float ps[2][BK][LD], qs[2][BK][LD];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int qrows = OP == FSDP_MATMUL_TN ? a.k : a.n;
+  const int nj = (qrows + BM - 1) / BM;
+  const Place t = OP == FSDP_MATMUL_TN ? weight_tile(a, (a.n + BM - 1) / BM, nj)
+                                       : ragged_tile<BM>(a, nj);
+  if (t.group < 0) return;
+  const int i0 = t.i * BM, j0 = t.j * BM;
+  const float* pa = static_cast<const float*>(a.a);
+  const float* qb = static_cast<const float*>(a.b);
+  int64_t to;
+  int pside, sum;
+  const int qside = qrows - j0;
+  if (OP == FSDP_MATMUL_TN) {
+    const int rounds = (t.hi - t.lo + BK - 1) / BK;
+    const int from = static_cast<int>(int64_t(rounds) * t.part / a.n_parts) * BK;
+    int end = static_cast<int>(int64_t(rounds) * (t.part + 1) / a.n_parts) * BK;
+    if (end > t.hi - t.lo) end = t.hi - t.lo;
+    pa += (t.lo + from) * a.lda + i0;
+    qb += (t.lo + from) * a.ldb + j0;
+    pside = a.n - i0;
+    sum = end - from;
+    to = t.group * a.group_stride + i0 * a.ldc + j0;
+  } else {
+    pa += (t.lo + i0) * a.lda;
+    qb += t.group * a.group_stride + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0));
+    pside = t.hi - t.lo - i0;
+    sum = a.k;
+    to = (t.lo + i0) * a.ldc + j0;
+  }
+  if (OP == FSDP_MATMUL_TN && sum == 0 && a.accumulate) return;
+  // 64 x 16 entries of an operand: four per lane, adjacent in memory where
+  // its rows lie across the sum, along it otherwise
+  auto fetch = [&](const float* p, int64_t ld, int side, bool across, int s0, float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = across ? threadIdx.x % 64 : threadIdx.x / 16 + 16 * e;
+      const int s = s0 + (across ? threadIdx.x / 64 + 4 * e : threadIdx.x % 16);
+      v[e] = 0.f;
+      if (r < side && s < sum) v[e] = across ? p[s * ld + r] : p[r * ld + s];
+    }
+  };
+  auto put = [&](float (*to_)[LD], bool across, const float (&v)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (across)
+        to_[threadIdx.x / 64 + 4 * e][threadIdx.x % 64] = v[e];
+      else
+        to_[threadIdx.x % 16][threadIdx.x / 16 + 16 * e] = v[e];
+    }
+  };
+  constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
+  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
+  f4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  float pv[4], qv[4];
+  fetch(pa, a.lda, pside, PA, 0, pv);
+  fetch(qb, a.ldb, qside, QA, 0, qv);
+  int buf = 0;
+  for (int s = 0; s < sum; s += BK, buf ^= 1) {
+    put(ps[buf], PA, pv);
+    put(qs[buf], QA, qv);
+    __syncthreads();
+    fetch(pa, a.lda, pside, PA, s + BK, pv);
+    fetch(qb, a.ldb, qside, QA, s + BK, qv);
+#pragma unroll
+    for (int kk = 0; kk < BK; kk += 4) {
+      float p[2], q[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p[i] = ps[buf][kk + (lane >> 4)][wm + i * 16 + (lane & 15)];
+        q[i] = qs[buf][kk + (lane >> 4)][wn + i * 16 + (lane & 15)];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[j], p[i], acc[i][j], 0, 0, 0);
+    }
+  }
+  finish<Bf16>(a, acc, to, wm, wn, pside, qside, nullptr, nullptr);
+}
+
+// ---------------------------------------------------------------- launchers
+using Small = Tile<64, 64, 2, 2, 3, 2>;
+using Mid = Tile<128, 128, 2, 2, 2, 2>;
+using Big = Tile<256, 256, 2, 4, 2, 2>;
+static_assert(Small::BM == kProductTiles[0] && Mid::BM == kProductTiles[1] &&
+              Big::BM == kProductTiles[2]);
+
+template <typename T, typename S, int OP, bool DIRECT>
+hipError_t launch_tile(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
+  ProductArgs a = args;
+  void* p[] = {&a};
+  hipError_t e = sink.launch(reinterpret_cast<const void*>(&k_product<T, S, OP, DIRECT>),
+                             dim3(static_cast<unsigned>(rule.grid)), dim3(S::Threads), p, 0);
+  if constexpr (OP == FSDP_MATMUL_TN) {
+    if (e == hipSuccess && rule.n_parts > 1)
+      e = sink.launch(reinterpret_cast<const void*>(&k_join_parts<S>),
+                      dim3(static_cast<unsigned>(rule.join)), dim3(S::Threads), p, 0);
+  }
+  return e;
+}
+
+template <typename T, int OP>
+hipError_t launch_op(const ProductArgs& a, const ProductRule& rule, const Sink& sink) {
+  if constexpr (T::kBytes == 2) {
+    if (!rule.direct) {
+      if (rule.tile == 0) return launch_tile<T, Small, OP, false>(a, rule, sink);
+      return launch_tile<T, Mid, OP, false>(a, rule, sink);
+    }
+  }
+  switch (rule.tile) {
+    case 0: return launch_tile<T, Small, OP, true>(a, rule, sink);
+    case 1: return launch_tile<T, Mid, OP, true>(a, rule, sink);
+    default: return launch_tile<T, Big, OP, true>(a, rule, sink);
+  }
+}
+
+template <int OP>
+hipError_t launch_f32(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
+  ProductArgs a = args;
+  void* p[] = {&a};
+  return sink.launch(reinterpret_cast<const void*>(&k_product_f32<OP>),
+                     dim3(static_cast<unsigned>(rule.grid)), dim3(256), p, 0);
+}
+
+}  // namespace
+
+hipError_t launch_product(const ProductArgs& a, ProductType type, int32_t op,
+                          const ProductRule& rule, const Sink& sink) {
+  switch (type) {
+    case kProductF32:
+      switch (op) {
+        case FSDP_MATMUL_NT: return launch_f32<FSDP_MATMUL_NT>(a, rule, sink);
+        case FSDP_MATMUL_NN: return launch_f32<FSDP_MATMUL_NN>(a, rule, sink);
+        default: return launch_f32<FSDP_MATMUL_TN>(a, rule, sink);
+      }
+    case kProductBf16:
+      switch (op) {
+        case FSDP_MATMUL_NT: return launch_op<Bf16, FSDP_MATMUL_NT>(a, rule, sink);
+        case FSDP_MATMUL_NN: return launch_op<Bf16, FSDP_MATMUL_NN>(a, rule, sink);
+        default: return launch_op<Bf16, FSDP_MATMUL_TN>(a, rule, sink);
+      }
+    default:
+      if (op == FSDP_MATMUL_NT) return launch_op<I8, FSDP_MATMUL_NT>(a, rule, sink);
+      return launch_op<I8, FSDP_MATMUL_NN>(a, rule, sink);
+  }
+}
+
+}  // namespace fsdp

@@ -539,6 +539,153 @@ fsdp_status fsdp_muon_shard_step(const fsdp_muon* mu, const fsdp_muon_hparams* h
                                  float* m, float* v, void* param_out, int32_t param_dtype,
                                  void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The unit's matrix products: what a rank computes with the weights that it
+ * gathered, and the gradients that the reduce-scatter takes ("Understanding
+ * FSDP from source" 2.2 and 4.4: a linear layer's forward, input gradient
+ * and weight gradient between the gather and the reduce-scatter).
+ *
+ * Weights are read where the gather left them (a parameter of two
+ * dimensions, or of three: one matrix per expert) and their gradients are
+ * written where the reduce-scatter reads them, in the rank's replica.
+ *
+ * The rows of the activations are sorted by group: group g has rows
+ * offsets[g] to offsets[g + 1], offsets being groups + 1 ascending numbers
+ * in device memory, read when the product runs (a router's counts need not
+ * reach the host).  Groups may be empty.  Rows before offsets[0] and behind
+ * offsets[groups] belong to none: they are not read, and results there are
+ * left as they are.  Offsets that do not ascend or leave [0, rows] give
+ * undefined results, and no access outside the arrays.
+ * --------------------------------------------------------------------- */
+enum {
+  FSDP_MATMUL_NT = 0, /* C[t,n] = sum_k A[t,k] B_g[n,k]   t: rows, g: t's group */
+  FSDP_MATMUL_NN = 1, /* C[t,n] = sum_k A[t,k] B_g[k,n]                         */
+  FSDP_MATMUL_TN = 2  /* C_g[n,k] = sum_t A[t,n] B[t,k]   over the rows t of g  */
+};
+
+/* For weights [out, in]: the forward pass is NT (n = out, k = in), the input
+ * gradient NN (n = in, k = out), the weight gradient TN of the output's
+ * gradient with the input (n = out, k = in).  For weights [in, out]: NN, NT,
+ * and TN of the input with the output's gradient. */
+typedef struct fsdp_matmul {
+  int32_t op;           /* FSDP_MATMUL_* */
+  int32_t groups;       /* >= 1 */
+  int64_t rows;         /* >= 0 */
+  int64_t n, k;         /* >= 1 */
+  int64_t lda, ldb, ldc; /* elements from one row to the next, at least a row */
+  int64_t group_stride; /* elements from one group's matrix to the next: B's
+                           (NT, NN; 0 shares one), or C's (TN) */
+  int32_t accumulate;   /* 0: C = the product; 1: C = C + the product */
+  int32_t reserved;     /* not read */
+} fsdp_matmul;
+
+/* Bytes of the workspace that fsdp_grouped_matmul takes for these sizes and
+ * operands of dtype (0 for most: only long sums of few results use one). */
+fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, int64_t* bytes);
+
+/* The product of bf16 or fp32 operands (both of dtype).  Sums are fp32, in a
+ * fixed order; with accumulate they are added to C in fp32; the result is
+ * rounded once to out_dtype.  A group without rows gives a weight gradient
+ * of zeros (accumulate: leaves it).
+ *   offsets may be NULL with one group: all rows.  Rows may begin anywhere;
+ *   bf16 operands whose rows begin and end at multiples of 16 bytes take a
+ *   faster path.  C overlaps neither operand, nor offsets, nor itself.
+ *   workspace: as fsdp_grouped_matmul_workspace says, 256-byte aligned
+ *   (NULL where it says 0), contents undefined before and after; calls that
+ *   may overlap in time (other streams, replays of captured graphs) need
+ *   one each.
+ *   FSDP_ERR_UNSUPPORTED: more than 65,536 groups, sizes of 2^30 or more, or
+ *   more work than one launch's grid takes. */
+fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, const void* a,
+                                const void* b, int32_t dtype, void* c, int32_t out_dtype,
+                                void* workspace, int64_t workspace_bytes, void* stream);
+
+/* The product of 8-bit codes (FSDP_MATMUL_NT or NN), each row of A with a
+ * scale, and each n with one per group or none (b_scale NULL):
+ *   C[t,n] = (sum_k A[t,k] B_g[..]) a_scale[t] b_scale[g b_scale_stride + n]
+ * The sum is exact (32-bit integers), its product with the scales fp32, left
+ * to right, and the result rounded once to out_dtype.  NT with codes of
+ * weights [out, in] is the forward pass.  Their input gradient is NN: as the
+ * weights' scales then lie along the sum, fsdp_quantize_rows takes them into
+ * A first (its `channel`), and b_scale is NULL.
+ *   Codes' rows begin at multiples of 16 bytes, are readable to the next
+ *   multiple of 16 behind their end, and A's are zero there
+ *   (fsdp_quantize_rows and fsdp_gather_quantize leave them so).
+ *   k is at most 131,072, rows of codes shorter than 8 MiB (else
+ *   FSDP_ERR_UNSUPPORTED); otherwise as fsdp_grouped_matmul. */
+fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets, const int8_t* a,
+                                   const float* a_scale, const int8_t* b, const float* b_scale,
+                                   int64_t b_scale_stride, void* c, int32_t out_dtype,
+                                   void* stream);
+
+/* Rows in 8 bits: with x' = x, or x' = x channel[g channel_stride + column]
+ * (fp32) where channel is given, a = max |x'| over the row,
+ *   scale = a / 127,  code = x' (127 / a)  rounded to nearest, ties to even
+ * both divisions and the product rounded to fp32.  A row whose a is below
+ * 2^-100 gives zeros and the scale 0, one that holds an infinity or a NaN
+ * zeros and the scale NaN (so its results are NaN, and no others).
+ *   x: rows x cols of dtype, ldx elements from row to row; codes: ldc bytes
+ *   from row to row, 16-byte aligned, ldc a multiple of 16 and at least cols
+ *   rounded up to one; the bytes from cols to there are set to 0.  scales:
+ *   fp32 [rows].  groups, offsets: as above (channel's groups; rows of no
+ *   group are left as they are); offsets NULL with one group: all rows. */
+fsdp_status fsdp_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64_t cols,
+                               int64_t ldx, const float* channel, int64_t channel_stride,
+                               const int32_t* offsets, int32_t groups, int8_t* codes, int64_t ldc,
+                               float* scales, void* stream);
+
+/* ---- The all-gather in 8 bits: a unit's matrices as codes and scales. ---- */
+
+typedef struct fsdp_quant fsdp_quant; /* opaque; immutable once created */
+
+/* Choose the parameters of `plan` that travel in 8 bits: n_params >= 1
+ * distinct indices, each of a parameter of at least two dimensions (else
+ * FSDP_ERR_INVALID_ARG).  Every row along the parameter's last dimension has
+ * a scale.  Host only; *out owns a new object, freed by fsdp_quant_destroy;
+ * the plan may be destroyed afterwards.  FSDP_ERR_UNSUPPORTED when a call's
+ * work would not fit one launch's grid.
+ *   A receiver has three buffers: codes (code_bytes, the chosen parameters
+ *   one after the other, rows `pitch` bytes apart), scales (fp32, one per
+ *   row, in the same order) and rest (the other parameters' elements, one
+ *   after the other). */
+fsdp_status fsdp_quant_plan(const fsdp_plan* plan, int32_t n_params, const int32_t* params,
+                            fsdp_quant** out);
+/* Free it with its device tables.  No call using it may still be in flight.
+ * NULL is ignored. */
+void fsdp_quant_destroy(fsdp_quant* qu);
+/* Upload its work tables to the current device now (synchronous).  Optional:
+ * the calls below do it on first use; needed before a capture. */
+fsdp_status fsdp_quant_prepare(const fsdp_quant* qu, void* stream);
+/* out[3] = {code_bytes, scales, elements of rest}. */
+fsdp_status fsdp_quant_sizes(const fsdp_quant* qu, int64_t* out);
+/* out[5] of parameter p = {first code's byte, rows, columns, pitch, first
+ * scale}, or, of one that is not chosen, {-1, first element in rest, its
+ * number of elements, 0, 0}. */
+fsdp_status fsdp_quant_param(const fsdp_quant* qu, int32_t p, int64_t* out);
+
+/* All-gather + quantise: every receiver gets the unit's chosen matrices as
+ * codes and scales (as fsdp_quantize_rows makes them of the shards' values)
+ * and the other parameters' elements, bit for bit.  fsdp_gather_unflatten with
+ * one byte per element to send.
+ *   shards: [R][S] of dtype.  codes, scales, rest: host arrays of R device
+ *   pointers; a receiver with codes NULL is skipped (its others are not
+ *   looked at).  rest may be NULL, or hold NULLs, where the unit has no other
+ *   parameters.  codes 16-byte aligned; the receivers' buffers are pairwise
+ *   disjoint and disjoint from the shards. */
+fsdp_status fsdp_gather_quantize(const fsdp_quant* qu, const void* shards, int32_t dtype,
+                                 int8_t* const* codes, float* const* scales, void* const* rest,
+                                 void* stream);
+
+/* Read units back: full_out[r] [T] of out_dtype gets code times scale for the
+ * chosen parameters (fp32, rounded once for FSDP_BF16) and the elements of
+ * rest (of rest_dtype) for the others.  Receivers with full_out NULL are
+ * skipped.  full_out are pairwise disjoint and disjoint from what is read;
+ * receivers may share what they read. */
+fsdp_status fsdp_dequantize(const fsdp_quant* qu, const int8_t* const* codes,
+                            const float* const* scales, const void* const* rest,
+                            int32_t rest_dtype, void* const* full_out, int32_t out_dtype,
+                            void* stream);
+
 /* Static, human-readable name of a status code (an fsdp_status value; any
  * other number gives "unknown status"). */
 const char* fsdp_status_string(int32_t status);
