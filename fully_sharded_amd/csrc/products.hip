@@ -348,75 +348,108 @@ __device__ __forceinline__ Place weight_tile(const ProductArgs& a, int ni, int n
 }
 
 // ------------------------------------------------------------------ results
-// Four adjacent results of a row, as they are and with what is there.
-template <bool F32>
-__device__ __forceinline__ void store4(void* c, int64_t at, f4 x, int have, bool add) {
+// N adjacent results of a row (4 in fp32, 8 in bf16: 16 bytes), as they are or
+// with what is there, `have` of them; they may begin anywhere.
+template <bool F32, int N>
+__device__ __forceinline__ void store_row(void* c, int64_t at, float (&x)[N], int have, bool add) {
+  static_assert(N == (F32 ? 4 : 8));
   if constexpr (F32) {
     typedef f4 any __attribute__((aligned(4)));
     float* p = static_cast<float*>(c) + at;
-    if (have >= 4) {
-      if (add) x += *reinterpret_cast<const any*>(p);
-      *reinterpret_cast<any*>(p) = x;
+    if (have >= N) {
+      f4 v = {x[0], x[1], x[2], x[3]};
+      if (add) v += *reinterpret_cast<const any*>(p);
+      *reinterpret_cast<any*>(p) = v;
     } else {
 #pragma unroll
-      for (int r = 0; r < 3; ++r)
-        if (r < have) p[r] = add ? p[r] + x[r] : x[r];
+      for (int e = 0; e < N - 1; ++e)
+        if (e < have) p[e] = add ? p[e] + x[e] : x[e];
     }
   } else {
-    typedef u2 any __attribute__((aligned(2)));
+    typedef u4 any __attribute__((aligned(2)));
     u16* p = static_cast<u16*>(c) + at;
-    if (have >= 4) {
+    if (have >= N) {
       if (add) {
-        const u2 o = *reinterpret_cast<const any*>(p);
-        x += f4{__uint_as_float(o.x << 16), __uint_as_float(o.x & 0xffff0000u),
-                __uint_as_float(o.y << 16), __uint_as_float(o.y & 0xffff0000u)};
-      }
-      *reinterpret_cast<any*>(p) = __builtin_bit_cast(u2, __builtin_convertvector(x, b4));
-    } else {
-#pragma unroll
-      for (int r = 0; r < 3; ++r)
-        if (r < have)
-          p[r] = static_cast<u16>(f32_to_bf16(add ? x[r] + bf16_to_f32(p[r]) : x[r]));
-    }
-  }
-}
-__device__ __forceinline__ void store4(const ProductArgs& a, int64_t at, f4 x, int have) {
-  if (a.out_f32)
-    store4<true>(a.c, at, x, have, a.accumulate);
-  else
-    store4<false>(a.c, at, x, have, a.accumulate);
-}
-
-// A wave's results: acc[i][j][r] is row r0 + 16 i + lane % 16, column c0 + 16 j
-// + 4 (lane / 16) + r of what begins at `to`; rows x cols of it exist.
-template <typename T, int FM, int FN>
-__device__ __forceinline__ void finish(const ProductArgs& a, const typename T::Acc (&acc)[FM][FN],
-                                       int64_t to, int r0, int c0, int rows, int cols,
-                                       const float* sa, const float* sb) {
-  const int lane = threadIdx.x & 63;
-  const int r = r0 + (lane & 15), c = c0 + (lane >> 4) * 4;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    if (r + i * 16 >= rows) continue;
-    float s = 1.f;
-    if constexpr (T::kBytes == 1) s = sa[r + i * 16];
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      const int have = cols - (c + j * 16);
-      if (have <= 0) continue;
-      f4 x;
-      if constexpr (T::kBytes == 1) {
+        const u4 o = *reinterpret_cast<const any*>(p);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          x[e] = static_cast<float>(acc[i][j][e]) * s;
-          if (sb) x[e] *= sb[c + j * 16 + (e < have ? e : 0)];
+          x[2 * e] += __uint_as_float(o[e] << 16);
+          x[2 * e + 1] += __uint_as_float(o[e] & 0xffff0000u);
         }
-      } else {
-        x = acc[i][j];
       }
-      store4(a, to + (r + i * 16) * a.ldc + c + j * 16, x, have);
+      typedef float f8 __attribute__((ext_vector_type(8)));
+      const f8 v = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+      *reinterpret_cast<any*>(p) = __builtin_bit_cast(u4, __builtin_convertvector(v, b8));
+    } else {
+#pragma unroll
+      for (int e = 0; e < N - 1; ++e)
+        if (e < have)
+          p[e] = static_cast<u16>(f32_to_bf16(add ? x[e] + bf16_to_f32(p[e]) : x[e]));
     }
   }
+}
+
+// A wave's results: entry e of acc[i][j] is row r0 + 16 i + lane % 16, column c0 +
+// 16 j + 4 (lane / 16) + e of what begins at `to`; rows x cols of it exist.  16
+// rows at a time pass through LDS (kStage floats of this wave's own), so that
+// memory gets whole lines: stored as the lanes hold them, 32 bytes of 16 rows
+// at a time, a 256 x 256 tile's end took xx us longer.
+template <int FN>
+constexpr int kStage = 16 * (FN * 16 + 4);
+
+template <typename T, bool F32, int FM, int FN>
+__device__ __forceinline__ void finish_as(const ProductArgs& a,
+                                          const typename T::Acc (&acc)[FM][FN], float* stage,
+                                          int64_t to, int r0, int c0, int rows, int cols,
+                                          const float* sa, const float* sb) {
+  constexpr int kCols = FN * 16, kPitch = kCols + 4, kN = F32 ? 4 : 8;
+  constexpr int kPerRow = kCols / kN, kAtOnce = 64 / kPerRow;  // lanes and rows of a store
+  static_assert(kAtOnce <= 16);
+  const int lane = threadIdx.x & 63;
+  const int r = lane / kPerRow, c = lane % kPerRow * kN;
+  const int have = cols - (c0 + c);
+  float scale[kN];
+  if constexpr (T::kBytes == 1) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) scale[e] = sb && e < have ? sb[c0 + c + e] : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      f4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = static_cast<float>(acc[i][j][e]);
+      *reinterpret_cast<f4*>(stage + (lane & 15) * kPitch + j * 16 + (lane >> 4) * 4) = x;
+    }
+#pragma unroll
+    for (int h = 0; h < 16; h += kAtOnce) {
+      const int row = r0 + i * 16 + h + r;
+      float x[kN];
+#pragma unroll
+      for (int e = 0; e < kN; e += 4) {
+        const f4 v = *reinterpret_cast<const f4*>(stage + (h + r) * kPitch + c + e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[e + k] = v[k];
+      }
+      if (row >= rows || have <= 0) continue;
+      if constexpr (T::kBytes == 1) {
+        const float s = sa[row];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) x[e] = x[e] * s * scale[e];
+      }
+      store_row<F32>(a.c, to + row * a.ldc + c0 + c, x, have, a.accumulate);
+    }
+  }
+}
+template <typename T, int FM, int FN>
+__device__ __forceinline__ void finish(const ProductArgs& a, const typename T::Acc (&acc)[FM][FN],
+                                       float* stage, int64_t to, int r0, int c0, int rows,
+                                       int cols, const float* sa, const float* sb) {
+  if (a.out_f32)
+    finish_as<T, true>(a, acc, stage, to, r0, c0, rows, cols, sa, sb);
+  else
+    finish_as<T, false>(a, acc, stage, to, r0, c0, rows, cols, sa, sb);
 }
 
 // ------------------------------------------------------------- the tile loop
@@ -583,11 +616,14 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
       return;
     }
   }
+  static_assert(S::NW * kStage<FN> * 4 <= S::RoundBytes * NS);
+  __syncthreads();  // every wave is done with the operands in LDS
+  float* stage = reinterpret_cast<float*>(lds) + wave * kStage<FN>;
   if constexpr (T::kBytes == 1) {
-    finish<T>(a, acc, to, wm * S::TM, wn * S::TN, po.side, qo.side, a.sa + t.lo + i0,
+    finish<T>(a, acc, stage, to, wm * S::TM, wn * S::TN, po.side, qo.side, a.sa + t.lo + i0,
               a.sb ? a.sb + t.group * a.sb_stride + j0 : nullptr);
   } else {
-    finish<T>(a, acc, to, wm * S::TM, wn * S::TN, po.side, qo.side, nullptr, nullptr);
+    finish<T>(a, acc, stage, to, wm * S::TM, wn * S::TN, po.side, qo.side, nullptr, nullptr);
   }
 }
 
@@ -599,6 +635,7 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
   const int g = blockIdx.x / (ni * nj), id = blockIdx.x % (ni * nj);
   const int i0 = id / nj * S::BM, j0 = id % nj * S::BN;
   const int wave = threadIdx.x >> 6;
+  __shared__ __align__(16) float stage[S::NW * kStage<FN>];
   const f4* part = reinterpret_cast<const f4*>(a.parts) +
                    int64_t(blockIdx.x) * a.n_parts * (FM * FN * S::Threads) + threadIdx.x;
   f4 acc[FM][FN];
@@ -613,7 +650,7 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] += part[(i * FN + j) * S::Threads];
   }
-  finish<Bf16>(a, acc, g * a.group_stride + int64_t(i0) * a.ldc + j0, wave / S::WN * S::TM,
+  finish<Bf16>(a, acc, stage + wave * kStage<FN>, g * a.group_stride + int64_t(i0) * a.ldc + j0, wave / S::WN * S::TM,
                wave % S::WN * S::TN, a.n - i0, a.k - j0, nullptr, nullptr);
 }
 
@@ -707,7 +744,9 @@ __global__ __launch_bounds__(256) void k_product_f32(ProductArgs a) {
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[j], p[i], acc[i][j], 0, 0, 0);
     }
   }
-  finish<Bf16>(a, acc, to, wm, wn, pside, qside, nullptr, nullptr);
+  __syncthreads();
+  static_assert(4 * kStage<2> <= 2 * BK * LD);
+  finish<Bf16>(a, acc, &ps[0][0][0] + wave * kStage<2>, to, wm, wn, pside, qside, nullptr, nullptr);
 }
 
 // ---------------------------------------------------------------- launchers
