@@ -27,23 +27,26 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   const int64_t met = std::max<int64_t>(1, std::min<int64_t>(m.groups, m.rows));
   // tiles about as many as there will be: every group's last row of tiles is
   // half empty
-  auto tiles = [&](int64_t side) {
-    return weight ? m.groups * ceil_div(m.n, side) * ceil_div(m.k, side)
-                  : (met == 1 ? ceil_div(m.rows, side) : m.rows / side + (met + 1) / 2) *
-                        ceil_div(m.n, side);
+  auto tiles = [&](ProductTile t) {
+    const int64_t down = kProductRows[t], across = kProductCols[t];
+    return weight ? m.groups * ceil_div(m.n, down) * ceil_div(m.k, across)
+                  : (met == 1 ? ceil_div(m.rows, down) : m.rows / down + (met + 1) / 2) *
+                        ceil_div(m.n, across);
   };
   r.direct = direct && type != kProductF32;
-  r.tile = 0;
+  r.tile = kSmall;
   if (type != kProductF32) {
-    if (r.direct && tiles(256) >= kCus)
-      r.tile = 2;
-    else if (tiles(128) >= kCus)
-      r.tile = 1;
+    if (r.direct && !weight && m.rows <= 16 * met)
+      r.tile = kThin;
+    else if (r.direct && tiles(kBig) >= (weight ? 2 * kCus : kCus))
+      r.tile = kBig;
+    else if (tiles(kMid) >= kCus)
+      r.tile = r.direct && type == kProductBf16 && tiles(kMid) <= kCus ? kDeep : kMid;
   }
-  const int64_t side = kProductTiles[r.tile];
+  const int64_t down = kProductRows[r.tile], across = kProductCols[r.tile];
   r.n_parts = 1;
   if (weight) {
-    const int64_t per_group = ceil_div(m.n, side) * ceil_div(m.k, side);
+    const int64_t per_group = ceil_div(m.n, down) * ceil_div(m.k, across);
     const int64_t all = per_group * m.groups;
     // long sums of few tiles in parts, eight rounds of 64 rows or more each
     if (type == kProductBf16 && all < kCus)
@@ -51,10 +54,12 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
           1, std::min<int64_t>({2 * kCus / all, m.rows / met / 512, 64})));
     r.grid = kXcds * ceil_div(per_group * r.n_parts, kXcds) * m.groups;
     r.join = all;
-    if (r.n_parts > 1) r.workspace = all * r.n_parts * side * side * 4;
+    if (r.n_parts > 1) r.workspace = all * r.n_parts * down * across * 4;
   } else {
-    const int64_t down = m.groups == 1 ? ceil_div(m.rows, side) : m.rows / side + met;
-    r.grid = kXcds * ceil_div(down * ceil_div(m.n, side), kXcds);
+    const int64_t most = m.groups == 1 ? ceil_div(m.rows, down) : m.rows / down + met;
+    r.grid = kXcds * ceil_div(most * ceil_div(m.n, across), kXcds);
+    // up to half as many tiles as compute units may be cut, in four at most
+    if (r.tile == kBig) r.grid += 3 * kCus / 4;
   }
   return r;
 }

@@ -62,6 +62,19 @@ struct Tile {
   static constexpr int RoundBytes = (BM + BN) * kRow;
 };
 
+using Small = Tile<64, 64, 2, 2, 3, 2>;
+// TN: a wave's results are 64 columns wide, so 16 rows of fp32 ones are 256
+// bytes each (50 and 57 us for 16 groups of 2048 x 512 that are added to).
+template <int OP>
+using Mid = std::conditional_t<OP == FSDP_MATMUL_TN, Tile<128, 128, 4, 2, 2, 4>,
+                               Tile<128, 128, 2, 4, 2, 4>>;
+template <int OP>
+using Deep = std::conditional_t<OP == FSDP_MATMUL_TN, Tile<128, 128, 4, 2, 4, 2>,
+                                Tile<128, 128, 2, 4, 4, 2>>;
+using Big = Tile<256, 256, 2, 4, 2, 2>;
+using Half = Tile<128, 256, 2, 4, 2, 2>;
+using Quarter = Tile<128, 128, 2, 4, 4, 2>;
+
 // The place of 16-byte piece c of row r along the sum: the 16 rows that a wave
 // reads at one piece spread over all banks.
 __device__ __forceinline__ int place(int r, int c) { return c ^ (r & 7); }
@@ -79,7 +92,8 @@ __device__ __forceinline__ int place_across(int r, int c) {
   } else {
     return c ^ (BM == 256  ? (r & 7) | ((r >> 1) & 8)
                 : BM == 128 ? ((r >> 1) & 3) | ((r >> 2) & 4)
-                            : ((r >> 2) & 1) | ((r >> 3) & 2));
+                : BM == 64  ? ((r >> 2) & 1) | ((r >> 3) & 2)
+                            : (r >> 4) & 1);
   }
 }
 
@@ -257,7 +271,8 @@ struct Fetch {
 struct Place {
   int group;       // < 0: none
   int lo, hi;      // its rows
-  int i, j, part;  // the tile
+  int i, j;        // the tile
+  int part, parts; // of it
 };
 
 __device__ __forceinline__ int clamp_to(int x, int lo, int hi) {
@@ -278,7 +293,7 @@ __device__ __forceinline__ void rows_of(const ProductArgs& a, int g, int* lo, in
 // Tiles are numbered along bands of 8 tiles down, column by column, and each of
 // the 8 dies, to which workgroups go in turn, takes a contiguous range: the 32
 // tiles that a die has in flight share 8 panels of A and 4 of B in its L2.
-constexpr int kBand = 8, kXcds = 8;
+constexpr int kBand = 8, kXcds = 8, kCus = 256;
 __device__ __forceinline__ bool in_band(int id, int ni, int nj, int* i, int* j) {
   const int band = id / (kBand * nj), first = band * kBand;
   const int high = ni - first < kBand ? ni - first : kBand;
@@ -290,10 +305,14 @@ __device__ __forceinline__ bool in_band(int id, int ni, int nj, int* i, int* j) 
 
 // Tiles of NT and NN: every group's rows in tiles of BM, which a wave counts
 // with one group per lane.
-template <int BM>
+//   SPLIT: the tiles behind the last that fill all compute units are cut in two
+// or four, t.part being which, where the parts still find a compute unit each:
+// one launch of 1,100 tiles (4.3 per compute unit) of depth 14336 took xx us,
+// and xx without.
+template <int BM, bool SPLIT>
 __device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
   const int lane = threadIdx.x & 63;
-  Place t{-1, 0, 0, 0, 0, 0};
+  Place t{-1, 0, 0, 0, 0, 0, 1};
   int ni = 0, lo = 0, hi = 0, incl = 0;
   auto scan = [&](int base) {  // inclusive count over 64 groups from base on
     lo = hi = 0;
@@ -307,9 +326,28 @@ __device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
     return __builtin_amdgcn_readlane(incl, 63);
   };
   for (int base = 0; base < a.groups; base += 64) ni += scan(base);
-  const int total = ni * nj, per = (total + kXcds - 1) / kXcds;
-  const int id = (blockIdx.x % kXcds) * per + blockIdx.x / kXcds;
-  if (static_cast<int>(blockIdx.x / kXcds) >= per || id >= total) return t;
+  const int total = ni * nj;
+  int whole = total;
+  if constexpr (SPLIT) {
+    const int rest = total % kCus;
+    if (total > kCus && rest > 0 && rest <= kCus / 2) {
+      whole = total - rest;
+      t.parts = rest <= kCus / 4 ? 4 : 2;
+    }
+  }
+  const int b = blockIdx.x;
+  int id;
+  if (b < whole || t.parts == 1) {
+    const int per = (whole + kXcds - 1) / kXcds;
+    id = (b % kXcds) * per + b / kXcds;
+    if (b / kXcds >= per || id >= whole) return t;
+    t.parts = 1;
+  } else {
+    const int rest = total - whole;
+    id = whole + (b - whole) % rest;
+    t.part = (b - whole) / rest;
+    if (t.part >= t.parts) return t;
+  }
   int i, j;
   if (!in_band(id, ni, nj, &i, &j)) return t;
   for (int base = 0, before = 0; base < a.groups; base += 64) {
@@ -333,10 +371,23 @@ __device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
 // Tiles of TN: ni x nj of every group, each in a.n_parts parts.  The dies share
 // every group, as groups differ in length.
 __device__ __forceinline__ Place weight_tile(const ProductArgs& a, int ni, int nj) {
-  Place t{-1, 0, 0, 0, 0, 0};
+  Place t{-1, 0, 0, 0, 0, 0, 1};
   const int tiles = ni * nj, all = tiles * a.n_parts, per = (all + kXcds - 1) / kXcds;
-  const int q = blockIdx.x / kXcds, g = q / per;
+  const int q = blockIdx.x / kXcds;
+  int g = q / per;
   if (g >= a.groups) return t;
+  if (a.offsets && a.groups <= 64) {
+    // the longest groups first: their tiles would otherwise end last
+    const int lane = threadIdx.x & 63;
+    int lo = 0, hi = -1, rank = 0;
+    if (lane < a.groups) rows_of(a, lane, &lo, &hi);
+    const int mine = hi - lo;
+    for (int m = 0; m < a.groups; ++m) {
+      const int other = __builtin_amdgcn_readlane(mine, m);
+      rank += other > mine || (other == mine && m < lane);
+    }
+    g = __builtin_ctzll(__ballot(rank == g));
+  }
   const int die = (blockIdx.x + static_cast<uint32_t>(g) * static_cast<uint32_t>(all)) % kXcds;
   const int id = die * per + q % per;
   if (id >= all) return t;
@@ -348,44 +399,74 @@ __device__ __forceinline__ Place weight_tile(const ProductArgs& a, int ni, int n
 }
 
 // ------------------------------------------------------------------ results
-// N adjacent results of a row (4 in fp32, 8 in bf16: 16 bytes), as they are or
-// with what is there, `have` of them; they may begin anywhere.
-template <bool F32, int N>
-__device__ __forceinline__ void store_row(void* c, int64_t at, float (&x)[N], int have, bool add) {
-  static_assert(N == (F32 ? 4 : 8));
+// N adjacent results of a row (4 in fp32, 8 in bf16: 16 bytes), `have` of them;
+// they may begin anywhere.
+template <bool F32>
+__device__ __forceinline__ u4 load_row(const void* c, int64_t at, int have) {
+  u4 v = {0, 0, 0, 0};
   if constexpr (F32) {
-    typedef f4 any __attribute__((aligned(4)));
-    float* p = static_cast<float*>(c) + at;
-    if (have >= N) {
-      f4 v = {x[0], x[1], x[2], x[3]};
-      if (add) v += *reinterpret_cast<const any*>(p);
-      *reinterpret_cast<any*>(p) = v;
-    } else {
+    typedef u4 any __attribute__((aligned(4)));
+    const uint32_t* p = static_cast<const uint32_t*>(c) + at;
+    if (have >= 4) return *reinterpret_cast<const any*>(p);
 #pragma unroll
-      for (int e = 0; e < N - 1; ++e)
-        if (e < have) p[e] = add ? p[e] + x[e] : x[e];
+    for (int e = 0; e < 3; ++e)
+      if (e < have) v[e] = p[e];
+  } else {
+    typedef u4 any __attribute__((aligned(2)));
+    const u16* p = static_cast<const u16*>(c) + at;
+    if (have >= 8) return *reinterpret_cast<const any*>(p);
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < have) v[e / 2] |= static_cast<uint32_t>(p[e]) << (e % 2 * 16);
+  }
+  return v;
+}
+template <bool F32>
+__device__ __forceinline__ void store_row(void* c, int64_t at, u4 v, int have) {
+  if constexpr (F32) {
+    typedef u4 any __attribute__((aligned(4)));
+    uint32_t* p = static_cast<uint32_t*>(c) + at;
+    if (have >= 4) {
+      *reinterpret_cast<any*>(p) = v;
+      return;
     }
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < have) p[e] = v[e];
   } else {
     typedef u4 any __attribute__((aligned(2)));
     u16* p = static_cast<u16*>(c) + at;
-    if (have >= N) {
-      if (add) {
-        const u4 o = *reinterpret_cast<const any*>(p);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[2 * e] += __uint_as_float(o[e] << 16);
-          x[2 * e + 1] += __uint_as_float(o[e] & 0xffff0000u);
-        }
-      }
-      typedef float f8 __attribute__((ext_vector_type(8)));
-      const f8 v = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-      *reinterpret_cast<any*>(p) = __builtin_bit_cast(u4, __builtin_convertvector(v, b8));
-    } else {
-#pragma unroll
-      for (int e = 0; e < N - 1; ++e)
-        if (e < have)
-          p[e] = static_cast<u16>(f32_to_bf16(add ? x[e] + bf16_to_f32(p[e]) : x[e]));
+    if (have >= 8) {
+      *reinterpret_cast<any*>(p) = v;
+      return;
     }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < have) p[e] = static_cast<u16>(v[e / 2] >> (e % 2 * 16));
+  }
+}
+// Their values in fp32, and back.
+template <bool F32, int N>
+__device__ __forceinline__ void add_row(float (&x)[N], u4 v) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (F32) {
+      x[e] += __uint_as_float(v[e]);
+    } else {
+      x[2 * e] += __uint_as_float(v[e] << 16);
+      x[2 * e + 1] += __uint_as_float(v[e] & 0xffff0000u);
+    }
+  }
+}
+template <bool F32, int N>
+__device__ __forceinline__ u4 pack_row(const float (&x)[N]) {
+  if constexpr (F32) {
+    return u4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+              __float_as_uint(x[3])};
+  } else {
+    typedef float f8 __attribute__((ext_vector_type(8)));
+    const f8 v = {x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+    return __builtin_bit_cast(u4, __builtin_convertvector(v, b8));
   }
 }
 
@@ -413,8 +494,21 @@ __device__ __forceinline__ void finish_as(const ProductArgs& a,
 #pragma unroll
     for (int e = 0; e < kN; ++e) scale[e] = sb && e < have ? sb[c0 + c + e] : 1.f;
   }
+  // what the results are added to is asked for 16 rows ahead
+  constexpr int kStores = 16 / kAtOnce;
+  u4 old[2][kStores];
+  auto ask = [&](int i) {
+#pragma unroll
+    for (int h = 0; h < kStores; ++h) {
+      const int row = r0 + i * 16 + h * kAtOnce + r;
+      if (row < rows && have > 0)
+        old[i & 1][h] = load_row<F32>(a.c, to + row * a.ldc + c0 + c, have);
+    }
+  };
+  if (a.accumulate) ask(0);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
+    if (a.accumulate && i + 1 < FM) ask(i + 1);
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
       f4 x;
@@ -423,12 +517,12 @@ __device__ __forceinline__ void finish_as(const ProductArgs& a,
       *reinterpret_cast<f4*>(stage + (lane & 15) * kPitch + j * 16 + (lane >> 4) * 4) = x;
     }
 #pragma unroll
-    for (int h = 0; h < 16; h += kAtOnce) {
-      const int row = r0 + i * 16 + h + r;
+    for (int h = 0; h < kStores; ++h) {
+      const int row = r0 + i * 16 + h * kAtOnce + r;
       float x[kN];
 #pragma unroll
       for (int e = 0; e < kN; e += 4) {
-        const f4 v = *reinterpret_cast<const f4*>(stage + (h + r) * kPitch + c + e);
+        const f4 v = *reinterpret_cast<const f4*>(stage + (h * kAtOnce + r) * kPitch + c + e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[e + k] = v[k];
       }
@@ -438,7 +532,8 @@ __device__ __forceinline__ void finish_as(const ProductArgs& a,
 #pragma unroll
         for (int e = 0; e < kN; ++e) x[e] = x[e] * s * scale[e];
       }
-      store_row<F32>(a.c, to + row * a.ldc + c0 + c, x, have, a.accumulate);
+      if (a.accumulate) add_row<F32>(x, old[i & 1][h]);
+      store_row<F32>(a.c, to + row * a.ldc + c0 + c, pack_row<F32>(x), have);
     }
   }
 }
@@ -452,33 +547,18 @@ __device__ __forceinline__ void finish(const ProductArgs& a, const typename T::A
     finish_as<T, false>(a, acc, stage, to, r0, c0, rows, cols, sa, sb);
 }
 
-// ------------------------------------------------------------- the tile loop
-// One tile, all waves on the same rounds of 128 bytes of the sum.  The products
-// of one half of a round are issued row by row with the LDS reads of the next
-// half and the loads of a later round between them.
-template <typename T, typename S, int OP, bool DIRECT>
-__global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a) {
-  constexpr int FM = S::FM, FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
-  constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
-  constexpr int kSum = kRow / T::kBytes;
-  using Acc = typename T::Acc;
-  __shared__ __align__(1024) char lds[S::RoundBytes * NS];
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WN, wn = wave % S::WN;
-  // P's rows and Q's are the result's rows and columns
-  const int prows = OP == FSDP_MATMUL_TN ? a.n : 0, qrows = OP == FSDP_MATMUL_TN ? a.k : a.n;
-  const int nj = (qrows + S::BN - 1) / S::BN;
-  const Place t = OP == FSDP_MATMUL_TN ? weight_tile(a, (prows + S::BM - 1) / S::BM, nj)
-                                       : ragged_tile<S::BM>(a, nj);
-  if (t.group < 0) return;
-  const int i0 = t.i * S::BM, j0 = t.j * S::BN;
-
-  Operand po, qo;
+// Where a tile's operands begin, and its results: those from row i0 and column
+// j0 on of t's group (of TN's gradient).
+struct Site {
+  Operand p, q;
   int64_t to;
+};
+template <typename T, int OP>
+__device__ __forceinline__ Site site_of(const ProductArgs& a, const Place& t, int i0, int j0) {
+  constexpr int B = T::kBytes, kSum = kRow / B;
   const char* ab = static_cast<const char*>(a.a);
   const char* bb = static_cast<const char*>(a.b);
-  constexpr int B = T::kBytes;
+  Site s;
   if constexpr (OP == FSDP_MATMUL_TN) {
     // this part's rows of the group, whole rounds but for the last
     const int rounds = (t.hi - t.lo + kSum - 1) / kSum;
@@ -486,19 +566,41 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
     int end = static_cast<int>(int64_t(rounds) * (t.part + 1) / a.n_parts) * kSum;
     if (end > t.hi - t.lo) end = t.hi - t.lo;
     const int64_t row = t.lo + from;
-    po = Operand{ab + (row * a.lda + i0) * B, a.lda * B, a.n - i0, end - from};
-    qo = Operand{bb + (row * a.ldb + j0) * B, a.ldb * B, a.k - j0, end - from};
-    to = t.group * a.group_stride + i0 * a.ldc + j0;
+    s.p = Operand{ab + (row * a.lda + i0) * B, a.lda * B, a.n - i0, end - from};
+    s.q = Operand{bb + (row * a.ldb + j0) * B, a.ldb * B, a.k - j0, end - from};
+    s.to = t.group * a.group_stride + i0 * a.ldc + j0;
   } else {
     const int64_t row = t.lo + i0;
-    po = Operand{ab + row * a.lda * B, a.lda * B, t.hi - t.lo - i0, a.k};
     const char* b = bb + t.group * a.group_stride * B;
-    if constexpr (OP == FSDP_MATMUL_NT)
-      qo = Operand{b + j0 * a.ldb * B, a.ldb * B, a.n - j0, a.k};
-    else
-      qo = Operand{b + int64_t(j0) * B, a.ldb * B, a.n - j0, a.k};
-    to = row * a.ldc + j0;
+    s.p = Operand{ab + row * a.lda * B, a.lda * B, t.hi - t.lo - i0, a.k};
+    s.q = Operand{b + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0)) * B, a.ldb * B, a.n - j0,
+                  a.k};
+    s.to = row * a.ldc + j0;
   }
+  return s;
+}
+
+__device__ __forceinline__ uint32_t lds_address(const char* lds) {
+  return static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)lds));
+}
+
+// ------------------------------------------------------------- the tile loop
+// One tile, all waves on the same rounds of 128 bytes of the sum.  The products
+// of one half of a round are issued row by row with the LDS reads of the next
+// half and the loads of a later round between them.
+template <typename T, typename S, int OP, bool DIRECT>
+__device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i0, int j0,
+                                     char* lds) {
+  constexpr int FM = S::FM, FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
+  constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
+  constexpr int B = T::kBytes, kSum = kRow / B;
+  using Acc = typename T::Acc;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const Site site = site_of<T, OP>(a, t, i0, j0);
+  const Operand &po = site.p, &qo = site.q;
+  const int64_t to = site.to;
   const int total = (po.sum + kSum - 1) / kSum;
   if (OP == FSDP_MATMUL_TN && total == 0 && a.accumulate && a.n_parts == 1) return;
 
@@ -508,8 +610,7 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
   ql.begin(qo, wave);
   const Fetch<T, S::BM, FM, PA> pf(wm * S::TM);
   const Fetch<T, S::BN, FN, QA> qf(wn * S::TN);
-  const uint32_t lds0 = static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+  const uint32_t lds0 = lds_address(lds);
 
   Acc acc[FM][FN];
 #pragma unroll
@@ -517,8 +618,15 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
+  // bf16: the dies begin at different eighths of the sum, so that they do not
+  // all ask memory for the same columns at once
+  const int start = B == 2 && OP != FSDP_MATMUL_TN
+                        ? static_cast<int>(int64_t(total) * (blockIdx.x % kXcds) / kXcds)
+                        : 0;
   auto load = [&](int round, int buf, int x) {
     if constexpr (DIRECT) {
+      round += start;
+      if (round >= total) round -= total;
       if (x < LP)
         pl.load(round, lds0 + buf * S::RoundBytes, x < LP ? x : 0);
       else
@@ -605,9 +713,9 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 
   if constexpr (OP == FSDP_MATMUL_TN) {
     if (a.n_parts > 1) {
-      const int tiles = ((prows + S::BM - 1) / S::BM) * nj;
-      const int64_t at =
-          ((int64_t(t.group) * tiles + t.i * nj + t.j) * a.n_parts + t.part) * (FM * FN * S::Threads);
+      const int ni = (a.n + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
+      const int64_t at = ((int64_t(t.group) * ni * nj + t.i * nj + t.j) * a.n_parts + t.part) *
+                         (FM * FN * S::Threads);
       f4* part = reinterpret_cast<f4*>(a.parts) + at + threadIdx.x;
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -624,6 +732,134 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
               a.sb ? a.sb + t.group * a.sb_stride + j0 : nullptr);
   } else {
     finish<T>(a, acc, stage, to, wm * S::TM, wn * S::TN, po.side, qo.side, nullptr, nullptr);
+  }
+}
+
+// ROWS: a 256 x 256 tile's, of which fewer may be left (a group's last rows) or
+// wanted (a tile that is cut): 128 of them take half the time.
+template <typename T, typename S, int OP, bool DIRECT>
+__global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a) {
+  __shared__ __align__(1024) char lds[S::RoundBytes * S::NS];
+  if constexpr (OP == FSDP_MATMUL_TN) {
+    const Place t = weight_tile(a, (a.n + S::BM - 1) / S::BM, (a.k + S::BN - 1) / S::BN);
+    if (t.group >= 0) tile<T, S, OP, DIRECT>(a, t, t.i * S::BM, t.j * S::BN, lds);
+  } else {
+    constexpr bool kSplit = S::BM == 256;
+    const Place t = ragged_tile<S::BM, kSplit>(a, (a.n + S::BN - 1) / S::BN);
+    if (t.group < 0) return;
+    int i0 = t.i * S::BM, j0 = t.j * S::BN;
+    if constexpr (kSplit) {
+      static_assert(Half::Threads == S::Threads && Quarter::Threads == S::Threads);
+      static_assert(Half::RoundBytes * Half::NS <= sizeof(lds) &&
+                    Quarter::RoundBytes * Quarter::NS <= sizeof(lds));
+      const int rows = t.hi - t.lo;
+      if (t.parts == 4) {
+        i0 += t.part / 2 * Quarter::BM;
+        j0 += t.part % 2 * Quarter::BN;
+        if (i0 < rows && j0 < a.n) tile<T, Quarter, OP, DIRECT>(a, t, i0, j0, lds);
+        return;
+      }
+      if (t.parts == 2) i0 += t.part * Half::BM;
+      if (t.parts == 2 || rows - i0 <= Half::BM) {
+        if (i0 < rows) tile<T, Half, OP, DIRECT>(a, t, i0, j0, lds);
+        return;
+      }
+    }
+    tile<T, S, OP, DIRECT>(a, t, i0, j0, lds);
+  }
+}
+
+// A 16 x 32 tile for few rows, with the sum dealt over 4 waves: wave w takes
+// rounds w, w + 4, ... with loads, LDS and accumulators of its own, so it waits
+// for nothing but its own loads, until the four are added up.  Bound by the
+// weights' way from memory.
+template <typename T, int OP>
+__global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
+  using S = Tile<16, 32, 1, 1, 2, 2>;
+  constexpr int FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
+  constexpr bool QA = OP != FSDP_MATMUL_NT;
+  constexpr int B = T::kBytes, kSum = kRow / B;
+  using Acc = typename T::Acc;
+  static_assert(S::FM == 1 && FN == 2);
+  __shared__ __align__(1024) char lds[4 * S::RoundBytes * NS];
+  const Place t = ragged_tile<S::BM, false>(a, (a.n + S::BN - 1) / S::BN);
+  if (t.group < 0) return;
+  const int i0 = t.i * S::BM, j0 = t.j * S::BN, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Site site = site_of<T, OP>(a, t, i0, j0);
+  const int total = (a.k + kSum - 1) / kSum, mine = (total - wave + 3) / 4;
+  char* own = lds + wave * S::RoundBytes * NS;
+  const uint32_t own0 = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * S::RoundBytes * NS);
+  Direct<T, S::BM, LP, false> pl;
+  Direct<T, S::BN, LQ, QA> ql;
+  pl.begin(site.p, 0);
+  ql.begin(site.q, 0);
+  const Fetch<T, S::BM, 1, false> pf(0);
+  const Fetch<T, S::BN, FN, QA> qf(0);
+  auto load = [&](int r, int buf) {  // behind the last: zeros, not read
+#pragma unroll
+    for (int x = 0; x < LP; ++x) pl.load(wave + 4 * r, own0 + buf * S::RoundBytes, x);
+#pragma unroll
+    for (int x = 0; x < LQ; ++x)
+      ql.load(wave + 4 * r, own0 + buf * S::RoundBytes + S::BM * kRow, x);
+  };
+  Acc acc[FN] = {};
+#pragma unroll
+  for (int s = 0; s < NS; ++s) load(s, s);
+  int buf = 0;
+  for (int r = 0; r < mine; ++r) {
+    wait_loads<(NS - 1) * (LP + LQ)>();
+    const char* image = own + buf * S::RoundBytes;
+    u4 p[2], q[2][FN];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      p[kk] = pf.get(image, kk, 0);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) q[kk][j] = qf.get(image + S::BM * kRow, kk, j);
+    }
+    wait_lds();  // the buffer is read: load it again
+    asm volatile("" ::: "memory");
+    load(r + NS, buf);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[j] = T::mma(q[kk][j], p[kk], acc[j]);
+    buf = buf + 1 == NS ? 0 : buf + 1;
+  }
+  wait_loads<0>();
+  // the four waves' sums, in their order: two adjacent results per lane
+  static_assert(FN * 1024 <= S::RoundBytes * NS);
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+    *reinterpret_cast<Acc*>(own + ((lane & 15) * 32 + j * 16 + (lane >> 4) * 4) * 4) = acc[j];
+  __syncthreads();
+  const int r = threadIdx.x >> 4, c = threadIdx.x % 16 * 2;
+  const int have = a.n - (j0 + c);
+  if (i0 + r >= t.hi - t.lo || have <= 0) return;
+  using E = std::conditional_t<B == 1, int, float>;
+  E sum[2] = {0, 0};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const E* from = reinterpret_cast<const E*>(lds + w * S::RoundBytes * NS) + r * 32 + c;
+    sum[0] += from[0];
+    sum[1] += from[1];
+  }
+  const int64_t at = site.to + r * a.ldc + c;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (e >= have) break;
+    float x = static_cast<float>(sum[e]);
+    if constexpr (B == 1) {
+      x *= a.sa[t.lo + i0 + r];
+      if (a.sb) x *= a.sb[t.group * a.sb_stride + j0 + c + e];
+    }
+    if (a.out_f32) {
+      float* to = static_cast<float*>(a.c) + at + e;
+      *to = a.accumulate ? *to + x : x;
+    } else {
+      u16* to = static_cast<u16*>(a.c) + at + e;
+      *to = static_cast<u16>(f32_to_bf16(a.accumulate ? bf16_to_f32(*to) + x : x));
+    }
   }
 }
 
@@ -666,7 +902,7 @@ __global__ __launch_bounds__(256) void k_product_f32(ProductArgs a) {
   const int qrows = OP == FSDP_MATMUL_TN ? a.k : a.n;
   const int nj = (qrows + BM - 1) / BM;
   const Place t = OP == FSDP_MATMUL_TN ? weight_tile(a, (a.n + BM - 1) / BM, nj)
-                                       : ragged_tile<BM>(a, nj);
+                                       : ragged_tile<BM, false>(a, nj);
   if (t.group < 0) return;
   const int i0 = t.i * BM, j0 = t.j * BM;
   const float* pa = static_cast<const float*>(a.a);
@@ -750,12 +986,6 @@ __global__ __launch_bounds__(256) void k_product_f32(ProductArgs a) {
 }
 
 // ---------------------------------------------------------------- launchers
-using Small = Tile<64, 64, 2, 2, 3, 2>;
-using Mid = Tile<128, 128, 2, 2, 2, 2>;
-using Big = Tile<256, 256, 2, 4, 2, 2>;
-static_assert(Small::BM == kProductTiles[0] && Mid::BM == kProductTiles[1] &&
-              Big::BM == kProductTiles[2]);
-
 template <typename T, typename S, int OP, bool DIRECT>
 hipError_t launch_tile(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
   ProductArgs a = args;
@@ -771,17 +1001,26 @@ hipError_t launch_tile(const ProductArgs& args, const ProductRule& rule, const S
 }
 
 template <typename T, int OP>
-hipError_t launch_op(const ProductArgs& a, const ProductRule& rule, const Sink& sink) {
+hipError_t launch_op(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
   if constexpr (T::kBytes == 2) {
     if (!rule.direct) {
-      if (rule.tile == 0) return launch_tile<T, Small, OP, false>(a, rule, sink);
-      return launch_tile<T, Mid, OP, false>(a, rule, sink);
+      if (rule.tile == kSmall) return launch_tile<T, Small, OP, false>(args, rule, sink);
+      return launch_tile<T, Mid<OP>, OP, false>(args, rule, sink);
+    }
+    if (rule.tile == kDeep) return launch_tile<T, Deep<OP>, OP, true>(args, rule, sink);
+  }
+  if constexpr (OP != FSDP_MATMUL_TN) {
+    if (rule.tile == kThin) {
+      ProductArgs a = args;
+      void* p[] = {&a};
+      return sink.launch(reinterpret_cast<const void*>(&k_thin<T, OP>),
+                         dim3(static_cast<unsigned>(rule.grid)), dim3(256), p, 0);
     }
   }
   switch (rule.tile) {
-    case 0: return launch_tile<T, Small, OP, true>(a, rule, sink);
-    case 1: return launch_tile<T, Mid, OP, true>(a, rule, sink);
-    default: return launch_tile<T, Big, OP, true>(a, rule, sink);
+    case kSmall: return launch_tile<T, Small, OP, true>(args, rule, sink);
+    case kMid: return launch_tile<T, Mid<OP>, OP, true>(args, rule, sink);
+    default: return launch_tile<T, Big, OP, true>(args, rule, sink);
   }
 }
 

@@ -30,12 +30,14 @@ struct ProductArgs {
   int32_t n_parts;
 };
 
-// Sides of the tiles.
-constexpr int kProductTiles[3] = {64, 128, 256};
+// The tiles: rows and columns of results that a workgroup makes.
+enum ProductTile { kThin, kSmall, kMid, kDeep, kBig };
+constexpr int kProductRows[5] = {16, 64, 128, 128, 256};
+constexpr int kProductCols[5] = {32, 64, 128, 128, 256};
 
 // How a call is carried out, a function of its sizes, types and alignment.
 struct ProductRule {
-  int tile;      // index into kProductTiles
+  int tile;      // ProductTile
   bool direct;   // operands go straight to LDS, in 16-byte pieces
   int n_parts;   // of a weight gradient's sums
   int64_t grid;  // workgroups

@@ -114,16 +114,19 @@ static void check_product(std::mt19937& rng) {
   const bool direct = pick(0, 1);
   const auto type = static_cast<fsdp::ProductType>(pick(0, m.op == FSDP_MATMUL_TN ? 1 : 2));
   const fsdp::ProductRule r = fsdp::product_rule(m, type, direct || type == fsdp::kProductI8);
-  const int64_t side = fsdp::kProductTiles[r.tile];
-  CHECK(r.tile >= 0 && r.tile < 3 && r.n_parts >= 1 && r.n_parts <= 64 && r.grid >= 0);
-  CHECK(type != fsdp::kProductF32 || (r.tile == 0 && r.n_parts == 1));
-  CHECK(r.direct || r.tile < 2);
-  auto tiles = [&](int64_t x) { return (x + side - 1) / side; };
+  CHECK(r.tile >= 0 && r.tile < 5);
+  const int64_t rows = fsdp::kProductRows[r.tile], cols = fsdp::kProductCols[r.tile];
+  CHECK(r.n_parts >= 1 && r.n_parts <= 64 && r.grid >= 0);
+  CHECK(type != fsdp::kProductF32 || (r.tile == fsdp::kSmall && r.n_parts == 1));
+  CHECK(r.direct || r.tile == fsdp::kSmall || r.tile == fsdp::kMid);
+  auto down = [&](int64_t x) { return (x + rows - 1) / rows; };
+  auto across = [&](int64_t x) { return (x + cols - 1) / cols; };
   if (m.op == FSDP_MATMUL_TN) {
-    const int64_t all = tiles(m.n) * tiles(m.k) * r.n_parts;
+    CHECK(r.tile != fsdp::kThin);
+    const int64_t all = down(m.n) * across(m.k) * r.n_parts;
     CHECK(r.grid >= (all + 7) / 8 * 8 * m.groups);
-    CHECK(r.join == tiles(m.n) * tiles(m.k) * m.groups);
-    CHECK(r.workspace == (r.n_parts > 1 ? all * m.groups * side * side * 4 : 0));
+    CHECK(r.join == down(m.n) * across(m.k) * m.groups);
+    CHECK(r.workspace == (r.n_parts > 1 ? all * m.groups * rows * cols * 4 : 0));
   } else {
     CHECK(r.workspace == 0 && r.n_parts == 1);
     // random sizes that add up to rows, and the worst ones: single rows
@@ -132,12 +135,19 @@ static void check_product(std::mt19937& rng) {
     cut[m.groups] = m.rows;
     for (int64_t g = 1; g < m.groups; ++g) cut[g] = pick(0, m.rows);
     std::sort(cut.begin(), cut.end());
-    int64_t down = 0;
-    for (int64_t g = 0; g < m.groups; ++g) down += tiles(cut[g + 1] - cut[g]);
-    CHECK(r.grid >= (down * tiles(m.n) + 7) / 8 * 8 && r.grid % 8 == 0);
+    // the last tiles of the largest may be cut in two or four
+    auto wanted = [&](int64_t tiles) {
+      const int64_t rest = tiles % 256;
+      if (r.tile == fsdp::kBig && tiles > 256 && rest <= 128)
+        tiles += rest * (rest <= 64 ? 3 : 1);
+      return (tiles + 7) / 8 * 8;
+    };
+    int64_t sum = 0;
+    for (int64_t g = 0; g < m.groups; ++g) sum += down(cut[g + 1] - cut[g]);
+    CHECK(r.grid >= wanted(sum * across(m.n)) && r.grid % 8 == 0);
     if (m.groups > 1) {
       const int64_t ones = std::min<int64_t>(m.groups - 1, m.rows);
-      CHECK(r.grid >= ((ones + tiles(m.rows - ones)) * tiles(m.n) + 7) / 8 * 8);
+      CHECK(r.grid >= wanted((ones + down(m.rows - ones)) * across(m.n)));
     }
   }
   int64_t bytes = -1;

@@ -135,6 +135,24 @@ def test_large_tiles_are_exact(op, k):
 
 
 @pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,n", [([2100, 0, 1990], 4104), ([1700, 300, 2500, 1], 3900),
+                                     ([4096], 4352), ([129, 4095], 4352)])
+def test_the_last_tiles_cut(op, sizes, n):
+    """A few 256 x 256 tiles more than fill the card: cut in two or four; groups
+    that end in the first or the second half of a tile."""
+    exact_case(op, sizes, n, 136)
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,n,k", [([16], 40, 600), ([7, 0, 30, 1, 2], 200, 1096),
+                                       ([1], 4104, 4096), ([3] * 70, 72, 264)])
+def test_few_rows(op, sizes, n, k):
+    """16 rows per group or fewer, and one group with more."""
+    exact_case(op, sizes, n, k)
+    exact_case(op, sizes, n, k, out="bf16", accumulate=True, cpad=3, first=1, tail=2)
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
 def test_many_groups(op):
     """More groups than a wave has lanes, most of them empty."""
     rng = np.random.default_rng(3)
@@ -287,6 +305,16 @@ def test_products_of_codes_results(op, out, accumulate, scales):
 @pytest.mark.parametrize("n,k", [(2056, 72), (2051, 70), (4104, 200)])
 def test_products_of_codes_in_larger_tiles(op, n, k):
     i8_case(op, [700, 0, 1, 1400] if n < 4000 else [2600, 3, 0, 1900], n, k)
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,n,k", [([2100, 0, 1990], 4104, 136), ([129, 4095], 4352, 200),
+                                       ([7, 0, 30, 1, 2], 200, 1096), ([1], 4104, 4099),
+                                       ([3] * 70, 71, 263)])
+def test_products_of_codes_last_tiles_and_few_rows(op, sizes, n, k):
+    i8_case(op, sizes, n, k)
+    if sum(sizes) < 300:
+        i8_case(op, sizes, n, k, out="bf16", accumulate=True, first=1, tail=2, scales=False)
 
 
 def test_codes_longest_sum():
