@@ -28,22 +28,24 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   // tiles about as many as there will be: every group's last row of tiles is
   // half empty
   auto tiles = [&](ProductTile t) {
-    const int64_t down = kProductRows[t], across = kProductCols[t];
-    return weight ? m.groups * ceil_div(m.n, down) * ceil_div(m.k, across)
-                  : (met == 1 ? ceil_div(m.rows, down) : m.rows / down + (met + 1) / 2) *
-                        ceil_div(m.n, across);
+    const int64_t down = kProductRows[t], across = product_cols(t, m.op);
+    if (weight) return m.groups * ceil_div(m.n, down) * ceil_div(m.k, across);
+    return (met == 1 ? ceil_div(m.rows, down) : std::max(met, m.rows / down + (met + 1) / 2)) *
+           ceil_div(m.n, across);
   };
   r.direct = direct && type != kProductF32;
   r.tile = kSmall;
-  if (type != kProductF32) {
-    if (r.direct && !weight && m.rows <= 16 * met)
-      r.tile = kThin;
-    else if (r.direct && tiles(kBig) >= (weight ? 2 * kCus : kCus))
-      r.tile = kBig;
-    else if (tiles(kMid) >= kCus)
-      r.tile = r.direct && type == kProductBf16 && tiles(kMid) <= kCus ? kDeep : kMid;
+  if (type == kProductF32) {
+    if (tiles(kMid) >= kCus) r.tile = kMid;
+  } else if (r.direct && !weight && tiles(kSmall) < kCus &&
+             tiles(kSmall) * ceil_div(m.rows, 16 * met) <= 2 * kCus) {
+    r.tile = kThin;
+  } else if (r.direct && tiles(kBig) >= (weight ? 2 * kCus : kCus)) {
+    r.tile = kBig;
+  } else if (tiles(kMid) >= kCus) {
+    r.tile = r.direct && type == kProductBf16 && tiles(kMid) <= kCus ? kDeep : kMid;
   }
-  const int64_t down = kProductRows[r.tile], across = kProductCols[r.tile];
+  const int64_t down = kProductRows[r.tile], across = product_cols(r.tile, m.op);
   r.n_parts = 1;
   if (weight) {
     const int64_t per_group = ceil_div(m.n, down) * ceil_div(m.k, across);

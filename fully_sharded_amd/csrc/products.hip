@@ -775,12 +775,12 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 // weights' way from memory.
 template <typename T, int OP>
 __global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
-  using S = Tile<16, 32, 1, 1, 2, 2>;
-  constexpr int FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
+  using S = Tile<16, OP == FSDP_MATMUL_NT ? 32 : 64, 1, 1, 2, 2>;
+  constexpr int FN = S::FN, BN = S::BN, NS = S::NS, LP = S::LP, LQ = S::LQ;
   constexpr bool QA = OP != FSDP_MATMUL_NT;
   constexpr int B = T::kBytes, kSum = kRow / B;
   using Acc = typename T::Acc;
-  static_assert(S::FM == 1 && FN == 2);
+  static_assert(S::FM == 1);
   __shared__ __align__(1024) char lds[4 * S::RoundBytes * NS];
   const Place t = ragged_tile<S::BM, false>(a, (a.n + S::BN - 1) / S::BN);
   if (t.group < 0) return;
@@ -827,26 +827,26 @@ __global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
     buf = buf + 1 == NS ? 0 : buf + 1;
   }
   wait_loads<0>();
-  // the four waves' sums, in their order: two adjacent results per lane
+  // the four waves' sums, in their order: a few adjacent results per lane
   static_assert(FN * 1024 <= S::RoundBytes * NS);
 #pragma unroll
   for (int j = 0; j < FN; ++j)
-    *reinterpret_cast<Acc*>(own + ((lane & 15) * 32 + j * 16 + (lane >> 4) * 4) * 4) = acc[j];
+    *reinterpret_cast<Acc*>(own + ((lane & 15) * BN + j * 16 + (lane >> 4) * 4) * 4) = acc[j];
   __syncthreads();
-  const int r = threadIdx.x >> 4, c = threadIdx.x % 16 * 2;
+  const int r = threadIdx.x >> 4, c = threadIdx.x % 16 * FN;
   const int have = a.n - (j0 + c);
   if (i0 + r >= t.hi - t.lo || have <= 0) return;
   using E = std::conditional_t<B == 1, int, float>;
-  E sum[2] = {0, 0};
+  E sum[FN] = {};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const E* from = reinterpret_cast<const E*>(lds + w * S::RoundBytes * NS) + r * 32 + c;
-    sum[0] += from[0];
-    sum[1] += from[1];
+    const E* from = reinterpret_cast<const E*>(lds + w * S::RoundBytes * NS) + r * BN + c;
+#pragma unroll
+    for (int e = 0; e < FN; ++e) sum[e] += from[e];
   }
   const int64_t at = site.to + r * a.ldc + c;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < FN; ++e) {
     if (e >= have) break;
     float x = static_cast<float>(sum[e]);
     if constexpr (B == 1) {
@@ -891,98 +891,140 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------- fp32
-// fp32 operands, one 64 x 64 tile by four waves of 32 x 32, 16 of the sum per
-// round.  Both operands are kept in LDS as rows across the sum, which is how
-// the matrix instruction reads single entries.
-template <int OP>
-__global__ __launch_bounds__(256) void k_product_f32(ProductArgs a) {
-  constexpr int BM = 64, BK = 16, LD = BM + 16;
-  __shared__ float ps[2][BK][LD], qs[2][BK][LD];
+// fp32 operands: BM x BM results by eight waves, 32 of the sum per round, which
+// pass through registers (rows may begin anywhere).  Both operands are kept in
+// LDS as rows across the sum, which is how the matrix instruction reads single
+// entries: entry k of row r at place r ^ 8 (k / 4) ^ 16 (k % 4) of row k, so that
+// neither the reads (16 rows of 4 k) nor the writes of rows along the sum (8 rows
+// of 8 times 4 k) meet on a bank.
+template <int BM>
+struct F32Tile {
+  static constexpr int BK = 32, WM = BM == 64 ? 4 : 2, WN = 8 / WM;
+  static constexpr int FM = BM / WM / 16, FN = BM / WN / 16;
+  static constexpr int L = BM * BK / 4 / 512;  // four entries each, of a lane
+};
+__device__ __forceinline__ int place_f32(int k, int r) {
+  return r ^ ((k >> 2 & 7) << 3) ^ ((k & 3) << 4);
+}
+
+template <int BM, bool ACROSS>
+struct F32Operand {
+  using S = F32Tile<BM>;
+  const float* p;
+  int64_t ld;
+  int side, sum;
+  f4 v[S::L];
+
+  // row (or column) and entry of the sum of this lane's x-th four
+  __device__ __forceinline__ static int row(int x) {
+    return ACROSS ? static_cast<int>(threadIdx.x) % (BM / 4) * 4
+                  : static_cast<int>(threadIdx.x) / 8 + 64 * x;
+  }
+  __device__ __forceinline__ static int entry(int x) {
+    return ACROSS ? static_cast<int>(threadIdx.x) / (BM / 4) + 2048 / BM * x
+                  : static_cast<int>(threadIdx.x) % 8 * 4;
+  }
+  __device__ __forceinline__ void fetch(int from) {
+    typedef f4 any __attribute__((aligned(4)));
+#pragma unroll
+    for (int x = 0; x < S::L; ++x) {
+      const int r = row(x), k = from + entry(x);
+      const int have = ACROSS ? (k < sum ? side - r : 0) : (r < side ? sum - k : 0);
+      const float* at = p + (ACROSS ? k * ld + r : r * ld + k);
+      f4 w = {0.f, 0.f, 0.f, 0.f};
+      if (have >= 4) {
+        w = *reinterpret_cast<const any*>(at);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < have) w[e] = at[e];
+      }
+      v[x] = w;
+    }
+  }
+  __device__ __forceinline__ void put(float* image) const {
+#pragma unroll
+    for (int x = 0; x < S::L; ++x) {
+      const int r = row(x), k = entry(x);
+      if constexpr (ACROSS) {
+        *reinterpret_cast<f4*>(image + k * BM + place_f32(k, r)) = v[x];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) image[(k + e) * BM + place_f32(k + e, r)] = v[x][e];
+      }
+    }
+  }
+};
+
+template <int OP, int BM>
+__global__ __launch_bounds__(512) void k_product_f32(ProductArgs a) {
+  using S = F32Tile<BM>;
+  constexpr int BK = S::BK, FM = S::FM, FN = S::FN, kImage = BK * BM;
+  __shared__ __align__(16) float lds[4 * kImage];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int qrows = OP == FSDP_MATMUL_TN ? a.k : a.n;
   const int nj = (qrows + BM - 1) / BM;
-  const Place t = OP == FSDP_MATMUL_TN ? weight_tile(a, (a.n + BM - 1) / BM, nj)
-                                       : ragged_tile<BM, false>(a, nj);
+  Place t;
+  if constexpr (OP == FSDP_MATMUL_TN)
+    t = weight_tile(a, (a.n + BM - 1) / BM, nj);
+  else
+    t = ragged_tile<BM, false>(a, nj);
   if (t.group < 0) return;
   const int i0 = t.i * BM, j0 = t.j * BM;
-  const float* pa = static_cast<const float*>(a.a);
-  const float* qb = static_cast<const float*>(a.b);
+  F32Operand<BM, OP == FSDP_MATMUL_TN> p;
+  F32Operand<BM, OP != FSDP_MATMUL_NT> q;
+  p.p = static_cast<const float*>(a.a);
+  q.p = static_cast<const float*>(a.b);
+  p.ld = a.lda;
+  q.ld = a.ldb;
+  q.side = qrows - j0;
   int64_t to;
-  int pside, sum;
-  const int qside = qrows - j0;
-  if (OP == FSDP_MATMUL_TN) {
-    const int rounds = (t.hi - t.lo + BK - 1) / BK;
-    const int from = static_cast<int>(int64_t(rounds) * t.part / a.n_parts) * BK;
-    int end = static_cast<int>(int64_t(rounds) * (t.part + 1) / a.n_parts) * BK;
-    if (end > t.hi - t.lo) end = t.hi - t.lo;
-    pa += (t.lo + from) * a.lda + i0;
-    qb += (t.lo + from) * a.ldb + j0;
-    pside = a.n - i0;
-    sum = end - from;
+  if constexpr (OP == FSDP_MATMUL_TN) {
+    p.p += t.lo * a.lda + i0;
+    q.p += t.lo * a.ldb + j0;
+    p.side = a.n - i0;
+    p.sum = t.hi - t.lo;
     to = t.group * a.group_stride + i0 * a.ldc + j0;
+    if (p.sum == 0 && a.accumulate) return;
   } else {
-    pa += (t.lo + i0) * a.lda;
-    qb += t.group * a.group_stride + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0));
-    pside = t.hi - t.lo - i0;
-    sum = a.k;
+    p.p += (t.lo + i0) * a.lda;
+    q.p += t.group * a.group_stride + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0));
+    p.side = t.hi - t.lo - i0;
+    p.sum = a.k;
     to = (t.lo + i0) * a.ldc + j0;
   }
-  if (OP == FSDP_MATMUL_TN && sum == 0 && a.accumulate) return;
-  // 64 x 16 entries of an operand: four per lane, adjacent in memory where
-  // its rows lie across the sum, along it otherwise
-  auto fetch = [&](const float* p, int64_t ld, int side, bool across, int s0, float (&v)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = across ? threadIdx.x % 64 : threadIdx.x / 16 + 16 * e;
-      const int s = s0 + (across ? threadIdx.x / 64 + 4 * e : threadIdx.x % 16);
-      v[e] = 0.f;
-      if (r < side && s < sum) v[e] = across ? p[s * ld + r] : p[r * ld + s];
-    }
-  };
-  auto put = [&](float (*to_)[LD], bool across, const float (&v)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (across)
-        to_[threadIdx.x / 64 + 4 * e][threadIdx.x % 64] = v[e];
-      else
-        to_[threadIdx.x % 16][threadIdx.x / 16 + 16 * e] = v[e];
-    }
-  };
-  constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
-  const int wm = wave / 2 * 32, wn = wave % 2 * 32;
-  f4 acc[2][2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-  float pv[4], qv[4];
-  fetch(pa, a.lda, pside, PA, 0, pv);
-  fetch(qb, a.ldb, qside, QA, 0, qv);
+  q.sum = p.sum;
+  const int wm = wave / S::WN * (BM / S::WM), wn = wave % S::WN * (BM / S::WN);
+  f4 acc[FM][FN] = {};
+  p.fetch(0);
+  q.fetch(0);
   int buf = 0;
-  for (int s = 0; s < sum; s += BK, buf ^= 1) {
-    put(ps[buf], PA, pv);
-    put(qs[buf], QA, qv);
-    __syncthreads();
-    fetch(pa, a.lda, pside, PA, s + BK, pv);
-    fetch(qb, a.ldb, qside, QA, s + BK, qv);
+  for (int s = 0; s < p.sum; s += BK, buf ^= 1) {
+    float* ps = lds + buf * 2 * kImage;
+    float* qs = ps + kImage;
+    p.put(ps);
+    q.put(qs);
+    __syncthreads();  // and the other buffer, written next, is read
+    p.fetch(s + BK);
+    q.fetch(s + BK);
 #pragma unroll
     for (int kk = 0; kk < BK; kk += 4) {
-      float p[2], q[2];
+      const int k = kk + (lane >> 4);
+      float x[FM], y[FN];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        p[i] = ps[buf][kk + (lane >> 4)][wm + i * 16 + (lane & 15)];
-        q[i] = qs[buf][kk + (lane >> 4)][wn + i * 16 + (lane & 15)];
-      }
+      for (int i = 0; i < FM; ++i) x[i] = ps[k * BM + place_f32(k, wm + i * 16 + (lane & 15))];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int j = 0; j < FN; ++j) y[j] = qs[k * BM + place_f32(k, wn + j * 16 + (lane & 15))];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(q[j], p[i], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(y[j], x[i], acc[i][j], 0, 0, 0);
     }
   }
   __syncthreads();
-  static_assert(4 * kStage<2> <= 2 * BK * LD);
-  finish<Bf16>(a, acc, &ps[0][0][0] + wave * kStage<2>, to, wm, wn, pside, qside, nullptr, nullptr);
+  static_assert(8 * kStage<FN> <= 4 * kImage);
+  finish<Bf16>(a, acc, lds + wave * kStage<FN>, to, wm, wn, p.side, q.side, nullptr, nullptr);
 }
 
 // ---------------------------------------------------------------- launchers
@@ -1028,8 +1070,9 @@ template <int OP>
 hipError_t launch_f32(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
   ProductArgs a = args;
   void* p[] = {&a};
-  return sink.launch(reinterpret_cast<const void*>(&k_product_f32<OP>),
-                     dim3(static_cast<unsigned>(rule.grid)), dim3(256), p, 0);
+  return sink.launch(rule.tile == kMid ? reinterpret_cast<const void*>(&k_product_f32<OP, 128>)
+                                       : reinterpret_cast<const void*>(&k_product_f32<OP, 64>),
+                     dim3(static_cast<unsigned>(rule.grid)), dim3(512), p, 0);
 }
 
 }  // namespace

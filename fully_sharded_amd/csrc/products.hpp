@@ -33,7 +33,9 @@ struct ProductArgs {
 // The tiles: rows and columns of results that a workgroup makes.
 enum ProductTile { kThin, kSmall, kMid, kDeep, kBig };
 constexpr int kProductRows[5] = {16, 64, 128, 128, 256};
-constexpr int kProductCols[5] = {32, 64, 128, 128, 256};
+inline int product_cols(int tile, int32_t op) {
+  return tile == kThin ? (op == FSDP_MATMUL_NT ? 32 : 64) : kProductRows[tile];
+}
 
 // How a call is carried out, a function of its sizes, types and alignment.
 struct ProductRule {

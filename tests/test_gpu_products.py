@@ -125,6 +125,15 @@ def test_middle_tiles_are_exact(op, n, k, off):
 
 
 @pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("off", [0, 1])
+def test_fp32_in_larger_tiles(op, off):
+    if op == "tn":
+        exact_case(op, [70, 61], 2051, 2050, dtype="f32", off=off)
+    else:
+        exact_case(op, [700, 0, 1, 1400], 2051, 70, dtype="f32", off=off)
+
+
+@pytest.mark.parametrize("op", OPS)
 @pytest.mark.parametrize("k", [72, 200])
 def test_large_tiles_are_exact(op, k):
     """Enough results for 256 x 256 tiles."""
