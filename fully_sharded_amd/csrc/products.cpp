@@ -36,7 +36,7 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   r.direct = direct && type != kProductF32;
   r.tile = kSmall;
   if (type == kProductF32) {
-    if (tiles(kMid) >= kCus) r.tile = kMid;
+    r.tile = tiles(kMid) >= kCus ? kMid : tiles(kSmall) >= 2 * kCus ? kSmall : kTiny;
   } else if (r.direct && !weight && tiles(kSmall) < kCus &&
              tiles(kSmall) * ceil_div(m.rows, 16 * met) <= 2 * kCus) {
     r.tile = kThin;

@@ -484,11 +484,11 @@ __device__ __forceinline__ void finish_as(const ProductArgs& a,
                                           int64_t to, int r0, int c0, int rows, int cols,
                                           const float* sa, const float* sb) {
   constexpr int kCols = FN * 16, kPitch = kCols + 4, kN = F32 ? 4 : 8;
-  constexpr int kPerRow = kCols / kN, kAtOnce = 64 / kPerRow;  // lanes and rows of a store
-  static_assert(kAtOnce <= 16);
+  constexpr int kPerRow = kCols / kN;  // lanes of a store's rows, and how many rows
+  constexpr int kAtOnce = 64 / kPerRow < 16 ? 64 / kPerRow : 16;
   const int lane = threadIdx.x & 63;
   const int r = lane / kPerRow, c = lane % kPerRow * kN;
-  const int have = cols - (c0 + c);
+  const int have = r < kAtOnce ? cols - (c0 + c) : 0;
   float scale[kN];
   if constexpr (T::kBytes == 1) {
 #pragma unroll
@@ -522,7 +522,8 @@ __device__ __forceinline__ void finish_as(const ProductArgs& a,
       float x[kN];
 #pragma unroll
       for (int e = 0; e < kN; e += 4) {
-        const f4 v = *reinterpret_cast<const f4*>(stage + (h * kAtOnce + r) * kPitch + c + e);
+        const f4 v = *reinterpret_cast<const f4*>(stage + (h * kAtOnce + r % kAtOnce) * kPitch +
+                                                  c + e);
 #pragma unroll
         for (int k = 0; k < 4; ++k) x[e + k] = v[k];
       }
@@ -891,7 +892,7 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------- fp32
-// fp32 operands: BM x BM results by eight waves, 32 of the sum per round, which
+// fp32 operands: BM x BM results by four or eight waves, 32 of the sum per round, which
 // pass through registers (rows may begin anywhere).  Both operands are kept in
 // LDS as rows across the sum, which is how the matrix instruction reads single
 // entries: entry k of row r at place r ^ 8 (k / 4) ^ 16 (k % 4) of row k, so that
@@ -899,12 +900,17 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 // of 8 times 4 k) meet on a bank.
 template <int BM>
 struct F32Tile {
-  static constexpr int BK = 32, WM = BM == 64 ? 4 : 2, WN = 8 / WM;
+  static constexpr int BK = 32, Threads = BM == 32 ? 256 : 512;
+  static constexpr int WM = BM == 64 ? 4 : 2, WN = Threads / 64 / WM;
   static constexpr int FM = BM / WM / 16, FN = BM / WN / 16;
-  static constexpr int L = BM * BK / 4 / 512;  // four entries each, of a lane
+  static constexpr int L = BM * BK / 4 / Threads;  // four entries each, of a lane
 };
+template <int BM>
 __device__ __forceinline__ int place_f32(int k, int r) {
-  return r ^ ((k >> 2 & 7) << 3) ^ ((k & 3) << 4);
+  if constexpr (BM == 32)  // two rows are all banks once
+    return r ^ ((k >> 2 & 3) << 3) ^ ((k >> 1 & 1) << 4);
+  else
+    return r ^ ((k >> 2 & 7) << 3) ^ ((k & 3) << 4);
 }
 
 template <int BM, bool ACROSS>
@@ -918,10 +924,10 @@ struct F32Operand {
   // row (or column) and entry of the sum of this lane's x-th four
   __device__ __forceinline__ static int row(int x) {
     return ACROSS ? static_cast<int>(threadIdx.x) % (BM / 4) * 4
-                  : static_cast<int>(threadIdx.x) / 8 + 64 * x;
+                  : static_cast<int>(threadIdx.x) / 8 + S::Threads / 8 * x;
   }
   __device__ __forceinline__ static int entry(int x) {
-    return ACROSS ? static_cast<int>(threadIdx.x) / (BM / 4) + 2048 / BM * x
+    return ACROSS ? static_cast<int>(threadIdx.x) / (BM / 4) + S::Threads * 4 / BM * x
                   : static_cast<int>(threadIdx.x) % 8 * 4;
   }
   __device__ __forceinline__ void fetch(int from) {
@@ -947,17 +953,17 @@ struct F32Operand {
     for (int x = 0; x < S::L; ++x) {
       const int r = row(x), k = entry(x);
       if constexpr (ACROSS) {
-        *reinterpret_cast<f4*>(image + k * BM + place_f32(k, r)) = v[x];
+        *reinterpret_cast<f4*>(image + k * BM + place_f32<BM>(k, r)) = v[x];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) image[(k + e) * BM + place_f32(k + e, r)] = v[x][e];
+        for (int e = 0; e < 4; ++e) image[(k + e) * BM + place_f32<BM>(k + e, r)] = v[x][e];
       }
     }
   }
 };
 
 template <int OP, int BM>
-__global__ __launch_bounds__(512) void k_product_f32(ProductArgs a) {
+__global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArgs a) {
   using S = F32Tile<BM>;
   constexpr int BK = S::BK, FM = S::FM, FN = S::FN, kImage = BK * BM;
   __shared__ __align__(16) float lds[4 * kImage];
@@ -1012,9 +1018,9 @@ __global__ __launch_bounds__(512) void k_product_f32(ProductArgs a) {
       const int k = kk + (lane >> 4);
       float x[FM], y[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) x[i] = ps[k * BM + place_f32(k, wm + i * 16 + (lane & 15))];
+      for (int i = 0; i < FM; ++i) x[i] = ps[k * BM + place_f32<BM>(k, wm + i * 16 + (lane & 15))];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) y[j] = qs[k * BM + place_f32(k, wn + j * 16 + (lane & 15))];
+      for (int j = 0; j < FN; ++j) y[j] = qs[k * BM + place_f32<BM>(k, wn + j * 16 + (lane & 15))];
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -1023,7 +1029,7 @@ __global__ __launch_bounds__(512) void k_product_f32(ProductArgs a) {
     }
   }
   __syncthreads();
-  static_assert(8 * kStage<FN> <= 4 * kImage);
+  static_assert(S::Threads / 64 * kStage<FN> <= 4 * kImage);
   finish<Bf16>(a, acc, lds + wave * kStage<FN>, to, wm, wn, p.side, q.side, nullptr, nullptr);
 }
 
@@ -1070,9 +1076,15 @@ template <int OP>
 hipError_t launch_f32(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
   ProductArgs a = args;
   void* p[] = {&a};
-  return sink.launch(rule.tile == kMid ? reinterpret_cast<const void*>(&k_product_f32<OP, 128>)
-                                       : reinterpret_cast<const void*>(&k_product_f32<OP, 64>),
-                     dim3(static_cast<unsigned>(rule.grid)), dim3(512), p, 0);
+  auto launch = [&](auto kernel, int threads) {
+    return sink.launch(reinterpret_cast<const void*>(kernel),
+                       dim3(static_cast<unsigned>(rule.grid)), dim3(threads), p, 0);
+  };
+  switch (rule.tile) {
+    case kTiny: return launch(&k_product_f32<OP, 32>, F32Tile<32>::Threads);
+    case kSmall: return launch(&k_product_f32<OP, 64>, F32Tile<64>::Threads);
+    default: return launch(&k_product_f32<OP, 128>, F32Tile<128>::Threads);
+  }
 }
 
 }  // namespace

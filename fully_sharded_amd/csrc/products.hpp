@@ -31,8 +31,9 @@ struct ProductArgs {
 };
 
 // The tiles: rows and columns of results that a workgroup makes.
-enum ProductTile { kThin, kSmall, kMid, kDeep, kBig };
-constexpr int kProductRows[5] = {16, 64, 128, 128, 256};
+// (kTiny: of fp32 operands only, which have kSmall and kMid besides).
+enum ProductTile { kThin, kTiny, kSmall, kMid, kDeep, kBig };
+constexpr int kProductRows[6] = {16, 32, 64, 128, 128, 256};
 inline int product_cols(int tile, int32_t op) {
   return tile == kThin ? (op == FSDP_MATMUL_NT ? 32 : 64) : kProductRows[tile];
 }
