@@ -11,6 +11,9 @@
 namespace fsdp {
 namespace {
 
+// Codes of all receivers that the memory-side cache (256 MiB) still holds.
+constexpr int64_t kCached = int64_t(1) << 28;
+
 // Rows per item of a matrix: about 4,096 elements, a multiple of the four
 // waves that share it.
 int64_t item_rows(int64_t cols) {
@@ -237,7 +240,8 @@ fsdp_status fsdp_gather_quantize(const fsdp_quant* qu, const void* shards, int32
     const fsdp_status st = qu->device(&items);
     if (st != FSDP_OK) return st;
     return status_of(launch_gather_quantize(items, static_cast<int64_t>(qu->items.size()), shards,
-                                            dtype, to, StreamSink(stream)));
+                                            dtype, to, to.n * qu->code_bytes > kCached,
+                                            StreamSink(stream)));
   });
 }
 

@@ -16,35 +16,53 @@ constexpr int kWavePass = 64 * kLane, kGroupPass = kThreads * kLane;
 constexpr int kWavePasses = kWaveRow / kWavePass;
 constexpr int kGroupPasses = 8;              // longer rows are read twice
 
-// `have` of eight adjacent elements as floats, zeros behind; they may begin
-// anywhere.
-__device__ __forceinline__ void load8(const u16* p, int have, float (&x)[8]) {
+// `have` of eight adjacent elements as they are, zeros behind; they may begin
+// anywhere.  A row waits for its largest magnitude in this form: as floats,
+// bf16 rows took twice the registers.
+struct Raw16 {
+  u4 v;
+};
+struct Raw32 {
+  f4 v[2];
+};
+__device__ __forceinline__ Raw16 load8(const u16* p, int have) {
   typedef u4 any __attribute__((aligned(2)));
+  Raw16 r;
   if (have >= 8) {
-    const u4 v = *reinterpret_cast<const any*>(p);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = __uint_as_float(v[k] << 16);
-      x[2 * k + 1] = __uint_as_float(v[k] & 0xffff0000u);
-    }
+    r.v = *reinterpret_cast<const any*>(p);
   } else {
+    r.v = u4{0, 0, 0, 0};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < have ? bf16_to_f32(p[k]) : 0.f;
+    for (int k = 0; k < 7; ++k)
+      if (k < have) r.v[k / 2] |= static_cast<uint32_t>(p[k]) << (k % 2 * 16);
+  }
+  return r;
+}
+__device__ __forceinline__ Raw32 load8(const float* p, int have) {
+  typedef f4 any __attribute__((aligned(4)));
+  Raw32 r;
+  if (have >= 8) {
+    r.v[0] = reinterpret_cast<const any*>(p)[0];
+    r.v[1] = reinterpret_cast<const any*>(p)[1];
+  } else {
+    r.v[0] = r.v[1] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+      if (k < have) r.v[k / 4][k % 4] = p[k];
+  }
+  return r;
+}
+// Their values.
+__device__ __forceinline__ void unpack(const Raw16& r, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = __uint_as_float(r.v[k] << 16);
+    x[2 * k + 1] = __uint_as_float(r.v[k] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, int have, float (&x)[8]) {
-  typedef f4 any __attribute__((aligned(4)));
-  if (have >= 8) {
+__device__ __forceinline__ void unpack(const Raw32& r, float (&x)[8]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f4 v = reinterpret_cast<const any*>(p)[h];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[4 * h + k] = v[k];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = k < have ? p[k] : 0.f;
-  }
+  for (int k = 0; k < 8; ++k) x[k] = r.v[k / 4][k % 4];
 }
 __device__ __forceinline__ void store8(u16* p, int have, const float (&x)[8]) {
   typedef u4 any __attribute__((aligned(2)));
@@ -52,7 +70,7 @@ __device__ __forceinline__ void store8(u16* p, int have, const float (&x)[8]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = f32_to_bf16(x[2 * k]) | f32_to_bf16(x[2 * k + 1]) << 16;
   if (have >= 8) {
-    *reinterpret_cast<any*>(p) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<any*>(p));
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -64,7 +82,8 @@ __device__ __forceinline__ void store8(float* p, int have, const float (&x)[8]) 
   if (have >= 8) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      reinterpret_cast<any*>(p)[h] = f4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+      __builtin_nontemporal_store(f4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]},
+                                  reinterpret_cast<any*>(p) + h);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -115,26 +134,37 @@ __device__ __forceinline__ u2 codes_of(const float (&x)[8], float factor) {
   return v;
 }
 
-// One row by a wave (PASSES = kWavePasses, cols <= kWaveRow) or a workgroup;
-// get(first, have, x) reads eight entries, put(first, codes) stores theirs.
-template <typename G, typename P, typename Q>
-__device__ __forceinline__ void wave_row(int cols, const G& get, const P& put, const Q& done) {
+// One row by a wave (cols <= kWaveRow) or a workgroup.  get(first, have) loads
+// eight entries, val(raw, first, have, x) are their values, put(first, codes)
+// stores theirs and done(scale) the scale.
+template <typename G, typename V, typename P, typename D>
+__device__ __forceinline__ void wave_row(int cols, const G& get, const V& val, const P& put,
+                                         const D& done) {
   const int lane = threadIdx.x & 63, padded = (cols + 15) / 16 * 16;
-  float x[kWavePasses][8];
+  decltype(get(0, 0)) raw[kWavePasses];
   uint32_t m = 0;
 #pragma unroll
   for (int p = 0; p < kWavePasses; ++p) {
     const int at = p * kWavePass + lane * kLane;
-    if (p * kWavePass < cols) get(at, cols - at, x[p]);
+    if (p * kWavePass < cols) raw[p] = get(at, cols - at);
   }
+  float x[8];
 #pragma unroll
-  for (int p = 0; p < kWavePasses; ++p)
-    if (p * kWavePass < cols) m = largest(m, x[p]);
+  for (int p = 0; p < kWavePasses; ++p) {
+    const int at = p * kWavePass + lane * kLane;
+    if (p * kWavePass < cols) {
+      val(raw[p], at, cols - at, x);
+      m = largest(m, x);
+    }
+  }
   const Scale s = scale_of(wave_largest(m));
 #pragma unroll
   for (int p = 0; p < kWavePasses; ++p) {
     const int at = p * kWavePass + lane * kLane;
-    if (at < padded) put(at, codes_of(x[p], s.factor));
+    if (at < padded) {
+      val(raw[p], at, cols - at, x);
+      put(at, codes_of(x, s.factor));
+    }
   }
   if (lane == 0) done(s.scale);
 }
@@ -149,37 +179,45 @@ __device__ __forceinline__ uint32_t group_largest(uint32_t m) {
   return m;
 }
 
-template <typename G, typename P, typename Q>
-__device__ __forceinline__ void group_row(int cols, const G& get, const P& put, const Q& done) {
+template <typename G, typename V, typename P, typename D>
+__device__ __forceinline__ void group_row(int cols, const G& get, const V& val, const P& put,
+                                          const D& done) {
   const int padded = (cols + 15) / 16 * 16, tid = threadIdx.x;
   uint32_t m = 0;
+  float x[8];
   if (cols <= kGroupPasses * kGroupPass) {
-    float x[kGroupPasses][8];
+    decltype(get(0, 0)) raw[kGroupPasses];
 #pragma unroll
     for (int p = 0; p < kGroupPasses; ++p) {
       const int at = p * kGroupPass + tid * kLane;
-      if (p * kGroupPass < cols) get(at, cols - at, x[p]);
+      if (p * kGroupPass < cols) raw[p] = get(at, cols - at);
     }
 #pragma unroll
-    for (int p = 0; p < kGroupPasses; ++p)
-      if (p * kGroupPass < cols) m = largest(m, x[p]);
+    for (int p = 0; p < kGroupPasses; ++p) {
+      const int at = p * kGroupPass + tid * kLane;
+      if (p * kGroupPass < cols) {
+        val(raw[p], at, cols - at, x);
+        m = largest(m, x);
+      }
+    }
     const Scale s = scale_of(group_largest(m));
 #pragma unroll
     for (int p = 0; p < kGroupPasses; ++p) {
       const int at = p * kGroupPass + tid * kLane;
-      if (at < padded) put(at, codes_of(x[p], s.factor));
+      if (at < padded) {
+        val(raw[p], at, cols - at, x);
+        put(at, codes_of(x, s.factor));
+      }
     }
     if (tid == 0) done(s.scale);
   } else {
     for (int at = tid * kLane; at < cols; at += kGroupPass) {
-      float x[8];
-      get(at, cols - at, x);
+      val(get(at, cols - at), at, cols - at, x);
       m = largest(m, x);
     }
     const Scale s = scale_of(group_largest(m));
     for (int at = tid * kLane; at < padded; at += kGroupPass) {
-      float x[8];
-      get(at, cols - at, x);
+      val(get(at, cols - at), at, cols - at, x);
       put(at, codes_of(x, s.factor));
     }
     if (tid == 0) done(s.scale);
@@ -208,11 +246,12 @@ __global__ __launch_bounds__(kThreads) void k_quantize_rows(QuantizeRows a) {
   const T* x = static_cast<const T*>(a.x) + row * a.ldx;
   const float* ch = a.channel ? a.channel + g * a.channel_stride : nullptr;
   int8_t* to = a.codes + row * a.ldc;
-  auto get = [&](int at, int have, float (&v)[8]) {
-    load8(x + at, have, v);
+  auto get = [&](int at, int have) { return load8(x + at, have); };
+  auto val = [&](const auto& raw, int at, int have, float (&v)[8]) {
+    unpack(raw, v);
     if (ch) {
       float c[8];
-      load8(ch + at, have, c);
+      unpack(load8(ch + at, have), c);
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = v[k] * c[k];
     }
@@ -220,9 +259,9 @@ __global__ __launch_bounds__(kThreads) void k_quantize_rows(QuantizeRows a) {
   auto put = [&](int at, u2 v) { *reinterpret_cast<u2*>(to + at) = v; };
   auto done = [&](float s) { a.scales[row] = s; };
   if constexpr (WAVE)
-    wave_row(a.cols, get, put, done);
+    wave_row(a.cols, get, val, put, done);
   else
-    group_row(a.cols, get, put, done);
+    group_row(a.cols, get, val, put, done);
 }
 
 // ------------------------------------------------------------- the gather
@@ -234,7 +273,10 @@ struct GatherArgs {
   int n;
 };
 
-template <typename T, int N>
+// STREAM: codes that the caches cannot hold pass them by (8 receivers of 218M
+// codes each 384 us and 396; 4 of 3.1M stay for their reader, 16.6 and 15.3 us
+// with it).
+template <typename T, int N, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_gather_quantize(const QuantItem* __restrict__ items,
                                                               const T* __restrict__ shards,
                                                               GatherArgs<N> to) {
@@ -250,11 +292,17 @@ __global__ __launch_bounds__(kThreads) void k_gather_quantize(const QuantItem* _
   auto row = [&](int i, auto body) {
     const T* x = shards + w.src + int64_t(i) * w.cols;
     body(
-        w.cols, [&](int at, int have, float (&v)[8]) { load8(x + at, have, v); },
+        w.cols, [&](int at, int have) { return load8(x + at, have); },
+        [&](const auto& raw, int, int, float (&v)[8]) { unpack(raw, v); },
         [&](int at, u2 v) {
-          for (int r = 0; r < to.n; ++r)
-            *reinterpret_cast<u2*>(static_cast<char*>(const_cast<void*>(to.codes[r])) + w.to +
-                                   int64_t(i) * w.pitch + at) = v;
+          for (int r = 0; r < to.n; ++r) {
+            u2* p = reinterpret_cast<u2*>(static_cast<char*>(const_cast<void*>(to.codes[r])) +
+                                          w.to + int64_t(i) * w.pitch + at);
+            if constexpr (STREAM)
+              __builtin_nontemporal_store(v, p);
+            else
+              *p = v;
+          }
         },
         [&](float s) {
           for (int r = 0; r < to.n; ++r)
@@ -333,10 +381,11 @@ GatherArgs<N> gather_args(const QuantBuffers& b) {
 
 template <typename T, int N>
 hipError_t gather(const QuantItem* items, int64_t n, const void* shards, const QuantBuffers& b,
-                  const Sink& sink) {
+                  bool stream, const Sink& sink) {
   GatherArgs<N> a = gather_args<N>(b);
   void* p[] = {&items, &shards, &a};
-  return sink.launch(reinterpret_cast<const void*>(&k_gather_quantize<T, N>),
+  return sink.launch(stream ? reinterpret_cast<const void*>(&k_gather_quantize<T, N, true>)
+                            : reinterpret_cast<const void*>(&k_gather_quantize<T, N, false>),
                      dim3(static_cast<unsigned>(n)), dim3(kThreads), p, 0);
 }
 
@@ -373,12 +422,12 @@ hipError_t quantize(const QuantizeRows& args, const Sink& sink) {
 }  // namespace
 
 hipError_t launch_gather_quantize(const QuantItem* items, int64_t n, const void* shards, int dt,
-                                  const QuantBuffers& to, const Sink& sink) {
+                                  const QuantBuffers& to, bool stream, const Sink& sink) {
   if (dt == FSDP_BF16)
-    return to.n <= kSmallPtrs ? gather<u16, kSmallPtrs>(items, n, shards, to, sink)
-                              : gather<u16, FSDP_MAX_RANKS>(items, n, shards, to, sink);
-  return to.n <= kSmallPtrs ? gather<float, kSmallPtrs>(items, n, shards, to, sink)
-                            : gather<float, FSDP_MAX_RANKS>(items, n, shards, to, sink);
+    return to.n <= kSmallPtrs ? gather<u16, kSmallPtrs>(items, n, shards, to, stream, sink)
+                              : gather<u16, FSDP_MAX_RANKS>(items, n, shards, to, stream, sink);
+  return to.n <= kSmallPtrs ? gather<float, kSmallPtrs>(items, n, shards, to, stream, sink)
+                            : gather<float, FSDP_MAX_RANKS>(items, n, shards, to, stream, sink);
 }
 
 hipError_t launch_dequantize(const QuantItem* items, int64_t n, const QuantBuffers& from,

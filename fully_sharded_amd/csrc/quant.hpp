@@ -67,8 +67,9 @@ struct QuantBuffers {
   int n = 0;
 };
 
+// stream: the codes pass the caches by.
 hipError_t launch_gather_quantize(const QuantItem* items, int64_t n, const void* shards, int dt,
-                                  const QuantBuffers& to, const Sink& sink);
+                                  const QuantBuffers& to, bool stream, const Sink& sink);
 hipError_t launch_dequantize(const QuantItem* items, int64_t n, const QuantBuffers& from,
                              int rest_dt, const PtrArray& full, int out_dt, const Sink& sink);
 

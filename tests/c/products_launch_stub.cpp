@@ -10,7 +10,7 @@ hipError_t launch_product(const ProductArgs&, ProductType, int32_t, const Produc
   return hipErrorNoDevice;
 }
 hipError_t launch_gather_quantize(const QuantItem*, int64_t, const void*, int, const QuantBuffers&,
-                                  const Sink&) {
+                                  bool, const Sink&) {
   return hipErrorNoDevice;
 }
 hipError_t launch_dequantize(const QuantItem*, int64_t, const QuantBuffers&, int, const PtrArray&,
