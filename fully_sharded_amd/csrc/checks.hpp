@@ -12,6 +12,14 @@ namespace fsdp {
 inline bool valid_dtype(int32_t dt) { return dt == FSDP_F32 || dt == FSDP_BF16; }
 inline int64_t dtype_size(int32_t dt) { return dt == FSDP_F32 ? 4 : 2; }
 
+// Elements from the first of n rows, ld apart, to behind `cols` of the last one;
+// -1 if that is no length an array can have.
+inline int64_t reach(int64_t n, int64_t ld, int64_t cols) {
+  if (n <= 0) return 0;
+  const double far = static_cast<double>(n - 1) * static_cast<double>(ld) + static_cast<double>(cols);
+  return far < 0x1p56 ? (n - 1) * ld + cols : -1;
+}
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Range {

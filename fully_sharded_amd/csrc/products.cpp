@@ -14,6 +14,7 @@ constexpr int64_t kCus = 256;      // compute units
 constexpr int64_t kXcds = 8;
 constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
 constexpr int64_t kMaxGroups = 65536;
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxSide = int64_t(1) << 26;
 // Rows that go straight to LDS: 256 of them within 2^31 bytes.
 constexpr int64_t kMaxPitch = (int64_t(1) << 23) - 1;
 
@@ -72,6 +73,21 @@ struct Extents {
   int64_t a, b, c;  // elements from the first to behind the last
 };
 
+// (-1: no length that an array can have)
+Extents extents(const fsdp_matmul& m) {
+  const bool nt = m.op == FSDP_MATMUL_NT;
+  // a group's matrix, then all groups' ones
+  auto stack = [&](int64_t rows, int64_t ld, int64_t cols) {
+    const int64_t one = reach(rows, ld, cols);
+    return one < 0 ? one : reach(m.groups, m.group_stride, one);
+  };
+  if (m.op == FSDP_MATMUL_TN)
+    return Extents{reach(m.rows, m.lda, m.n), reach(m.rows, m.ldb, m.k),
+                   stack(m.n, m.ldc, m.k)};
+  return Extents{reach(m.rows, m.lda, m.k), stack(nt ? m.n : m.k, m.ldb, nt ? m.k : m.n),
+                 reach(m.rows, m.ldc, m.n)};
+}
+
 // Sizes and strides, without the pointers.
 fsdp_status check_sizes(const fsdp_matmul* m, bool codes) {
   if (!m) return FSDP_ERR_INVALID_ARG;
@@ -79,40 +95,21 @@ fsdp_status check_sizes(const fsdp_matmul* m, bool codes) {
       m->groups < 1 || m->rows < 0 || m->n < 1 || m->k < 1 ||
       (m->accumulate != 0 && m->accumulate != 1))
     return FSDP_ERR_INVALID_ARG;
-  const int64_t most = INT32_MAX / 2;
-  if (m->groups > kMaxGroups || m->rows > most || m->n > most || m->k > most)
+  if (m->groups > kMaxGroups || m->rows >= kMaxRows || m->n >= kMaxSide || m->k >= kMaxSide)
     return FSDP_ERR_UNSUPPORTED;
   const int64_t a_cols = m->op == FSDP_MATMUL_TN ? m->n : m->k;
   const int64_t b_cols = m->op == FSDP_MATMUL_NN ? m->n : m->k;
   const int64_t c_cols = m->op == FSDP_MATMUL_TN ? m->k : m->n;
-  const int64_t far = int64_t(1) << 40;
   if (m->lda < a_cols || m->ldb < b_cols || m->ldc < c_cols || m->group_stride < 0)
     return FSDP_ERR_INVALID_ARG;
-  if (m->lda > far || m->ldb > far || m->ldc > far || m->group_stride > far)
-    return FSDP_ERR_UNSUPPORTED;
+  const Extents e = extents(*m);
+  if (e.a < 0 || e.b < 0 || e.c < 0) return FSDP_ERR_UNSUPPORTED;
   // a group's gradient must not meet the next one's
   if (m->op == FSDP_MATMUL_TN && m->groups > 1 &&
       m->group_stride < (m->n - 1) * m->ldc + m->k)
     return FSDP_ERR_INVALID_ARG;
   if (codes && m->k > kMaxSum) return FSDP_ERR_UNSUPPORTED;
   return FSDP_OK;
-}
-
-Extents extents(const fsdp_matmul& m) {
-  const int64_t behind = m.rows > 0 ? m.rows - 1 : 0;
-  Extents e{};
-  if (m.op == FSDP_MATMUL_TN) {
-    e.a = m.rows ? behind * m.lda + m.n : 0;
-    e.b = m.rows ? behind * m.ldb + m.k : 0;
-    e.c = (m.groups - 1) * m.group_stride + (m.n - 1) * m.ldc + m.k;
-  } else {
-    const int64_t rows = m.op == FSDP_MATMUL_NT ? m.n : m.k;
-    const int64_t cols = m.op == FSDP_MATMUL_NT ? m.k : m.n;
-    e.a = m.rows ? behind * m.lda + m.k : 0;
-    e.b = (m.groups - 1) * m.group_stride + (rows - 1) * m.ldb + cols;
-    e.c = m.rows ? behind * m.ldc + m.n : 0;
-  }
-  return e;
 }
 
 // Whether bf16 operands can go straight to LDS: every 16-byte piece of a row
@@ -225,8 +222,8 @@ fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets,
         (m->groups > 1 && m->group_stride % 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
         !aligned(c, ces) || !aligned(offsets, 4) || b_scale_stride < 0)
       return FSDP_ERR_INVALID_ARG;
-    if (m->lda > kMaxPitch || m->ldb > kMaxPitch || b_scale_stride > (int64_t(1) << 40))
-      return FSDP_ERR_UNSUPPORTED;
+    const int64_t scales = b_scale ? reach(m->groups, b_scale_stride, m->n) : 0;
+    if (m->lda > kMaxPitch || m->ldb > kMaxPitch || scales < 0) return FSDP_ERR_UNSUPPORTED;
     const ProductRule rule = product_rule(*m, kProductI8, true);
     if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
     Extents e = extents(*m);
@@ -236,7 +233,7 @@ fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets,
     const Range w = range_of(c, e.c * ces);
     const Range reads[] = {
         range_of(a, e.a), range_of(b, e.b), range_of(a_scale, m->rows * 4),
-        range_of(b_scale, b_scale ? ((m->groups - 1) * b_scale_stride + m->n) * 4 : 0),
+        range_of(b_scale, scales * 4),
         range_of(offsets, offsets ? (int64_t(m->groups) + 1) * 4 : 0)};
     for (const Range& r : reads)
       if (overlap(w, r)) return FSDP_ERR_INVALID_ARG;

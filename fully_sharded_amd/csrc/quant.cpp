@@ -285,9 +285,10 @@ fsdp_status fsdp_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64
         channel_stride < 0 || ldc % 16 || ldc < (cols + 15) / 16 * 16)
       return FSDP_ERR_INVALID_ARG;
     if (!offsets && groups != 1) return FSDP_ERR_INVALID_ARG;
-    const int64_t far = int64_t(1) << 40;
-    if (rows > kMaxItems || cols > kMaxCols || groups > 65536 || ldx > far || ldc > far ||
-        channel_stride > far)
+    const int64_t x_len = reach(rows, ldx, cols), c_len = reach(rows, ldc, (cols + 15) / 16 * 16);
+    const int64_t channels = channel ? reach(groups, channel_stride, cols) : 0;
+    if (rows > kMaxItems || cols > kMaxCols || groups > 65536 || x_len < 0 || c_len < 0 ||
+        channels < 0)
       return FSDP_ERR_UNSUPPORTED;
     const int64_t es = dtype_size(dtype);
     if (!aligned(x, es) || !aligned(channel, 4) || !aligned(offsets, 4) || !aligned(codes, 16) ||
@@ -296,10 +297,10 @@ fsdp_status fsdp_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64
     if (rows == 0) return FSDP_OK;
     if (!x || !codes || !scales) return FSDP_ERR_INVALID_ARG;
     Many reads, writes;
-    reads.add(x, ((rows - 1) * ldx + cols) * es);
-    reads.add(channel, channel ? ((groups - 1) * channel_stride + cols) * 4 : 0);
+    reads.add(x, x_len * es);
+    reads.add(channel, channels * 4);
     reads.add(offsets, offsets ? (int64_t(groups) + 1) * 4 : 0);
-    writes.add(codes, (rows - 1) * ldc + (cols + 15) / 16 * 16);
+    writes.add(codes, c_len);
     writes.add(scales, rows * 4);
     if (meet(writes, reads)) return FSDP_ERR_INVALID_ARG;
     const QuantizeRows a{x,   channel, offsets,        codes,

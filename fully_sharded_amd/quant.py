@@ -127,7 +127,7 @@ def _receivers(qu, what, buffers, numel, dtype=None):
             raise ValueError(f"{what} must have {numel} elements")
         if dtype is None:
             dtype = t.dtype
-        if t.dtype != dtype:
+        if numel and t.dtype != dtype:
             raise ValueError(f"{what} must be {dtype}")
     return buffers, dtype
 

@@ -39,9 +39,15 @@ def test_matmul_refusals(op):
     for more in bad:
         assert matmul(shape(op, **more)) == -1, more
     big = 1 << 30
+    side = 1 << 26
     for more in [dict(groups=65537), dict(rows=big), dict(n=big, lda=big, ldb=big, ldc=big,
                                                           group_stride=big * 40),
-                 dict(lda=(1 << 40) + 1), dict(ldb=(1 << 41)), dict(ldc=1 << 41)]:
+                 dict(n=side, lda=side, ldb=side, ldc=side, group_stride=side * 40),
+                 dict(k=side, lda=side, ldb=side, ldc=side, group_stride=side * 24),
+                 # lengths that no array has, and 64 bits do not hold
+                 dict(lda=1 << 55), dict(ldb=1 << 55), dict(lda=1 << 62), dict(ldb=1 << 62),
+                 dict(ldc=1 << 62, group_stride=(1 << 63) - 1),
+                 dict(group_stride=(1 << 63) - 1, groups=60000)]:
         assert matmul(shape(op, **more)) == -2, more
     m = shape(op)
     assert matmul(None) == -1
@@ -122,7 +128,7 @@ def test_quantize_rows_refusals():
                  dict(codes=at(3)), dict(scales=at(3))]:
         assert rows(**more) == -1, more
     for more in [dict(n=1 << 24), dict(cols=(1 << 30) + 1, ldx=1 << 31, ldc=1 << 31),
-                 dict(groups=65537), dict(ldx=1 << 41), dict(ldc=1 << 41), dict(stride=1 << 41)]:
+                 dict(groups=65537), dict(ldx=1 << 60), dict(ldc=1 << 60), dict(stride=1 << 60)]:
         assert rows(**more) == -2, more
     assert rows(n=0) == 0 and rows(n=0, x=None, codes=None, scales=None) == 0
 
