@@ -41,7 +41,7 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   } else if (r.direct && !weight && tiles(kSmall) < kCus &&
              tiles(kSmall) * ceil_div(m.rows, 16 * met) <= 2 * kCus) {
     r.tile = kThin;
-  } else if (r.direct && tiles(kBig) >= (weight ? 2 * kCus : kCus)) {
+  } else if (r.direct && tiles(kBig) >= (weight && m.groups > 1 ? 2 * kCus : kCus)) {
     r.tile = kBig;
   } else if (tiles(kMid) >= kCus) {
     r.tile = r.direct && type == kProductBf16 && tiles(kMid) <= kCus ? kDeep : kMid;
