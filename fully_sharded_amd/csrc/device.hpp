@@ -49,7 +49,17 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
-// The same and for all its LDS reads, then for the other waves.
+// Wait for all of this wave's LDS accesses, then for the other waves; global
+// loads into registers stay under way.
+__device__ __forceinline__ void meet() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (3 << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Wait for all but N global accesses and all LDS reads, then for the others.
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
   static_assert(N < 64);

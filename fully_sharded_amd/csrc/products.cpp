@@ -15,7 +15,7 @@ constexpr int64_t kXcds = 8;
 constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxSide = int64_t(1) << 26;
-// Rows that go straight to LDS: 256 of them within 2^31 bytes.
+// Bytes from one row of bf16 or codes to the next: 256 rows within 2^31.
 constexpr int64_t kMaxPitch = (int64_t(1) << 23) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -118,7 +118,7 @@ bool pieces(const fsdp_matmul& m, const void* a, const void* b) {
   const int64_t a_cols = m.op == FSDP_MATMUL_TN ? m.n : m.k;
   const int64_t b_cols = m.op == FSDP_MATMUL_NN ? m.n : m.k;
   return aligned(a, 16) && aligned(b, 16) && a_cols % 8 == 0 && b_cols % 8 == 0 &&
-         m.lda % 8 == 0 && m.ldb % 8 == 0 && 2 * m.lda <= kMaxPitch && 2 * m.ldb <= kMaxPitch &&
+         m.lda % 8 == 0 && m.ldb % 8 == 0 &&
          (m.op == FSDP_MATMUL_TN || m.groups == 1 || m.group_stride % 8 == 0);
 }
 
@@ -182,6 +182,8 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
     if (!aligned(a, es) || !aligned(b, es) || !aligned(c, ces) || !aligned(offsets, 4))
       return FSDP_ERR_INVALID_ARG;
     const ProductType type = static_cast<ProductType>(dtype);
+    if (type == kProductBf16 && (2 * m->lda > kMaxPitch || 2 * m->ldb > kMaxPitch))
+      return FSDP_ERR_UNSUPPORTED;
     const ProductRule rule = product_rule(*m, type, pieces(*m, a, b));
     if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
     const Extents e = extents(*m);

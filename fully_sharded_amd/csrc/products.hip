@@ -73,6 +73,9 @@ using Deep = std::conditional_t<OP == FSDP_MATMUL_TN, Tile<128, 128, 4, 2, 4, 2>
                                 Tile<128, 128, 2, 4, 4, 2>>;
 using Big = Tile<256, 256, 2, 4, 2, 2>;
 using Half = Tile<128, 256, 2, 4, 2, 2>;
+// Operands that pass through registers.
+using SmallStaged = Tile<64, 64, 2, 2, 2, 2>;
+using MidStaged = Tile<128, 128, 2, 4, 2, 4>;
 using Quarter = Tile<128, 128, 2, 4, 4, 2>;
 
 // The place of 16-byte piece c of row r along the sum: the 16 rows that a wave
@@ -176,45 +179,67 @@ struct Direct {
   }
 };
 
-// Pieces that pass through registers: for rows that begin anywhere.
-template <typename T, int SIDE, int L, bool ACROSS>
+// Pieces that pass through registers, AHEAD rounds ahead: for rows that begin
+// anywhere.  Every piece is the five words around its entries, of a buffer that
+// ends where the operand does, shifted by half a word where it begins at an odd
+// entry, and what is behind the row's or the sum's end set to 0 when it is
+// written to LDS: loads that branched at the ends were waited for one by one (38
+// us of 777 x 1025 x 2049 in two groups, 24 so).
+template <typename T, int SIDE, int L, bool ACROSS, int AHEAD>
 struct Staged {
+  static_assert(T::kBytes == 2);
   using P = Pieces<T, SIDE, L, ACROSS>;
-  Operand o;
-  u4 v[L];
-  int wave;
+  u4 v[AHEAD][L];
+  uint32_t more[AHEAD][L];  // the fifth words
+  uint32_t off[L];
+  const char* p;
+  int64_t step, bytes;  // to the operand's end
+  int side, sum, wave;
 
-  __device__ __forceinline__ void begin(const Operand& o_, int wave_) {
-    o = o_;
+  __device__ __forceinline__ void begin(const Operand& o, int wave_) {
     wave = wave_;
-  }
-  __device__ __forceinline__ void fetch(int round) {
+    const uint32_t half = reinterpret_cast<uintptr_t>(o.p) & 2;
+    p = o.p - half;
+    side = o.side;
+    sum = o.sum;
+    step = ACROSS ? P::kSum * o.ld : kRow;
+    bytes = half + (ACROSS ? (o.sum - 1) * o.ld + int64_t(o.side) * T::kBytes
+                           : (o.side - 1) * o.ld + int64_t(o.sum) * T::kBytes);
 #pragma unroll
     for (int x = 0; x < L; ++x) {
       const int r = P::row(wave, x), c = P::col(wave, x);
-      const int s = round * P::kSum + (ACROSS ? r : c);  // of the sum
-      const int left = o.sum - s, side = o.side - (ACROSS ? c : r);
-      const int have = ACROSS ? (left > 0 ? side : 0) : (side > 0 ? left : 0);
-      const char* from =
-          o.p + (ACROSS ? s * o.ld + int64_t(c) * T::kBytes : r * o.ld + int64_t(s) * T::kBytes);
-      u4 w = {0, 0, 0, 0};
-      if (have >= P::kEach) {
-        typedef u4 any __attribute__((aligned(2)));
-        w = *reinterpret_cast<const any*>(from);
-      } else {
-        static_assert(T::kBytes == 2);
-        const u16* h = reinterpret_cast<const u16*>(from);
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-          if (e < have) w[e / 2] |= static_cast<uint32_t>(h[e]) << (e % 2 * 16);
-      }
-      v[x] = w;
+      off[x] = half + static_cast<uint32_t>(r) * static_cast<uint32_t>(o.ld) + c * T::kBytes;
+      if ((ACROSS ? c : r) >= o.side) off[x] = kOutside;
     }
   }
-  __device__ __forceinline__ void put(char* image) const {
+  __device__ __forceinline__ void fetch(int round, int set) {
+    int64_t left = (bytes - round * step + 3) & ~int64_t(3);
+    if (left < 0) left = 0;
+    if (left > kOutside - 4) left = kOutside - 4;
+    const auto buffer = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p + round * step), 0, static_cast<int>(left), 0x00020000);
 #pragma unroll
-    for (int x = 0; x < L; ++x)
-      *reinterpret_cast<u4*>(image + (wave * L + x) * 1024 + (threadIdx.x & 63) * 16) = v[x];
+    for (int x = 0; x < L; ++x) {
+      const uint32_t at = off[x] & ~3u;
+      v[set][x] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(buffer, at, 0, 0));
+      more[set][x] = __builtin_amdgcn_raw_buffer_load_b32(buffer, at + 16, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void put(char* image, int round, int set) const {
+    const int left = sum - round * P::kSum;
+#pragma unroll
+    for (int x = 0; x < L; ++x) {
+      const int r = P::row(wave, x), c = P::col(wave, x);
+      const int have = ACROSS ? (r < left ? side - c : 0) : left - c;
+      u4 w = v[set][x];
+      if (off[x] & 2)
+        w = u4{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16,
+               w[3] >> 16 | more[set][x] << 16};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] &= have >= 2 * e + 2 ? 0xffffffffu : have == 2 * e + 1 ? 0xffffu : 0u;
+      *reinterpret_cast<u4*>(image + (wave * L + x) * 1024 + (threadIdx.x & 63) * 16) = w;
+    }
   }
 };
 
@@ -596,6 +621,8 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
   constexpr int FM = S::FM, FN = S::FN, NS = S::NS, LP = S::LP, LQ = S::LQ;
   constexpr bool PA = OP == FSDP_MATMUL_TN, QA = OP != FSDP_MATMUL_NT;
   constexpr int B = T::kBytes, kSum = kRow / B;
+  // (a second round in registers leaves room for one workgroup of 128 tiles)
+  constexpr int kAhead = S::BM == 64 ? 2 : 1;
   using Acc = typename T::Acc;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN;
@@ -605,8 +632,8 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
   const int total = (po.sum + kSum - 1) / kSum;
   if (OP == FSDP_MATMUL_TN && total == 0 && a.accumulate && a.n_parts == 1) return;
 
-  std::conditional_t<DIRECT, Direct<T, S::BM, LP, PA>, Staged<T, S::BM, LP, PA>> pl;
-  std::conditional_t<DIRECT, Direct<T, S::BN, LQ, QA>, Staged<T, S::BN, LQ, QA>> ql;
+  std::conditional_t<DIRECT, Direct<T, S::BM, LP, PA>, Staged<T, S::BM, LP, PA, kAhead>> pl;
+  std::conditional_t<DIRECT, Direct<T, S::BN, LQ, QA>, Staged<T, S::BN, LQ, QA, kAhead>> ql;
   pl.begin(po, wave);
   ql.begin(qo, wave);
   const Fetch<T, S::BM, FM, PA> pf(wm * S::TM);
@@ -670,46 +697,56 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
       else
         wait_and_meet<0>();
     } else {
-      for (int s = 0; s < NS; ++s) {
-        pl.fetch(s);
-        ql.fetch(s);
-        pl.put(lds + s * S::RoundBytes);
-        ql.put(lds + s * S::RoundBytes + S::BM * kRow);
+#pragma unroll
+      for (int s = 0; s < kAhead; ++s) {
+        pl.fetch(s, s);
+        ql.fetch(s, s);
       }
-      __syncthreads();
-      pl.fetch(NS);
-      ql.fetch(NS);
+      pl.put(lds, 0, 0);
+      ql.put(lds + S::BM * kRow, 0, 0);
+      pl.fetch(kAhead, 0);
+      ql.fetch(kAhead, 0);
+      meet();
     }
 #pragma unroll
     for (int j = 0; j < FN; ++j) q[0][j] = qf.get(lds + S::BM * kRow, 0, j);
 #pragma unroll
     for (int i = 0; i < FM; ++i) p[0][i] = pf.get(lds, 0, i);
-    // Before a round's last half: the next round has landed for every wave, and
-    // every wave is done reading this one, whose buffer is loaded again.  The
-    // last round reads operands that nothing uses.
     int buf = 0;
-    auto one = [&](int it, auto loads) {
-      const int next = buf + 1 == NS ? 0 : buf + 1;
-      wait_lds();  // set 0: asked for half a round ago
-      products(0, buf, 1, std::false_type{}, 0, 0);
-      if constexpr (DIRECT) {
+    if constexpr (DIRECT) {
+      // Before a round's last half: the next round has landed for every wave,
+      // and every wave is done reading this one, whose buffer is loaded again.
+      // The last round reads operands that nothing uses.
+      auto one = [&](int it, auto loads) {
+        const int next = buf + 1 == NS ? 0 : buf + 1;
+        wait_lds();  // set 0: asked for half a round ago
+        products(0, buf, 1, std::false_type{}, 0, 0);
         wait_and_meet<decltype(loads)::value ? (NS - 2) * (LP + LQ) : 0>();
         products(1, next, 0, loads, it + NS, buf);
-      } else {
-        __syncthreads();
-        if (decltype(loads)::value) {
-          pl.put(lds + buf * S::RoundBytes);
-          ql.put(lds + buf * S::RoundBytes + S::BM * kRow);
-          pl.fetch(it + NS + 1);
-          ql.fetch(it + NS + 1);
+        buf = next;
+      };
+      int it = 0;
+      for (; it + NS < total; ++it) one(it, std::true_type{});
+      for (; it < total; ++it) one(it, std::false_type{});
+    } else {
+      // Two buffers: the next round's is written while this one's is read.
+      // Rounds behind the last are zeros.
+      for (int it = 0; it < total; it += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int set = (u + 1) % kAhead;  // round it + u + 1
+          char* next = lds + (buf ^ 1) * S::RoundBytes;
+          pl.put(next, it + u + 1, set);
+          ql.put(next + S::BM * kRow, it + u + 1, set);
+          pl.fetch(it + u + 1 + kAhead, set);
+          ql.fetch(it + u + 1 + kAhead, set);
+          products(0, buf, 1, std::false_type{}, 0, 0);
+          meet();
+          products(1, buf ^ 1, 0, std::false_type{}, 0, 0);
+          buf ^= 1;
         }
-        products(1, next, 0, std::false_type{}, 0, 0);
       }
-      buf = next;
-    };
-    int it = 0;
-    for (; it + NS < total; ++it) one(it, std::true_type{});
-    for (; it < total; ++it) one(it, std::false_type{});
+    }
   }
 
   if constexpr (OP == FSDP_MATMUL_TN) {
@@ -1052,8 +1089,8 @@ template <typename T, int OP>
 hipError_t launch_op(const ProductArgs& args, const ProductRule& rule, const Sink& sink) {
   if constexpr (T::kBytes == 2) {
     if (!rule.direct) {
-      if (rule.tile == kSmall) return launch_tile<T, Small, OP, false>(args, rule, sink);
-      return launch_tile<T, Mid<OP>, OP, false>(args, rule, sink);
+      if (rule.tile == kSmall) return launch_tile<T, SmallStaged, OP, false>(args, rule, sink);
+      return launch_tile<T, MidStaged, OP, false>(args, rule, sink);
     }
     if (rule.tile == kDeep) return launch_tile<T, Deep<OP>, OP, true>(args, rule, sink);
   }
