@@ -15,7 +15,7 @@ constexpr int64_t kXcds = 8;
 constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxSide = int64_t(1) << 26;
-// Bytes from one row of bf16 or codes to the next: 256 rows within 2^31.
+// Bytes from one row of an operand to the next: 256 rows within 2^31.
 constexpr int64_t kMaxPitch = (int64_t(1) << 23) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -182,8 +182,7 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
     if (!aligned(a, es) || !aligned(b, es) || !aligned(c, ces) || !aligned(offsets, 4))
       return FSDP_ERR_INVALID_ARG;
     const ProductType type = static_cast<ProductType>(dtype);
-    if (type == kProductBf16 && (2 * m->lda > kMaxPitch || 2 * m->ldb > kMaxPitch))
-      return FSDP_ERR_UNSUPPORTED;
+    if (es * m->lda > kMaxPitch || es * m->ldb > kMaxPitch) return FSDP_ERR_UNSUPPORTED;
     const ProductRule rule = product_rule(*m, type, pieces(*m, a, b));
     if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
     const Extents e = extents(*m);

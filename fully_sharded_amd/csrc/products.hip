@@ -953,9 +953,10 @@ __device__ __forceinline__ int place_f32(int k, int r) {
 template <int BM, bool ACROSS>
 struct F32Operand {
   using S = F32Tile<BM>;
-  const float* p;
-  int64_t ld;
+  const char* p;
+  int64_t step, bytes;  // to the operand's end
   int side, sum;
+  uint32_t off[S::L];
   f4 v[S::L];
 
   // row (or column) and entry of the sum of this lane's x-th four
@@ -967,33 +968,44 @@ struct F32Operand {
     return ACROSS ? static_cast<int>(threadIdx.x) / (BM / 4) + S::Threads * 4 / BM * x
                   : static_cast<int>(threadIdx.x) % 8 * 4;
   }
-  __device__ __forceinline__ void fetch(int from) {
-    typedef f4 any __attribute__((aligned(4)));
-#pragma unroll
-    for (int x = 0; x < S::L; ++x) {
-      const int r = row(x), k = from + entry(x);
-      const int have = ACROSS ? (k < sum ? side - r : 0) : (r < side ? sum - k : 0);
-      const float* at = p + (ACROSS ? k * ld + r : r * ld + k);
-      f4 w = {0.f, 0.f, 0.f, 0.f};
-      if (have >= 4) {
-        w = *reinterpret_cast<const any*>(at);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (e < have) w[e] = at[e];
-      }
-      v[x] = w;
-    }
-  }
-  __device__ __forceinline__ void put(float* image) const {
+  __device__ __forceinline__ void begin(const float* from, int64_t ld, int side_, int sum_) {
+    p = reinterpret_cast<const char*>(from);
+    side = side_;
+    sum = sum_;
+    step = ACROSS ? S::BK * ld * 4 : S::BK * 4;
+    bytes = 4 * (ACROSS ? (sum - 1) * ld + side : (side - 1) * ld + sum);
 #pragma unroll
     for (int x = 0; x < S::L; ++x) {
       const int r = row(x), k = entry(x);
+      off[x] = 4 * (ACROSS ? static_cast<uint32_t>(k) * static_cast<uint32_t>(ld) + r
+                           : static_cast<uint32_t>(r) * static_cast<uint32_t>(ld) + k);
+      if (r >= side) off[x] = kOutside;
+    }
+  }
+  __device__ __forceinline__ void fetch(int round) {
+    int64_t left = bytes - round * step;
+    if (left < 0) left = 0;
+    if (left > kOutside - 4) left = kOutside - 4;
+    const auto buffer = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p + round * step), 0, static_cast<int>(left), 0x00020000);
+#pragma unroll
+    for (int x = 0; x < S::L; ++x)
+      v[x] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(buffer, off[x], 0, 0));
+  }
+  // what is behind the row's or the sum's end becomes 0
+  __device__ __forceinline__ void put(float* image, int round) const {
+#pragma unroll
+    for (int x = 0; x < S::L; ++x) {
+      const int r = row(x), k = entry(x), left = sum - round * S::BK;
+      const int have = ACROSS ? (k < left ? side - r : 0) : left - k;
+      f4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = e < have ? v[x][e] : 0.f;
       if constexpr (ACROSS) {
-        *reinterpret_cast<f4*>(image + k * BM + place_f32<BM>(k, r)) = v[x];
+        *reinterpret_cast<f4*>(image + k * BM + place_f32<BM>(k, r)) = w;
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) image[(k + e) * BM + place_f32<BM>(k + e, r)] = v[x][e];
+        for (int e = 0; e < 4; ++e) image[(k + e) * BM + place_f32<BM>(k + e, r)] = w[e];
       }
     }
   }
@@ -1016,40 +1028,39 @@ __global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArg
   const int i0 = t.i * BM, j0 = t.j * BM;
   F32Operand<BM, OP == FSDP_MATMUL_TN> p;
   F32Operand<BM, OP != FSDP_MATMUL_NT> q;
-  p.p = static_cast<const float*>(a.a);
-  q.p = static_cast<const float*>(a.b);
-  p.ld = a.lda;
-  q.ld = a.ldb;
-  q.side = qrows - j0;
+  const float* pa = static_cast<const float*>(a.a);
+  const float* qb = static_cast<const float*>(a.b);
   int64_t to;
+  int side, sum;
   if constexpr (OP == FSDP_MATMUL_TN) {
-    p.p += t.lo * a.lda + i0;
-    q.p += t.lo * a.ldb + j0;
-    p.side = a.n - i0;
-    p.sum = t.hi - t.lo;
+    pa += t.lo * a.lda + i0;
+    qb += t.lo * a.ldb + j0;
+    side = a.n - i0;
+    sum = t.hi - t.lo;
     to = t.group * a.group_stride + i0 * a.ldc + j0;
-    if (p.sum == 0 && a.accumulate) return;
+    if (sum == 0 && a.accumulate) return;
   } else {
-    p.p += (t.lo + i0) * a.lda;
-    q.p += t.group * a.group_stride + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0));
-    p.side = t.hi - t.lo - i0;
-    p.sum = a.k;
+    pa += (t.lo + i0) * a.lda;
+    qb += t.group * a.group_stride + (OP == FSDP_MATMUL_NT ? j0 * a.ldb : int64_t(j0));
+    side = t.hi - t.lo - i0;
+    sum = a.k;
     to = (t.lo + i0) * a.ldc + j0;
   }
-  q.sum = p.sum;
+  p.begin(pa, a.lda, side, sum);
+  q.begin(qb, a.ldb, qrows - j0, sum);
   const int wm = wave / S::WN * (BM / S::WM), wn = wave % S::WN * (BM / S::WN);
   f4 acc[FM][FN] = {};
   p.fetch(0);
   q.fetch(0);
   int buf = 0;
-  for (int s = 0; s < p.sum; s += BK, buf ^= 1) {
+  for (int it = 0; it * BK < sum; ++it, buf ^= 1) {
     float* ps = lds + buf * 2 * kImage;
     float* qs = ps + kImage;
-    p.put(ps);
-    q.put(qs);
-    __syncthreads();  // and the other buffer, written next, is read
-    p.fetch(s + BK);
-    q.fetch(s + BK);
+    p.put(ps, it);
+    q.put(qs, it);
+    meet();  // and the other buffer, written next, is read
+    p.fetch(it + 1);
+    q.fetch(it + 1);
 #pragma unroll
     for (int kk = 0; kk < BK; kk += 4) {
       const int k = kk + (lane >> 4);

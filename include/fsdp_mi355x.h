@@ -595,7 +595,7 @@ fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, i
  *   may overlap in time (other streams, replays of captured graphs) need
  *   one each.
  *   FSDP_ERR_UNSUPPORTED: more than 65,536 groups, 2^30 rows or more, n or k
- *   of 2^26 or more, rows of a bf16 operand 8 MiB apart or more, or more work than one launch's grid takes. */
+ *   of 2^26 or more, rows of an operand 8 MiB apart or more, or more work than one launch's grid takes. */
 fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, const void* a,
                                 const void* b, int32_t dtype, void* c, int32_t out_dtype,
                                 void* workspace, int64_t workspace_bytes, void* stream);
