@@ -332,8 +332,9 @@ __device__ __forceinline__ bool in_band(int id, int ni, int nj, int* i, int* j) 
 // with one group per lane.
 //   SPLIT: the tiles behind the last that fill all compute units are cut in two
 // or four, t.part being which, where the parts still find a compute unit each:
-// one launch of 1,100 tiles (4.3 per compute unit) of depth 14336 took xx us,
-// and xx without.
+// 1,100 tiles (4.3 per compute unit) of depth 14336 take 1,660 us, and 1,795
+// without; 3,860 of depth 4096 (15.1) 1,644 and 1,670.  (Tiles with at most 128
+// rows left in their group as halves, whole launches over: level or 1% longer.)
 template <int BM, bool SPLIT>
 __device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
   const int lane = threadIdx.x & 63;
@@ -394,25 +395,13 @@ __device__ __forceinline__ Place ragged_tile(const ProductArgs& a, int nj) {
 }
 
 // Tiles of TN: ni x nj of every group, each in a.n_parts parts.  The dies share
-// every group, as groups differ in length.
+// every group, as groups differ in length.  (The longest groups first measured
+// level.)
 __device__ __forceinline__ Place weight_tile(const ProductArgs& a, int ni, int nj) {
   Place t{-1, 0, 0, 0, 0, 0, 1};
   const int tiles = ni * nj, all = tiles * a.n_parts, per = (all + kXcds - 1) / kXcds;
-  const int q = blockIdx.x / kXcds;
-  int g = q / per;
+  const int q = blockIdx.x / kXcds, g = q / per;
   if (g >= a.groups) return t;
-  if (a.offsets && a.groups <= 64) {
-    // the longest groups first: their tiles would otherwise end last
-    const int lane = threadIdx.x & 63;
-    int lo = 0, hi = -1, rank = 0;
-    if (lane < a.groups) rows_of(a, lane, &lo, &hi);
-    const int mine = hi - lo;
-    for (int m = 0; m < a.groups; ++m) {
-      const int other = __builtin_amdgcn_readlane(mine, m);
-      rank += other > mine || (other == mine && m < lane);
-    }
-    g = __builtin_ctzll(__ballot(rank == g));
-  }
   const int die = (blockIdx.x + static_cast<uint32_t>(g) * static_cast<uint32_t>(all)) % kXcds;
   const int id = die * per + q % per;
   if (id >= all) return t;
@@ -498,8 +487,9 @@ __device__ __forceinline__ u4 pack_row(const float (&x)[N]) {
 // A wave's results: entry e of acc[i][j] is row r0 + 16 i + lane % 16, column c0 +
 // 16 j + 4 (lane / 16) + e of what begins at `to`; rows x cols of it exist.  16
 // rows at a time pass through LDS (kStage floats of this wave's own), so that
-// memory gets whole lines: stored as the lanes hold them, 32 bytes of 16 rows
-// at a time, a 256 x 256 tile's end took xx us longer.
+// memory gets whole lines (stored as the lanes hold them, 32 bytes of 16 rows
+// at a time, 256 tiles of 256 x 256 took 3 us longer; their end in a loop over
+// the rows, in place of straight code, level).
 template <int FN>
 constexpr int kStage = 16 * (FN * 16 + 4);
 
@@ -615,6 +605,16 @@ __device__ __forceinline__ uint32_t lds_address(const char* lds) {
 // One tile, all waves on the same rounds of 128 bytes of the sum.  The products
 // of one half of a round are issued row by row with the LDS reads of the next
 // half and the loads of a later round between them.
+//
+// Measured, 256 x 256 tiles: bf16 8192 cubed 757 us (1,450 TFLOP/s; a library's
+// 1,380-1,600 by order of the operands), 8192 x 14336 x 4096 700 us (1,375) in
+// each of the three products; codes 387 us (2,490 TOP/s), 8192 x 4096 x 14336 337
+// (2,860).  A round of 64 KB takes 1.45 us: its products alone 0.83 (2,048 cycles),
+// with the LDS reads 1.15, and the rest is the loads' way from L2 (11-12 TB/s over
+// all dies) and the clock under load (zeros for operands: 1,700 TFLOP/s).  Rounds
+// of 64 bytes four or five deep, all LDS reads at a half's beginning, four waves
+// of 128 x 128 and 32 x 32 matrix instructions measured level to 10% longer.  A
+// tile's beginning and end take 10 us, of which the next tile hides what fits.
 template <typename T, typename S, int OP, bool DIRECT>
 __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i0, int j0,
                                      char* lds) {
@@ -646,15 +646,8 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = Acc{0, 0, 0, 0};
 
-  // bf16: the dies begin at different eighths of the sum, so that they do not
-  // all ask memory for the same columns at once
-  const int start = B == 2 && OP != FSDP_MATMUL_TN
-                        ? static_cast<int>(int64_t(total) * (blockIdx.x % kXcds) / kXcds)
-                        : 0;
   auto load = [&](int round, int buf, int x) {
     if constexpr (DIRECT) {
-      round += start;
-      if (round >= total) round -= total;
       if (x < LP)
         pl.load(round, lds0 + buf * S::RoundBytes, x < LP ? x : 0);
       else
@@ -773,8 +766,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
   }
 }
 
-// ROWS: a 256 x 256 tile's, of which fewer may be left (a group's last rows) or
-// wanted (a tile that is cut): 128 of them take half the time.
+// A workgroup's tile; of the largest, where few are left, a half or a quarter.
 template <typename T, typename S, int OP, bool DIRECT>
 __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a) {
   __shared__ __align__(1024) char lds[S::RoundBytes * S::NS];
@@ -797,8 +789,8 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
         if (i0 < rows && j0 < a.n) tile<T, Quarter, OP, DIRECT>(a, t, i0, j0, lds);
         return;
       }
-      if (t.parts == 2) i0 += t.part * Half::BM;
-      if (t.parts == 2 || rows - i0 <= Half::BM) {
+      if (t.parts == 2) {
+        i0 += t.part * Half::BM;
         if (i0 < rows) tile<T, Half, OP, DIRECT>(a, t, i0, j0, lds);
         return;
       }
