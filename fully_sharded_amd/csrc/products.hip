@@ -1044,7 +1044,19 @@ __global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArg
   p.begin(pa, a.lda, side, sum);
   q.begin(qb, a.ldb, qrows - j0, sum);
   const int wm = wave / S::WN * (BM / S::WM), wn = wave % S::WN * (BM / S::WN);
-  f4 acc[FM][FN] = {};
+  // sums of 128 entries are added up apart: of 8192 entries in one go they were
+  // off by twice as much
+  constexpr int kFlush = 4;
+  f4 acc[FM][FN] = {}, all[FM][FN] = {};
+  auto flush = [&] {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        all[i][j] += acc[i][j];
+        acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+      }
+  };
 #pragma unroll
   for (int u = 0; u < S::Ahead; ++u) {
     p.fetch(u, u);
@@ -1079,10 +1091,12 @@ __global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArg
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(y[j], x[i], acc[i][j], 0, 0, 0);
       }
     }
+    if (it % kFlush == kFlush - S::Ahead) flush();
   }
+  flush();
   __syncthreads();
   static_assert(S::Threads / 64 * kStage<FN> <= 4 * kImage);
-  finish<Bf16>(a, acc, lds + wave * kStage<FN>, to, wm, wn, p.side, q.side, nullptr, nullptr);
+  finish<Bf16>(a, all, lds + wave * kStage<FN>, to, wm, wn, p.side, q.side, nullptr, nullptr);
 }
 
 // ---------------------------------------------------------------- launchers

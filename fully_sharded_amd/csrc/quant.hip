@@ -107,8 +107,8 @@ __device__ __forceinline__ uint32_t wave_largest(uint32_t m) {
 // per entry in place of a division: of bf16 entries it gives the rounding of the
 // exact x 127 / a but at a tie (x = a / 2 and the like), where it gives either
 // neighbour.  (Entries are xs 2^e and as 2^f with 8-bit xs and as: x 127 / a is a
-// tie or at least 1 / (2 as 2^j) from one, j = f - e, while the two roundings move
-// it by at most 2^(7 - j) 2^-23.)
+// tie or at least 1 / (2 as 2^j) from one, j = f - e, while the three roundings
+// move it by less than 2^(7 - j) 2^-22.)
 struct Scale {
   float scale, factor;
 };
@@ -116,7 +116,7 @@ __device__ __forceinline__ Scale scale_of(uint32_t m) {
   if (m >= 0x7f800000u) return Scale{__uint_as_float(0x7fc00000u), 0.f};
   const float a = __uint_as_float(m);
   if (a < 0x1p-100f) return Scale{0.f, 0.f};
-  return Scale{a / 127.f, 127.f / a};
+  return Scale{a * (1.f / 127.f), 1.f / a * 127.f};
 }
 __device__ __forceinline__ u2 codes_of(const float (&x)[8], float factor) {
   u2 v;

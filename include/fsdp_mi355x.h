@@ -620,8 +620,8 @@ fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets,
 
 /* Rows in 8 bits: with x' = x, or x' = x channel[g channel_stride + column]
  * (fp32) where channel is given, a = max |x'| over the row,
- *   scale = a / 127,  code = x' (127 / a)  rounded to nearest, ties to even
- * both divisions and the product rounded to fp32.  A row whose a is below
+ *   scale = a (1 / 127),  code = x' ((1 / a) 127)  rounded to nearest, ties to
+ * even, every reciprocal and product in fp32, in that order.  A row whose a is below
  * 2^-100 gives zeros and the scale 0, one that holds an infinity or a NaN
  * zeros and the scale NaN (so its results are NaN, and no others).
  *   x: rows x cols of dtype, ldx elements from row to row; codes: ldc bytes

@@ -11,14 +11,15 @@ widen, cast = M.widen, M.cast
 
 def quantize(x, channel=None):
     """(codes int8, scales fp32) of the rows of an fp32 x [rows, cols]; channel:
-    fp32, broadcast to x's shape.  Divisions and products in fp32."""
+    fp32, broadcast to x's shape.  Every reciprocal and product in fp32."""
     x = np.asarray(x, np.float32)
     with np.errstate(all="ignore"):
         if channel is not None:
             x = (x * np.asarray(channel, np.float32)).astype(np.float32)
         a = np.abs(x).max(-1, keepdims=True)           # NaN where a row has one
-        scale = (a / np.float32(127)).astype(np.float32)
-        factor = (np.float32(127) / a).astype(np.float32)
+        one = np.float32(1)
+        scale = (a * (one / np.float32(127))).astype(np.float32)
+        factor = ((one / a).astype(np.float32) * np.float32(127)).astype(np.float32)
         codes = np.rint((x * factor).astype(np.float32))
     bad, tiny = ~np.isfinite(a), a < np.float32(2.0 ** -100)
     codes = np.where(bad | tiny, np.float32(0), codes)

@@ -87,8 +87,8 @@ def test_bf16_codes_are_the_exact_roundings():
     exact quotient 127 x / a.  With x = xs 2^e, a = as 2^f and j = f - e >= 0 the
     quotient times 2 as 2^j is a whole number, and so is a tie's (2 c + 1) / 2, so
     it is a tie or at least 1 / (2 as 2^j) >= 2^-(9 + j) from one.  The code is
-    the rounding of x fl(127 / a) in fp32: two roundings of 2^-24 each move it
-    by less than 2^(7 - j) 2^-23 = 2^-(16 + j).  So it is the exact rounding, but
+    the rounding of x fl(fl(1 / a) 127) in fp32: three roundings of 2^-24 each move
+    it by less than 2^(7 - j) 2^-22 = 2^-(15 + j).  So it is the exact rounding, but
     for ties, where the product may be on either side and both neighbours are
     half a step off."""
     sig = np.arange(128, 256).astype(np.float64)
