@@ -22,6 +22,23 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+// The tile: the largest that gives every compute unit one (the weight gradients
+// of several groups, which differ in length: two).  Measured, us a call:
+//   kBig and kMid: one weight's gradient 4096 x 4096, sum 2048 (256 tiles of 256)
+//     59 and 74; 16 groups' of 2048 x 512 (256, groups of 0 to 1,400 rows) 67, 56
+//   kDeep (bf16, no more tiles than compute units) and kMid: 2048 cubed 20 and 26,
+//     8192 x 512 x 2048 in one group 21 and 26; with 288 tiles 35 and 30; codes
+//     level
+//   kMid and kSmall: the same 288 tiles 30 and 34, 8 groups of 1024 x 1024 over
+//     4,096 rows 17.1 and 18.6
+//   kThin and kSmall, codes and weights read along the sum: 16 x 4096 x 14336 11.7
+//     and 28.2, 32 x 4096 x 4096 6.2 and 10.9, 64 x 4096 x 4096 8.2 and 11.1; 64 x
+//     14336 x 4096, where 64 tiles are 224 and thin ones read the weights four
+//     times, 21.0 and 12.6; eight groups of 2048 x 512 with two rows each (256
+//     tiles) 5.0 and 4.8
+//   fp32, kSmall and kTiny: 512 x 512 x 2048 61 and 27, 1024 cubed (256) 33 and 32
+// A weight gradient's sums in parts, where there are fewer tiles than compute
+// units: 2,001 rows of 1001 x 1003 in 28 us.
 ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   ProductRule r{};
   const bool weight = m.op == FSDP_MATMUL_TN;

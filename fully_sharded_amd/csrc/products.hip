@@ -802,7 +802,9 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 // A 16 x 32 tile for few rows, with the sum dealt over 4 waves: wave w takes
 // rounds w, w + 4, ... with loads, LDS and accumulators of its own, so it waits
 // for nothing but its own loads, until the four are added up.  Bound by the
-// weights' way from memory.
+// weights' way from memory: one row of 14336 x 4096 codes 11.7 us (5.0 TB/s), in
+// bf16 22.6 (5.2 TB/s); three or four rounds ahead measured level or longer, as did
+// 32 columns where the weights lie across the sum (36 us and 26).
 template <typename T, int OP>
 __global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
   using S = Tile<16, OP == FSDP_MATMUL_NT ? 32 : 64, 1, 1, 2, 2>;
@@ -921,7 +923,8 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------- fp32
-// fp32 operands: BM x BM results by four or eight waves, 32 of the sum per round, which
+// fp32 operands (4096 cubed 1,150 us, 119 TFLOP/s of the matrix cores' 157; a
+// library's 142): BM x BM results by four or eight waves, 32 of the sum per round, which
 // pass through registers (rows may begin anywhere).  Both operands are kept in
 // LDS as rows across the sum, which is how the matrix instruction reads single
 // entries: entry k of row r at place r ^ 8 (k / 4) ^ 16 (k % 4) of row k, so that
@@ -1044,8 +1047,8 @@ __global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArg
   p.begin(pa, a.lda, side, sum);
   q.begin(qb, a.ldb, qrows - j0, sum);
   const int wm = wave / S::WN * (BM / S::WM), wn = wave % S::WN * (BM / S::WN);
-  // sums of 128 entries are added up apart: of 8192 entries in one go they were
-  // off by twice as much
+  // sums of 128 entries are added up apart: of 8192 entries they are off by 2.5e-7
+  // of the result (rms; a library's in one go by 1.6e-6), for 3% of the time
   constexpr int kFlush = 4;
   f4 acc[FM][FN] = {}, all[FM][FN] = {};
   auto flush = [&] {
