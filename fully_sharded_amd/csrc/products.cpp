@@ -34,8 +34,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   kThin and kSmall, codes and weights read along the sum: 16 x 4096 x 14336 11.7
 //     and 28.2, 32 x 4096 x 4096 6.2 and 10.9, 64 x 4096 x 4096 8.2 and 11.1; 64 x
 //     14336 x 4096, where 64 tiles are 224 and thin ones read the weights four
-//     times, 21.0 and 12.6; eight groups of 2048 x 512 with two rows each (256
-//     tiles) 5.0 and 4.8
+//     times, 21.0 and 12.6; 32 x 14336 x 4096 (448 thin tiles) 13.3 and 11.8, in
+//     bf16 across the sum 40 and 30; eight groups of 2048 x 512 with two rows each
+//     (256 tiles) 5.0 and 4.8
+//   kApart and kSmall, 64-row tiles that are full for the most: 512 x 2048 x 2048
+//     in bf16 10.3 and 11.1, 128 x 4096 x 14336 64 and 84, codes 23 and 30; 400 x
+//     1024 x 4096 in four groups 16.3 and 18.7, codes across the sum 15.5 and 14.1;
+//     sums under 4 KiB: 512 cubed in bf16 5.8 and 4.8; eight groups of 12 rows,
+//     which wait for the weights, 14.3 and 12.9
 //   fp32, kSmall and kTiny: 512 x 512 x 2048 61 and 27, 1024 cubed (256) 33 and 32
 // A weight gradient's sums in parts, where there are fewer tiles than compute
 // units: 2,001 rows of 1001 x 1003 in 28 us.
@@ -56,8 +62,11 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   if (type == kProductF32) {
     r.tile = tiles(kMid) >= kCus ? kMid : tiles(kSmall) >= 2 * kCus ? kSmall : kTiny;
   } else if (r.direct && !weight && tiles(kSmall) < kCus &&
-             tiles(kSmall) * ceil_div(m.rows, 16 * met) <= 2 * kCus) {
+             tiles(kSmall) * ceil_div(m.rows, 16 * met) <= kCus) {
     r.tile = kThin;
+  } else if (r.direct && !weight && tiles(kSmall) <= kCus && m.rows > 64 * met &&
+             m.k * (type == kProductI8 ? 1 : 2) >= 4096) {
+    r.tile = kApart;
   } else if (r.direct && tiles(kBig) >= (weight && m.groups > 1 ? 2 * kCus : kCus)) {
     r.tile = kBig;
   } else if (tiles(kMid) >= kCus) {

@@ -23,8 +23,6 @@
 namespace fsdp {
 namespace {
 
-typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-typedef __bf16 b4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef int i2 __attribute__((ext_vector_type(2)));
 typedef int i4 __attribute__((ext_vector_type(4)));
@@ -60,6 +58,10 @@ struct Tile {
   static constexpr int FM = TM / 16, FN = TN / 16;  // its 16 x 16 parts
   static constexpr int LP = BM * kRow / 1024 / NW, LQ = BN * kRow / 1024 / NW;
   static constexpr int RoundBytes = (BM + BN) * kRow;
+  // LDS of a wave that has rounds, and at the end results, of its own
+  static constexpr int Pitch = BN + 4;
+  static constexpr int Own =
+      RoundBytes * NS > BM * Pitch * 4 ? RoundBytes * NS : BM * Pitch * 4;
 };
 
 using Small = Tile<64, 64, 2, 2, 3, 2>;
@@ -73,10 +75,14 @@ using Deep = std::conditional_t<OP == FSDP_MATMUL_TN, Tile<128, 128, 4, 2, 4, 2>
                                 Tile<128, 128, 2, 4, 4, 2>>;
 using Big = Tile<256, 256, 2, 4, 2, 2>;
 using Half = Tile<128, 256, 2, 4, 2, 2>;
+using Quarter = Tile<128, 128, 2, 4, 4, 2>;
 // Operands that pass through registers.
 using SmallStaged = Tile<64, 64, 2, 2, 2, 2>;
 using MidStaged = Tile<128, 128, 2, 4, 2, 4>;
-using Quarter = Tile<128, 128, 2, 4, 4, 2>;
+// Tiles whose waves share the sum.
+template <int OP>
+using Thin = Tile<16, OP == FSDP_MATMUL_NT ? 32 : 64, 1, 1, 2, 2>;
+using Apart = Tile<64, 64, 1, 1, 2, 1>;
 
 // The place of 16-byte piece c of row r along the sum: the 16 rows that a wave
 // reads at one piece spread over all banks.
@@ -91,12 +97,11 @@ template <int BM, int BYTES>
 __device__ __forceinline__ int place_across(int r, int c) {
   if constexpr (BYTES == 2) {
     const int b = (r & 3) | ((r >> 1) & 4);
-    return c ^ (BM == 32 ? (b & 4) >> 1 : BM == 64 ? b & 6 : b << 1);
+    return c ^ (BM == 64 ? b & 6 : b << 1);
   } else {
     return c ^ (BM == 256  ? (r & 7) | ((r >> 1) & 8)
                 : BM == 128 ? ((r >> 1) & 3) | ((r >> 2) & 4)
-                : BM == 64  ? ((r >> 2) & 1) | ((r >> 3) & 2)
-                            : (r >> 4) & 1);
+                            : ((r >> 2) & 1) | ((r >> 3) & 2));
   }
 }
 
@@ -128,8 +133,7 @@ struct Operand {
   int sum;         // entries of the sum
 };
 
-// This wave's pieces of an operand's round, L of 1024 bytes each.  ROUND: bytes
-// of an along row or entries of an across column per round.
+// This wave's pieces of an operand's round, L of 1024 bytes each.
 template <typename T, int SIDE, int L, bool ACROSS>
 struct Pieces {
   static constexpr int kEach = 16 / T::kBytes;     // entries of a piece
@@ -799,35 +803,38 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
   }
 }
 
-// A 16 x 32 tile for few rows, with the sum dealt over 4 waves: wave w takes
-// rounds w, w + 4, ... with loads, LDS and accumulators of its own, so it waits
-// for nothing but its own loads, until the four are added up.  Bound by the
-// weights' way from memory: one row of 14336 x 4096 codes 11.7 us (5.0 TB/s), in
-// bf16 22.6 (5.2 TB/s); three or four rounds ahead measured level or longer, as did
-// 32 columns where the weights lie across the sum (36 us and 26).
-template <typename T, int OP>
-__global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
-  using S = Tile<16, OP == FSDP_MATMUL_NT ? 32 : 64, 1, 1, 2, 2>;
-  constexpr int FN = S::FN, BN = S::BN, NS = S::NS, LP = S::LP, LQ = S::LQ;
+// A tile with the sum dealt over 4 waves: wave w takes rounds w, w + 4, ... with
+// loads, LDS and accumulators of its own, so it waits for nothing but its own
+// loads, until the four are added up.
+//   Thin, for few rows, is bound by the weights' way from memory: one row of
+// 14336 x 4096 codes 11.7 us (5.0 TB/s), in bf16 22.6 (5.2 TB/s); three or four
+// rounds ahead measured level or longer, as did 32 columns where the weights lie
+// across the sum (36 us and 26).
+//   Apart, for no more tiles than compute units: alone on its unit, a workgroup has
+// nothing else that covers a wait, and four waves that each wait alone wait less
+// than four that meet every round (128 x 4096 x 14336 in bf16 64 us; waves that
+// share the tile's rounds 84).  The joining costs 1 us, so short sums stay there.
+template <typename T, typename S, int OP>
+__global__ __launch_bounds__(256, S::Waves) void k_apart(ProductArgs a) {
+  constexpr int FM = S::FM, FN = S::FN, BN = S::BN, NS = S::NS, LP = S::LP, LQ = S::LQ;
   constexpr bool QA = OP != FSDP_MATMUL_NT;
   constexpr int B = T::kBytes, kSum = kRow / B;
   using Acc = typename T::Acc;
-  static_assert(S::FM == 1);
-  __shared__ __align__(1024) char lds[4 * S::RoundBytes * NS];
-  const Place t = ragged_tile<S::BM, false>(a, (a.n + S::BN - 1) / S::BN);
+  __shared__ __align__(1024) char lds[4 * S::Own];
+  const Place t = ragged_tile<S::BM, false>(a, (a.n + BN - 1) / BN);
   if (t.group < 0) return;
-  const int i0 = t.i * S::BM, j0 = t.j * S::BN, lane = threadIdx.x & 63;
+  const int i0 = t.i * S::BM, j0 = t.j * BN, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const Site site = site_of<T, OP>(a, t, i0, j0);
   const int total = (a.k + kSum - 1) / kSum, mine = (total - wave + 3) / 4;
-  char* own = lds + wave * S::RoundBytes * NS;
-  const uint32_t own0 = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * S::RoundBytes * NS);
+  char* own = lds + wave * S::Own;
+  const uint32_t own0 = __builtin_amdgcn_readfirstlane(lds_address(lds) + wave * S::Own);
   Direct<T, S::BM, LP, false> pl;
-  Direct<T, S::BN, LQ, QA> ql;
+  Direct<T, BN, LQ, QA> ql;
   pl.begin(site.p, 0);
   ql.begin(site.q, 0);
-  const Fetch<T, S::BM, 1, false> pf(0);
-  const Fetch<T, S::BN, FN, QA> qf(0);
+  const Fetch<T, S::BM, FM, false> pf(0);
+  const Fetch<T, BN, FN, QA> qf(0);
   auto load = [&](int r, int buf) {  // behind the last: zeros, not read
 #pragma unroll
     for (int x = 0; x < LP; ++x) pl.load(wave + 4 * r, own0 + buf * S::RoundBytes, x);
@@ -835,17 +842,18 @@ __global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
     for (int x = 0; x < LQ; ++x)
       ql.load(wave + 4 * r, own0 + buf * S::RoundBytes + S::BM * kRow, x);
   };
-  Acc acc[FN] = {};
+  Acc acc[FM][FN] = {};
 #pragma unroll
   for (int s = 0; s < NS; ++s) load(s, s);
   int buf = 0;
   for (int r = 0; r < mine; ++r) {
     wait_loads<(NS - 1) * (LP + LQ)>();
     const char* image = own + buf * S::RoundBytes;
-    u4 p[2], q[2][FN];
+    u4 p[2][FM], q[2][FN];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      p[kk] = pf.get(image, kk, 0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) p[kk][i] = pf.get(image, kk, i);
 #pragma unroll
       for (int j = 0; j < FN; ++j) q[kk][j] = qf.get(image + S::BM * kRow, kk, j);
     }
@@ -855,42 +863,71 @@ __global__ __launch_bounds__(256) void k_thin(ProductArgs a) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-      for (int j = 0; j < FN; ++j) acc[j] = T::mma(q[kk][j], p[kk], acc[j]);
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = T::mma(q[kk][j], p[kk][i], acc[i][j]);
     buf = buf + 1 == NS ? 0 : buf + 1;
   }
   wait_loads<0>();
-  // the four waves' sums, in their order: a few adjacent results per lane
-  static_assert(FN * 1024 <= S::RoundBytes * NS);
+  // the four waves' sums, in their order: adjacent results of a row per lane
 #pragma unroll
-  for (int j = 0; j < FN; ++j)
-    *reinterpret_cast<Acc*>(own + ((lane & 15) * BN + j * 16 + (lane >> 4) * 4) * 4) = acc[j];
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      *reinterpret_cast<Acc*>(own + ((i * 16 + (lane & 15)) * S::Pitch + j * 16 +
+                                     (lane >> 4) * 4) * 4) = acc[i][j];
   __syncthreads();
-  const int r = threadIdx.x >> 4, c = threadIdx.x % 16 * FN;
+  constexpr int kEach = S::BM * BN / 256, kPerRow = BN / kEach;
+  const int r = threadIdx.x / kPerRow, c = threadIdx.x % kPerRow * kEach;
   const int have = a.n - (j0 + c);
   if (i0 + r >= t.hi - t.lo || have <= 0) return;
   using E = std::conditional_t<B == 1, int, float>;
-  E sum[FN] = {};
+  E sum[kEach] = {};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const E* from = reinterpret_cast<const E*>(lds + w * S::RoundBytes * NS) + r * BN + c;
+    const E* from = reinterpret_cast<const E*>(lds + w * S::Own) + r * S::Pitch + c;
 #pragma unroll
-    for (int e = 0; e < FN; ++e) sum[e] += from[e];
+    for (int e = 0; e < kEach; ++e) sum[e] += from[e];
   }
   const int64_t at = site.to + r * a.ldc + c;
+  float x[kEach];
 #pragma unroll
-  for (int e = 0; e < FN; ++e) {
-    if (e >= have) break;
-    float x = static_cast<float>(sum[e]);
+  for (int e = 0; e < kEach; ++e) {
+    x[e] = static_cast<float>(sum[e]);
     if constexpr (B == 1) {
-      x *= a.sa[t.lo + i0 + r];
-      if (a.sb) x *= a.sb[t.group * a.sb_stride + j0 + c + e];
+      x[e] *= a.sa[t.lo + i0 + r];
+      if (a.sb && e < have) x[e] *= a.sb[t.group * a.sb_stride + j0 + c + e];
     }
-    if (a.out_f32) {
-      float* to = static_cast<float*>(a.c) + at + e;
-      *to = a.accumulate ? *to + x : x;
-    } else {
-      u16* to = static_cast<u16*>(a.c) + at + e;
-      *to = static_cast<u16>(f32_to_bf16(a.accumulate ? bf16_to_f32(*to) + x : x));
+  }
+  if constexpr (kEach % 8 == 0) {
+    auto rows = [&](auto f32) {
+      constexpr bool F32 = decltype(f32)::value;
+      constexpr int kN = F32 ? 4 : 8;
+#pragma unroll
+      for (int e = 0; e < kEach; e += kN) {
+        if (e >= have) break;
+        float y[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k) y[k] = x[e + k];
+        if (a.accumulate) add_row<F32>(y, load_row<F32>(a.c, at + e, have - e));
+        store_row<F32>(a.c, at + e, pack_row<F32>(y), have - e);
+      }
+    };
+    if (a.out_f32)
+      rows(std::true_type{});
+    else
+      rows(std::false_type{});
+  } else {
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (e >= have) break;
+      if (a.out_f32) {
+        float* to = static_cast<float*>(a.c) + at + e;
+        *to = a.accumulate ? *to + x[e] : x[e];
+      } else {
+        u16* to = static_cast<u16*>(a.c) + at + e;
+        *to = static_cast<u16>(f32_to_bf16(a.accumulate ? bf16_to_f32(*to) + x[e] : x[e]));
+      }
     }
   }
 }
@@ -1127,10 +1164,12 @@ hipError_t launch_op(const ProductArgs& args, const ProductRule& rule, const Sin
     if (rule.tile == kDeep) return launch_tile<T, Deep<OP>, OP, true>(args, rule, sink);
   }
   if constexpr (OP != FSDP_MATMUL_TN) {
-    if (rule.tile == kThin) {
+    if (rule.tile == kThin || rule.tile == kApart) {
       ProductArgs a = args;
       void* p[] = {&a};
-      return sink.launch(reinterpret_cast<const void*>(&k_thin<T, OP>),
+      return sink.launch(rule.tile == kThin
+                             ? reinterpret_cast<const void*>(&k_apart<T, Thin<OP>, OP>)
+                             : reinterpret_cast<const void*>(&k_apart<T, Apart, OP>),
                          dim3(static_cast<unsigned>(rule.grid)), dim3(256), p, 0);
     }
   }

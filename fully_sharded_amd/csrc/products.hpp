@@ -31,9 +31,10 @@ struct ProductArgs {
 };
 
 // The tiles: rows and columns of results that a workgroup makes.
-// (kTiny: of fp32 operands only, which have kSmall and kMid besides).
-enum ProductTile { kThin, kTiny, kSmall, kMid, kDeep, kBig };
-constexpr int kProductRows[6] = {16, 32, 64, 128, 128, 256};
+// (kTiny: of fp32 operands only, which have kSmall and kMid besides; kThin and
+// kApart: their waves share the sum).
+enum ProductTile { kThin, kTiny, kApart, kSmall, kMid, kDeep, kBig };
+constexpr int kProductRows[7] = {16, 32, 64, 64, 128, 128, 256};
 inline int product_cols(int tile, int32_t op) {
   return tile == kThin ? (op == FSDP_MATMUL_NT ? 32 : 64) : kProductRows[tile];
 }

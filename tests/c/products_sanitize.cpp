@@ -114,7 +114,7 @@ static void check_product(std::mt19937& rng) {
   const bool direct = pick(0, 1);
   const auto type = static_cast<fsdp::ProductType>(pick(0, m.op == FSDP_MATMUL_TN ? 1 : 2));
   const fsdp::ProductRule r = fsdp::product_rule(m, type, direct || type == fsdp::kProductI8);
-  CHECK(r.tile >= 0 && r.tile < 6);
+  CHECK(r.tile >= 0 && r.tile < 7);
   const int64_t rows = fsdp::kProductRows[r.tile], cols = fsdp::product_cols(r.tile, m.op);
   CHECK(r.n_parts >= 1 && r.n_parts <= 64 && r.grid >= 0);
   CHECK(type != fsdp::kProductF32 || ((r.tile == fsdp::kTiny || r.tile == fsdp::kSmall || r.tile == fsdp::kMid) &&
@@ -124,7 +124,7 @@ static void check_product(std::mt19937& rng) {
   auto down = [&](int64_t x) { return (x + rows - 1) / rows; };
   auto across = [&](int64_t x) { return (x + cols - 1) / cols; };
   if (m.op == FSDP_MATMUL_TN) {
-    CHECK(r.tile != fsdp::kThin);
+    CHECK(r.tile != fsdp::kThin && r.tile != fsdp::kApart);
     const int64_t all = down(m.n) * across(m.k) * r.n_parts;
     CHECK(r.grid >= (all + 7) / 8 * 8 * m.groups);
     CHECK(r.join == down(m.n) * across(m.k) * m.groups);

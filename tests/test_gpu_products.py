@@ -162,6 +162,16 @@ def test_few_rows(op, sizes, n, k):
 
 
 @pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,n,k", [([777], 1000, 2056), ([70, 0, 200, 1, 300], 328, 4100),
+                                       ([640], 72, 2048)])
+def test_long_sums_of_few_tiles(op, sizes, n, k):
+    """More rows than the thin tiles take, fewer 64 x 64 tiles than compute
+    units, sums of 4 KiB and more: the waves of a tile share the sum."""
+    exact_case(op, sizes, n, k)
+    exact_case(op, sizes, n, k, out="bf16", accumulate=True, cpad=3, first=1, tail=2)
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
 def test_many_groups(op):
     """More groups than a wave has lanes, most of them empty."""
     rng = np.random.default_rng(3)
@@ -324,6 +334,14 @@ def test_products_of_codes_last_tiles_and_few_rows(op, sizes, n, k):
     i8_case(op, sizes, n, k)
     if sum(sizes) < 300:
         i8_case(op, sizes, n, k, out="bf16", accumulate=True, first=1, tail=2, scales=False)
+
+
+@pytest.mark.parametrize("op", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,n,k", [([777], 1000, 4112), ([70, 0, 200, 1, 300], 329, 5001),
+                                       ([640], 72, 4096)])
+def test_products_of_codes_long_sums_of_few_tiles(op, sizes, n, k):
+    i8_case(op, sizes, n, k)
+    i8_case(op, sizes, n, k, out="bf16", accumulate=True, first=1, tail=2, scales=False)
 
 
 def test_codes_longest_sum():
