@@ -17,8 +17,9 @@ Tensors are matrices with rows anywhere (stride of the last dimension 1);
 weights may have a leading dimension of groups.  Every call runs on the GPU
 that holds its tensors, which has to be the current one, and on the current
 stream unless another is given; tensors of a call on another stream have to
-live until it is done there.  The bind_* forms check the tensors and marshal
-the pointers once, for loops.
+live until it is done there, and the caller orders it with what else writes and
+reads them.  The bind_* forms check the tensors and marshal the pointers once,
+for loops.
 """
 
 from __future__ import annotations
@@ -105,8 +106,20 @@ def _workspace_bytes(shape, dtype):
 
 def grouped_matmul_workspace(op, a, b, c):
     """A workspace for this product, or None where it needs none."""
+    return _workspace_for(op, a, b, c, None)
+
+
+def _workspace_for(op, a, b, c, stream):
+    """grouped_matmul_workspace for a call on `stream` (None: the current one).
+    Memory that the allocator hands out may still be in use by work of the
+    stream that it is allocated on, so that is the stream that will use it."""
     n = _workspace_bytes(_shape(op, a, b, c, False), _dtype_code(a))
-    return torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
+    if not n or stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=a.device) if n else None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_b._stream(stream).value or 0)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=a.device)
 
 
 def _plain(op, a, b, c, offsets, accumulate, workspace):
@@ -117,8 +130,6 @@ def _plain(op, a, b, c, offsets, accumulate, workspace):
         raise ValueError("a and b must have one dtype")
     out = _dtype_code(c)
     off = _offsets(offsets, shape.groups)
-    if workspace is None:
-        workspace = grouped_matmul_workspace(op, a, b, c)
     ws, n = None, 0
     if workspace is not None:
         if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
@@ -133,9 +144,16 @@ def _plain(op, a, b, c, offsets, accumulate, workspace):
 def bind_grouped_matmul(op: str, a, b, c, offsets=None, accumulate: bool = False,
                         workspace=None):
     """fsdp_grouped_matmul with cached arguments; call as f(stream=None).  A
-    workspace that is needed and not given is allocated and kept: calls of one
-    binding that may overlap in time, on two streams or in replays of two
-    captured graphs, then race on it."""
+    workspace that is needed and not given is allocated and kept, and the
+    binding waits for the current stream, whose work may still use that memory
+    (bound while that stream is captured it does not: such a workspace is the
+    graph's): so any stream may use it, but calls of one binding that may
+    overlap in time, on two streams or in replays of two captured graphs, race
+    on it."""
+    if workspace is None:
+        workspace = grouped_matmul_workspace(op, a, b, c)
+        if workspace is not None and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(a.device).synchronize()
     args, keep, tensors = _plain(op, a, b, c, offsets, accumulate, workspace)
     return _bound("fsdp_grouped_matmul", args, keep, tensors)
 
@@ -147,13 +165,10 @@ def fsdp_grouped_matmul(op: str, a, b, c, offsets=None, accumulate: bool = False
       "nt"  c[t] = a[t] b_g^T      "nn"  c[t] = a[t] b_g
       "tn"  c_g = a[rows of g]^T b[rows of g]
     accumulate: added to what c holds."""
+    if workspace is None:
+        workspace = _workspace_for(op, a, b, c, stream)
     args, keep, tensors = _plain(op, a, b, c, offsets, accumulate, workspace)
     _bound("fsdp_grouped_matmul", args, keep, tensors)(stream)
-    if workspace is None and stream is not None and keep[-1].dtype == torch.uint8:
-        # the allocator may hand it out again only when the call is done there
-        of = torch.cuda.ExternalStream(stream.value or 0) \
-            if isinstance(stream, ctypes.c_void_p) else stream
-        keep[-1].record_stream(of)
 
 
 def _codes(t, what, dims=(2,)):
