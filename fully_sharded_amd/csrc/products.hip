@@ -938,6 +938,9 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
   constexpr int FM = S::FM, FN = S::FN;
   const int ni = (a.n + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
   const int g = blockIdx.x / (ni * nj), id = blockIdx.x % (ni * nj);
+  int lo, hi;
+  rows_of(a, g, &lo, &hi);
+  if (a.accumulate && lo == hi) return;  // nothing to add: C as it is (a -0 too)
   const int i0 = id / nj * S::BM, j0 = id % nj * S::BN;
   const int wave = threadIdx.x >> 6;
   __shared__ __align__(16) float stage[S::NW * kStage<FN>];
@@ -955,7 +958,8 @@ __global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] += part[(i * FN + j) * S::Threads];
   }
-  finish<Bf16>(a, acc, stage + wave * kStage<FN>, g * a.group_stride + int64_t(i0) * a.ldc + j0, wave / S::WN * S::TM,
+  finish<Bf16>(a, acc, stage + wave * kStage<FN>,
+               g * a.group_stride + int64_t(i0) * a.ldc + j0, wave / S::WN * S::TM,
                wave % S::WN * S::TN, a.n - i0, a.k - j0, nullptr, nullptr);
 }
 
