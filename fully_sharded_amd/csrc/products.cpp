@@ -26,11 +26,23 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // of several groups, which differ in length: two).  Measured, us a call:
 //   kBig and kMid: one weight's gradient 4096 x 4096, sum 2048 (256 tiles of 256)
 //     59 and 74; 16 groups' of 2048 x 512 (256, groups of 0 to 1,400 rows) 67, 56
-//   kDeep (bf16, no more tiles than compute units) and kMid: 2048 cubed 20 and 26,
-//     8192 x 512 x 2048 in one group 21 and 26; with 288 tiles 35 and 30; codes
-//     level
-//   kMid and kSmall: the same 288 tiles 30 and 34, 8 groups of 1024 x 1024 over
-//     4,096 rows 17.1 and 18.6
+//   kDeep, kMid and kSmall (bf16, up to one tile of 128 per compute unit: a workgroup
+//   has all of its LDS, and four rounds in it):
+//     n = 2048, sum 2048: 128 tiles of 128 17, 24 and 15, 144 to 192 17, 24 and 20,
+//     208 to 240 18, 25 and 26, 256 19, 25 and 26, 272 33, 26 and 30; sum 4096: 128
+//     28, 42 and 26, 144 28, 43 and 35, 256 33, 44 and 49; sum 512: 128 7.6, 8.0 and
+//     6.4, 144 8.0, 9.1 and 8.0, 256 8.6, 9.7 and 11.1; the other two products within
+//     a tenth of these.  200 tiles that hold 400 of 64 (25600 x 64), which all run at
+//     once: along the sum 2048 30, 37 and 29, 4096 47, 65 and 49; across it 1024
+//     12.3, 14.3 and 12.9, 2048 25, 32 and 32.
+//     Several groups: 12 of 80 rows each (208 tiles), sum 512 9.2, 9.8 and 9.0, 768
+//     11.9, 13.1 and 12.5; 6 of 100 (224), sum 512 9.9, 10.1 and 9.0; four of 250 on
+//     average (144), sum 512 8.1, 9.2 and 8.6, 256 6.3, 6.5 and 6.1, of 400 (224) 512
+//     8.7, 9.7 and 11.3; weight gradients of four of 512 rows on average, 160 tiles
+//     10.6, 12.6 and 9.5, 224 11.9, 13.3 and 12.9.
+//   Codes: kDeep and kMid level.
+//   kMid and kSmall: 288 tiles (8192 x 512 x 2048 in 16 groups) 30 and 34, 8 groups
+//     of 1024 x 1024 over 4,096 rows 17.1 and 18.6
 //   kThin and kSmall, codes and weights read along the sum: 16 x 4096 x 14336 11.7
 //     and 28.2, 32 x 4096 x 4096 6.2 and 10.9, 64 x 4096 x 4096 8.2 and 11.1; 64 x
 //     14336 x 4096, where 64 tiles are 224 and thin ones read the weights four
@@ -57,6 +69,13 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
     return (met == 1 ? ceil_div(m.rows, down) : std::max(met, m.rows / down + (met + 1) / 2)) *
            ceil_div(m.n, across);
   };
+  // of up to one tile of 128 per compute unit
+  auto deep = [&] {
+    const int64_t t = tiles(kMid), sum = weight ? m.rows / met : m.k;
+    if (t <= kCus / 2) return false;
+    if (tiles(kSmall) <= 2 * kCus) return sum >= (m.op == FSDP_MATMUL_NT ? 4096 : 2048);
+    return met == 1 || sum >= 768 || (t > 3 * kCus / 4 && (weight || m.rows >= 128 * met));
+  };
   r.direct = direct && type != kProductF32;
   r.tile = kSmall;
   if (type == kProductF32) {
@@ -69,8 +88,10 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
     r.tile = kApart;
   } else if (r.direct && tiles(kBig) >= (weight && m.groups > 1 ? 2 * kCus : kCus)) {
     r.tile = kBig;
+  } else if (r.direct && type == kProductBf16 && tiles(kMid) <= kCus) {
+    if (deep()) r.tile = kDeep;
   } else if (tiles(kMid) >= kCus) {
-    r.tile = r.direct && type == kProductBf16 && tiles(kMid) <= kCus ? kDeep : kMid;
+    r.tile = kMid;
   }
   const int64_t down = kProductRows[r.tile], across = product_cols(r.tile, m.op);
   r.n_parts = 1;
@@ -78,7 +99,7 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
     const int64_t per_group = ceil_div(m.n, down) * ceil_div(m.k, across);
     const int64_t all = per_group * m.groups;
     // long sums of few tiles in parts, eight rounds of 64 rows or more each
-    if (type == kProductBf16 && all < kCus)
+    if (type == kProductBf16 && r.tile == kSmall && all < kCus)
       r.n_parts = static_cast<int>(std::max<int64_t>(
           1, std::min<int64_t>({2 * kCus / all, m.rows / met / 512, 64})));
     r.grid = kXcds * ceil_div(per_group * r.n_parts, kXcds) * m.groups;

@@ -1,0 +1,58 @@
+"""Which kernels the unit's products get (no GPU): the rules that choose between
+their forms."""
+
+import os
+
+import pytest
+
+from tests import products_rules as R
+from tests.products_tiles import CASES
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    """f([(op, type, groups, rows, n, k), ...]) -> their Rules."""
+    if not os.path.exists(R.HIPCC):
+        pytest.skip("no hipcc")
+    exe = R.build(tmp_path_factory.mktemp("rules"))
+    return lambda products: R.rules(exe, products)
+
+
+def test_cases_get_the_kernels_that_they_are_named_for(rules):
+    """The products by which every kernel is tested on the GPU."""
+    got = rules([(op, kind, len(sizes), sum(sizes), n, k, 0, 0, 0, int(off == 0))
+                 for op, kind, sizes, n, k, off in CASES.values()])
+    for name, r in zip(CASES, got):
+        kind, op, tile, how = name.split()[:4]
+        assert (kind, op) == (CASES[name][1], CASES[name][0]) and r.status == R.REACHED, name
+        assert (r.tile, r.direct) == (tile, how == "direct"), (name, r)
+
+
+@pytest.mark.parametrize("op", R.OPS)
+def test_tiles_by_their_number(rules, op):
+    """bf16 products of one weight with a sum of 2048, by their number of 128 x 128
+    tiles: 64 x 64 ones up to half of the 256 compute units, where four times as
+    many still run at once, deep ones up to all of them, shallow ones beyond.  No
+    number stands alone."""
+    def product(t):
+        return (op, "bf16", 1, 2048, 128 * t, 2048) if op == "tn" else \
+            (op, "bf16", 1, 128 * t, 2048, 2048)
+    for down, r in zip(range(2, 24), rules([product(t) for t in range(2, 24)])):
+        tiles = 16 * down
+        want = {"deep"} if 128 < tiles <= 256 else {"mid"} if tiles > 256 else {"small", "apart"}
+        assert r.tile in want, (tiles, r)
+    # a few rows fewer or more do not change it
+    near = [(op, "bf16", 1, 2048, x, 2048) if op == "tn" else (op, "bf16", 1, x, 2048, 2048)
+            for x in (1920, 2000, 2040)]
+    assert [r.tile for r in rules(near)] == ["deep"] * 3
+
+
+def test_sums_in_parts_are_of_small_tiles(rules):
+    """The joining launch is there for them alone."""
+    products = [("tn", kind, groups, rows, n, k)
+                for kind in ("f32", "bf16") for groups in (1, 3) for rows in (900, 40000)
+                for n in (64, 200, 1000, 2000) for k in (8, 72, 1003, 2100)]
+    got = rules(products)
+    assert any(r.parts > 1 for r in got)
+    for p, r in zip(products, got):
+        assert r.parts == 1 or (r.tile == "small" and p[1] == "bf16"), (p, r)
