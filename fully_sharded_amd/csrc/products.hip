@@ -746,7 +746,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i
     }
   }
 
-  if constexpr (OP == FSDP_MATMUL_TN) {
+  if constexpr (OP == FSDP_MATMUL_TN && S::BM == Small::BM) {
     if (a.n_parts > 1) {
       const int ni = (a.n + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
       const int64_t at = ((int64_t(t.group) * ni * nj + t.i * nj + t.j) * a.n_parts + t.part) *
@@ -932,9 +932,11 @@ __global__ __launch_bounds__(256, S::Waves) void k_apart(ProductArgs a) {
   }
 }
 
-// A weight gradient's tiles that came in parts, added up in their order.
-template <typename S>
-__global__ __launch_bounds__(S::Threads) void k_join_parts(ProductArgs a) {
+// A weight gradient's tiles that came in parts, added up in their order.  Parts
+// are of 64 x 64 tiles: there are few results.
+__global__ __launch_bounds__(Small::Threads) void k_join_parts(ProductArgs a) {
+  using S = Small;
+  static_assert(S::WM == SmallStaged::WM && S::WN == SmallStaged::WN);
   constexpr int FM = S::FM, FN = S::FN;
   const int ni = (a.n + S::BM - 1) / S::BM, nj = (a.k + S::BN - 1) / S::BN;
   const int g = blockIdx.x / (ni * nj), id = blockIdx.x % (ni * nj);
@@ -1150,9 +1152,9 @@ hipError_t launch_tile(const ProductArgs& args, const ProductRule& rule, const S
   void* p[] = {&a};
   hipError_t e = sink.launch(reinterpret_cast<const void*>(&k_product<T, S, OP, DIRECT>),
                              dim3(static_cast<unsigned>(rule.grid)), dim3(S::Threads), p, 0);
-  if constexpr (OP == FSDP_MATMUL_TN) {
+  if constexpr (OP == FSDP_MATMUL_TN && S::BM == Small::BM) {
     if (e == hipSuccess && rule.n_parts > 1)
-      e = sink.launch(reinterpret_cast<const void*>(&k_join_parts<S>),
+      e = sink.launch(reinterpret_cast<const void*>(&k_join_parts),
                       dim3(static_cast<unsigned>(rule.join)), dim3(S::Threads), p, 0);
   }
   return e;

@@ -580,7 +580,8 @@ typedef struct fsdp_matmul {
 } fsdp_matmul;
 
 /* Bytes of the workspace that fsdp_grouped_matmul takes for these sizes and
- * operands of dtype (0 for most: only long sums of few results use one). */
+ * operands of dtype (0 for most: only bf16 weight gradients, TN, with few
+ * results and long sums use one, which are made in parts). */
 fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, int64_t* bytes);
 
 /* The product of bf16 or fp32 operands (both of dtype).  Sums are fp32, in a
