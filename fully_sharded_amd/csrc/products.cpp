@@ -15,7 +15,8 @@ constexpr int64_t kXcds = 8;
 constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxSide = int64_t(1) << 26;
-// Bytes from one row of an operand to the next: 256 rows within 2^31.
+// Bytes from one row of an operand to the next: 256 rows within 2^31.  (Of one
+// row, nothing is reached by it.)
 constexpr int64_t kMaxPitch = (int64_t(1) << 23) - 1;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -159,6 +160,22 @@ fsdp_status check_sizes(const fsdp_matmul* m, bool codes) {
   return FSDP_OK;
 }
 
+// The product with the pitches of operands of one row, which nothing is apart
+// by, set to the row's length.
+fsdp_matmul with_pitches(const fsdp_matmul& given) {
+  fsdp_matmul m = given;
+  const bool tn = m.op == FSDP_MATMUL_TN, nt = m.op == FSDP_MATMUL_NT;
+  if (m.rows <= 1) m.lda = tn ? m.n : m.k;
+  if ((tn ? m.rows : nt ? m.n : m.k) <= 1) m.ldb = nt || tn ? m.k : m.n;
+  return m;
+}
+// Whether rows of either operand, of es bytes per entry, lie too far apart.
+bool too_far(const fsdp_matmul& m, int64_t es) {
+  const int64_t b_rows =
+      m.op == FSDP_MATMUL_TN ? m.rows : m.op == FSDP_MATMUL_NT ? m.n : m.k;
+  return (m.rows > 1 && m.lda > kMaxPitch / es) || (b_rows > 1 && m.ldb > kMaxPitch / es);
+}
+
 // Whether bf16 operands can go straight to LDS: every 16-byte piece of a row
 // is aligned and inside the row.
 bool pieces(const fsdp_matmul& m, const void* a, const void* b) {
@@ -213,13 +230,14 @@ fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, i
   return FSDP_OK;
 }
 
-fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, const void* a,
+fsdp_status fsdp_grouped_matmul(const fsdp_matmul* given, const int32_t* offsets, const void* a,
                                 const void* b, int32_t dtype, void* c, int32_t out_dtype,
                                 void* workspace, int64_t workspace_bytes, void* stream) {
   return guarded([&]() -> fsdp_status {
     if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return FSDP_ERR_INVALID_ARG;
-    fsdp_status st = check_sizes(m, false);
+    fsdp_status st = check_sizes(given, false);
     if (st != FSDP_OK) return st;
+    const fsdp_matmul one = with_pitches(*given), *m = &one;
     if (!offsets && m->groups != 1) return FSDP_ERR_INVALID_ARG;
     const bool reads_b = m->op != FSDP_MATMUL_TN || m->rows > 0;
     // (an array of nothing may be at NULL)
@@ -229,7 +247,7 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
     if (!aligned(a, es) || !aligned(b, es) || !aligned(c, ces) || !aligned(offsets, 4))
       return FSDP_ERR_INVALID_ARG;
     const ProductType type = static_cast<ProductType>(dtype);
-    if (es * m->lda > kMaxPitch || es * m->ldb > kMaxPitch) return FSDP_ERR_UNSUPPORTED;
+    if (too_far(*m, es)) return FSDP_ERR_UNSUPPORTED;
     const ProductRule rule = product_rule(*m, type, pieces(*m, a, b));
     if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
     const Extents e = extents(*m);
@@ -255,23 +273,25 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
   });
 }
 
-fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets, const int8_t* a,
-                                   const float* a_scale, const int8_t* b, const float* b_scale,
-                                   int64_t b_scale_stride, void* c, int32_t out_dtype,
-                                   void* stream) {
+fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* given, const int32_t* offsets,
+                                   const int8_t* a, const float* a_scale, const int8_t* b,
+                                   const float* b_scale, int64_t b_scale_stride, void* c,
+                                   int32_t out_dtype, void* stream) {
   return guarded([&]() -> fsdp_status {
     if (!valid_dtype(out_dtype) || !b) return FSDP_ERR_INVALID_ARG;
-    fsdp_status st = check_sizes(m, true);
+    fsdp_status st = check_sizes(given, true);
     if (st != FSDP_OK) return st;
+    if (given->lda % 16 || given->ldb % 16) return FSDP_ERR_INVALID_ARG;
+    const fsdp_matmul one = with_pitches(*given), *m = &one;
     if (!offsets && m->groups != 1) return FSDP_ERR_INVALID_ARG;
     if (m->rows > 0 && (!a || !a_scale || !c)) return FSDP_ERR_INVALID_ARG;
     const int64_t ces = dtype_size(out_dtype);
-    if (!aligned(a, 16) || !aligned(b, 16) || m->lda % 16 || m->ldb % 16 ||
-        (m->groups > 1 && m->group_stride % 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
-        !aligned(c, ces) || !aligned(offsets, 4) || b_scale_stride < 0)
+    if (!aligned(a, 16) || !aligned(b, 16) || (m->groups > 1 && m->group_stride % 16) ||
+        !aligned(a_scale, 4) || !aligned(b_scale, 4) || !aligned(c, ces) || !aligned(offsets, 4) ||
+        b_scale_stride < 0)
       return FSDP_ERR_INVALID_ARG;
     const int64_t scales = b_scale ? reach(m->groups, b_scale_stride, m->n) : 0;
-    if (m->lda > kMaxPitch || m->ldb > kMaxPitch || scales < 0) return FSDP_ERR_UNSUPPORTED;
+    if (too_far(*m, 1) || scales < 0) return FSDP_ERR_UNSUPPORTED;
     const ProductRule rule = product_rule(*m, kProductI8, true);
     if (!fits(rule)) return FSDP_ERR_UNSUPPORTED;
     Extents e = extents(*m);

@@ -596,7 +596,8 @@ fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, i
  *   may overlap in time (other streams, replays of captured graphs) need
  *   one each.
  *   FSDP_ERR_UNSUPPORTED: more than 65,536 groups, 2^30 rows or more, n or k
- *   of 2^26 or more, rows of an operand 8 MiB apart or more, or more work than one launch's grid takes. */
+ *   of 2^26 or more, rows of an operand 8 MiB apart or more (an operand of one
+ *   row may be longer), or more work than one launch's grid takes. */
 fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, const void* a,
                                 const void* b, int32_t dtype, void* c, int32_t out_dtype,
                                 void* workspace, int64_t workspace_bytes, void* stream);
@@ -612,8 +613,8 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
  *   Codes' rows begin at multiples of 16 bytes, are readable to the next
  *   multiple of 16 behind their end, and A's are zero there
  *   (fsdp_quantize_rows and fsdp_gather_quantize leave them so).
- *   k is at most 131,072, rows of codes shorter than 8 MiB (else
- *   FSDP_ERR_UNSUPPORTED); otherwise as fsdp_grouped_matmul. */
+ *   k is at most 131,072 (else FSDP_ERR_UNSUPPORTED); otherwise as
+ *   fsdp_grouped_matmul. */
 fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets, const int8_t* a,
                                    const float* a_scale, const int8_t* b, const float* b_scale,
                                    int64_t b_scale_stride, void* c, int32_t out_dtype,

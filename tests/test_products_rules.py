@@ -56,3 +56,35 @@ def test_sums_in_parts_are_of_small_tiles(rules):
     assert any(r.parts > 1 for r in got)
     for p, r in zip(products, got):
         assert r.parts == 1 or (r.tile == "small" and p[1] == "bf16"), (p, r)
+
+
+LONG = 1 << 22   # entries: 8 MiB in bf16
+
+
+@pytest.mark.parametrize("kind,groups,op,rows,n,k", [
+    ("bf16", 1, "tn", 1, LONG, 8), ("bf16", 1, "tn", 1, 8, LONG + 1), ("bf16", 1, "nn", 3, LONG, 1),
+    ("bf16", 5, "nn", 7, LONG + 3, 1), ("bf16", 1, "nt", 1, 1, LONG), ("f32", 1, "tn", 1, LONG, 3),
+    ("f32", 2, "nn", 3, LONG, 1), ("f32", 1, "nt", 1, 1, LONG), ("bf16", 1, "nt", 1, 1, 1 << 25),
+    ("i8", 1, "nn", 3, 1 << 23, 1)])
+def test_operands_of_one_row_may_be_long(rules, kind, groups, op, rows, n, k):
+    """Rows 8 MiB apart are refused; of one row nothing is apart, whatever the
+    pitch is said to be."""
+    far = 1 << 59 if kind == "i8" else (1 << 62) + 3
+    lone_a = rows == 1
+    lone_b = {"tn": rows, "nt": n, "nn": k}[op] == 1
+    for lda in (0, far) if lone_a else (0,):
+        for ldb in (0, far) if lone_b and groups == 1 else (0,):
+            r, = rules([(op, kind, groups, rows, n, k, lda, ldb, 0, 1)])
+            assert r.status == R.REACHED, (lda, ldb, r)
+
+
+@pytest.mark.parametrize("op,rows,n,k", [("tn", 2, LONG, 8), ("tn", 2, 8, LONG),
+                                         ("nn", 3, LONG, 2), ("nt", 1, 2, LONG),
+                                         ("nt", 2, 1, LONG)])
+def test_rows_far_apart_are_refused(rules, op, rows, n, k):
+    at_most = (1 << 23) - 1
+    assert [r.status for r in rules([
+        (op, "bf16", 1, rows, n, k), (op, "f32", 1, rows, n, k),
+        (op, "f32", 1, rows, min(n, at_most // 4), min(k, at_most // 4)),
+        (op, "bf16", 1, rows, min(n, at_most // 2), min(k, at_most // 2))])] == \
+        [R.UNSUPPORTED] * 2 + [R.REACHED] * 2
