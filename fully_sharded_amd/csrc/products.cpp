@@ -12,7 +12,8 @@ namespace {
 
 constexpr int64_t kCus = 256;      // compute units
 constexpr int64_t kXcds = 8;
-constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits
+constexpr int64_t kMaxSum = 131072;  // of codes: 127 * 127 * this fits 31 bits (128 * 128
+                                     // * this does not: such codes are for shorter sums)
 constexpr int64_t kMaxGroups = 65536;
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxSide = int64_t(1) << 26;
 // Bytes from one row of an operand to the next: 256 rows within 2^31.  (Of one

@@ -215,7 +215,8 @@ def bind_grouped_matmul_i8(op: str, a, a_scale, b, b_scale, c, offsets=None,
 
 def fsdp_grouped_matmul_i8(op: str, a, a_scale, b, b_scale, c, offsets=None,
                            accumulate: bool = False, stream=None):
-    """The product of 8-bit codes into c (bf16 or fp32), "nt" or "nn" as in
+    """The product of 8-bit codes (-127 to 127; -128 too where the sum has at most
+    131,071 terms) into c (bf16 or fp32), "nt" or "nn" as in
     fsdp_grouped_matmul, times a_scale [rows] and b_scale [groups, n] (None: no
     such factor).  accumulate: added to what c holds."""
     bind_grouped_matmul_i8(op, a, a_scale, b, b_scale, c, offsets, accumulate)(stream)

@@ -605,8 +605,10 @@ fsdp_status fsdp_grouped_matmul(const fsdp_matmul* m, const int32_t* offsets, co
 /* The product of 8-bit codes (FSDP_MATMUL_NT or NN), each row of A with a
  * scale, and each n with one per group or none (b_scale NULL):
  *   C[t,n] = (sum_k A[t,k] B_g[..]) a_scale[t] b_scale[g b_scale_stride + n]
- * The sum is exact (32-bit integers), its product with the scales fp32, left
- * to right, and the result rounded once to out_dtype.  NT with codes of
+ * Codes lie in -127..127, as fsdp_quantize_rows makes them (-128 as well where
+ * k is at most 131,071: the sum of 131,072 squares of it is 2^31).  The sum is
+ * exact (32-bit integers), its product with the scales fp32, left to right,
+ * and the result rounded once to out_dtype.  NT with codes of
  * weights [out, in] is the forward pass.  Their input gradient is NN: as the
  * weights' scales then lie along the sum, fsdp_quantize_rows takes them into
  * A first (its `channel`), and b_scale is NULL.
