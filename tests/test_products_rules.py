@@ -28,6 +28,19 @@ def test_cases_get_the_kernels_that_they_are_named_for(rules):
         assert (r.tile, r.direct) == (tile, how == "direct"), (name, r)
 
 
+def test_every_kernel_is_in_some_case():
+    """As the launchers have them: thin and apart for products over rows, deep for
+    bf16, and what passes through registers."""
+    have = {tuple(name.split()[:4]) for name in CASES}
+    tiles = {"bf16 direct": ["small", "mid", "deep", "big"], "i8 direct": ["small", "mid", "big"],
+             "bf16 registers": ["small", "mid"], "f32 registers": ["tiny", "small", "mid"]}
+    want = {(kind, op, tile, how) for key, all_of in tiles.items() for tile in all_of
+            for kind, how in [key.split()] for op in R.OPS if (kind, op) != ("i8", "tn")}
+    want |= {(kind, op, tile, "direct") for kind in ("bf16", "i8") for op in ("nt", "nn")
+             for tile in ("thin", "apart")}
+    assert have == want
+
+
 @pytest.mark.parametrize("op", R.OPS)
 def test_tiles_by_their_number(rules, op):
     """bf16 products of one weight with a sum of 2048, by their number of 128 x 128
