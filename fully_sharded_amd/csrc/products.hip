@@ -1093,6 +1093,7 @@ __global__ __launch_bounds__(F32Tile<BM>::Threads) void k_product_f32(ProductArg
   // sums of 128 entries are added up apart: of 8192 entries they are off by 2.5e-7
   // of the result (rms; a library's in one go by 1.6e-6), for 3% of the time
   constexpr int kFlush = 4;
+  static_assert(kFlush % S::Ahead == 0);  // the loop's steps meet it
   f4 acc[FM][FN] = {}, all[FM][FN] = {};
   auto flush = [&] {
 #pragma unroll
