@@ -110,8 +110,9 @@ __device__ __forceinline__ uint32_t wave_largest(uint32_t m) {
 // per entry in place of a division: of bf16 entries it gives the rounding of the
 // exact x 127 / a but at a tie (x = a / 2 and the like), where it gives either
 // neighbour.  (Entries are xs 2^e and as 2^f with 8-bit xs and as: x 127 / a is a
-// tie or at least 1 / (2 as 2^j) from one, j = f - e, while the three roundings
-// move it by less than 2^(7 - j) 2^-22.)
+// tie or at least 1 / (2 as 2^j) > 2^-(9 + j) from one, j = f - e, while the three
+// roundings move it by less than 2^(7 - j) 2^-21: each by 2^-24 of it at most, and
+// the reciprocal of an a above 2^126, which is subnormal, by 2^-22.)
 struct Scale {
   float scale, factor;
 };
