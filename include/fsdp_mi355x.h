@@ -590,7 +590,10 @@ fsdp_status fsdp_grouped_matmul_workspace(const fsdp_matmul* m, int32_t dtype, i
  * of zeros (accumulate: leaves it).
  *   offsets may be NULL with one group: all rows.  Rows may begin anywhere;
  *   bf16 operands whose rows begin and end at multiples of 16 bytes take a
- *   faster path.  C overlaps neither operand, nor offsets, nor itself.
+ *   faster path.  C's addresses, from its first entry to its last, meet none
+ *   of the operands', of offsets or of the workspace (so C and an operand may
+ *   not be columns side by side in the same rows), and C does not overlap
+ *   itself.
  *   workspace: as fsdp_grouped_matmul_workspace says, 256-byte aligned
  *   (NULL where it says 0), contents undefined before and after; calls that
  *   may overlap in time (other streams, replays of captured graphs) need
@@ -632,7 +635,10 @@ fsdp_status fsdp_grouped_matmul_i8(const fsdp_matmul* m, const int32_t* offsets,
  *   from row to row, 16-byte aligned, ldc a multiple of 16 and at least cols
  *   rounded up to one; the bytes from cols to there are set to 0.  scales:
  *   fp32 [rows].  groups, offsets: as above (channel's groups; rows of no
- *   group are left as they are); offsets NULL with one group: all rows. */
+ *   group are left as they are); offsets NULL with one group: all rows.  Codes
+ *   and scales meet neither each other nor what is read.
+ *   FSDP_ERR_UNSUPPORTED: 2^24 rows or more, more than 2^30 columns or 65,536
+ *   groups. */
 fsdp_status fsdp_quantize_rows(const void* x, int32_t dtype, int64_t rows, int64_t cols,
                                int64_t ldx, const float* channel, int64_t channel_stride,
                                const int32_t* offsets, int32_t groups, int8_t* codes, int64_t ldc,
