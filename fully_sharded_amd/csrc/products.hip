@@ -618,7 +618,8 @@ __device__ __forceinline__ uint32_t lds_address(const char* lds) {
 // all dies) and the clock under load (zeros for operands: 1,700 TFLOP/s).  Rounds
 // of 64 bytes four or five deep, all LDS reads at a half's beginning, four waves
 // of 128 x 128 and 32 x 32 matrix instructions measured level to 10% longer.  A
-// tile's beginning and end take 10 us, of which the next tile hides what fits.
+// tile's beginning and end take 10 us, which nothing hides: one workgroup has a
+// compute unit's LDS.
 template <typename T, typename S, int OP, bool DIRECT>
 __device__ __forceinline__ void tile(const ProductArgs& a, const Place& t, int i0, int j0,
                                      char* lds) {
@@ -816,8 +817,8 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 // across the sum (36 us and 26).
 //   Apart, for no more tiles than compute units: alone on its unit, a workgroup has
 // nothing else that covers a wait, and four waves that each wait alone wait less
-// than four that meet every round (128 x 4096 x 14336 in bf16 64 us; waves that
-// share the tile's rounds 84).  The joining costs 1 us, so short sums stay there.
+// than four that meet every round (128 x 4096 x 14336 in bf16 64 us, 41 where the
+// memory-side cache has the weights; waves that share the tile's rounds 84).  The joining costs 1 us, so short sums stay there.
 template <typename T, typename S, int OP>
 __global__ __launch_bounds__(256, S::Waves) void k_apart(ProductArgs a) {
   constexpr int FM = S::FM, FN = S::FN, BN = S::BN, NS = S::NS, LP = S::LP, LQ = S::LQ;

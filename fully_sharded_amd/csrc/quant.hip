@@ -1,10 +1,13 @@
 // gfx950 kernels of the 8-bit codes: rows quantised (of a tensor, or of a
 // unit's shards for every receiver) and units read back.  All are bound by
 // memory; a row is read once, into registers, and its largest magnitude found
-// before its codes are made.  Measured: 218M elements gathered for 8 ranks 388 us
-// (5.6 TB/s), read back by all 862 (6.1 TB/s; units' stores that stay in the caches
-// 890); 3.1M for 4 ranks 6.6 and 7.9 us; 8192 rows of 4096 bf16 18.5 us (5.4
-// TB/s), of 14336 64 (70 with the row waiting as floats).
+// before its codes are made.  Measured: 218M elements gathered for 8 ranks 384 us
+// (5.7 TB/s; of fp32 483, 5.4 TB/s), read back by all 865 (6.0 TB/s; units' stores
+// that stay in the caches 890; to fp32 1,927, 4.5 TB/s: a lane's 32 bytes in two
+// stores); 3.1M for 4 ranks 6.6 and 8.0 us.  8192 rows of 4096 bf16 22.5 us (4.5
+// TB/s; from the memory-side cache 19.5), of fp32 31 (5.4 TB/s), of 14336 bf16 64
+// (5.5 TB/s; 70 with the row waiting as floats); times a channel's scales, which
+// every row reads twice from L2, 31, 37 and 86.
 #include <hip/hip_runtime.h>
 
 #include "device.hpp"
