@@ -37,11 +37,21 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //     a tenth of these.  200 tiles that hold 400 of 64 (25600 x 64), which all run at
 //     once: along the sum 2048 30, 37 and 29, 4096 47, 65 and 49; across it 1024
 //     12.3, 14.3 and 12.9, 2048 25, 32 and 32.
-//     Several groups: 12 of 80 rows each (208 tiles), sum 512 9.2, 9.8 and 9.0, 768
-//     11.9, 13.1 and 12.5; 6 of 100 (224), sum 512 9.9, 10.1 and 9.0; four of 250 on
-//     average (144), sum 512 8.1, 9.2 and 8.6, 256 6.3, 6.5 and 6.1, of 400 (224) 512
-//     8.7, 9.7 and 11.3; weight gradients of four of 512 rows on average, 160 tiles
-//     10.6, 12.6 and 9.5, 224 11.9, 13.3 and 12.9.
+//     Several groups, kDeep and kSmall: 12 of 80 rows each (208 tiles), sum 512 9.2
+//     and 9.0, 768 11.9 and 12.5; 6 of 100 (224), sum 512 9.9 and 9.0; four of 400
+//     (224), sum 512 8.7 and 11.3, 256 6.7 and 8.5, of 250 (144) 6.3 and 6.1; 128 of
+//     136 (200, every second one nearly empty), sum 824 16.0 and 13.8.  Where they
+//     fill little of a tile: 80 of 64 rows x 192, sum 4096 43 and 36; 12 of 16 rows x
+//     2048, sum 2048 25.4 and 25.3; weights across the sum, 64 of 12 rows x 408 (256),
+//     sum 2256 27 and 33, 128 of 31 x 168 (256), sum 3208 38 and 46, 80 of 64 x 192
+//     (160), sum 4096 42 and 36.
+//     Weight gradients of several: four of 512 rows, unlike in length, 160 tiles
+//     10.6 and 9.5, 224 11.9 and 12.9; eight of 312 x 128 x 3288 (208) 11.2 and 9.9;
+//     fifteen of 512 x 512 (240), 1,024 rows each 18 and 26; sixty of 256 x 256 (240)
+//     26 and 31, 256 rows 13.3 and 11.5; 200 of 128 x 128, 1,024 rows 56 and 40 (a
+//     group's tiles are dealt to eight dies); 150 of 64 x 64, 2,048 rows 49 and, in
+//     parts, 20.  Where kDeep does not pay at 256 tiles, kMid and kSmall: 32 of 960 x
+//     120, 19 rows 5.5 and 7.5; forward, 128 of 2 rows x 176, sum 3752 70 and 47.
 //   Codes: kDeep and kMid level.
 //   kMid and kSmall: 288 tiles (8192 x 512 x 2048 in 16 groups) 30 and 34, 8 groups
 //     of 1024 x 1024 over 4,096 rows 17.1 and 18.6
@@ -73,10 +83,21 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
   };
   // of up to one tile of 128 per compute unit
   auto deep = [&] {
-    const int64_t t = tiles(kMid), sum = weight ? m.rows / met : m.k;
+    const int64_t t = tiles(kMid), small = tiles(kSmall), sum = weight ? m.rows / met : m.k;
     if (t <= kCus / 2) return false;
-    if (tiles(kSmall) <= 2 * kCus) return sum >= (m.op == FSDP_MATMUL_NT ? 4096 : 2048);
-    return met == 1 || sum >= 768 || (t > 3 * kCus / 4 && (weight || m.rows >= 128 * met));
+    // 64 x 64 tiles that do not all run at once, and fill the larger ones for the most
+    const bool full = small > 2 * kCus && 5 * t <= 2 * small;
+    const bool most = t > 3 * kCus / 4;
+    if (weight ? m.groups == 1 : met == 1)
+      return full ? most || sum >= 192 : sum >= (m.op == FSDP_MATMUL_NT ? 4096 : 2048);
+    if (!full)
+      return m.op == FSDP_MATMUL_NN && most && sum >= 2048 && 4 * t <= 3 * small;
+    if (weight) return most && sum >= 512 && t >= m.groups * (sum >= 1024 ? 4 : 8);
+    if (m.rows < 128 * met) return sum >= 768;
+    // (groups a little longer than a tile fill two by half, and groups' lengths may
+    // give a row of tiles more)
+    return m.rows >= 192 * met && t + ceil_div(m.n, 128) <= kCus &&
+           (sum >= 768 || (most && sum >= 384));
   };
   r.direct = direct && type != kProductF32;
   r.tile = kSmall;
@@ -90,9 +111,10 @@ ProductRule product_rule(const fsdp_matmul& m, ProductType type, bool direct) {
     r.tile = kApart;
   } else if (r.direct && tiles(kBig) >= (weight && m.groups > 1 ? 2 * kCus : kCus)) {
     r.tile = kBig;
-  } else if (r.direct && type == kProductBf16 && tiles(kMid) <= kCus) {
-    if (deep()) r.tile = kDeep;
-  } else if (tiles(kMid) >= kCus) {
+  } else if (r.direct && type == kProductBf16 && tiles(kMid) <= kCus && deep()) {
+    r.tile = kDeep;
+  } else if (tiles(kMid) > kCus ||
+             (tiles(kMid) == kCus && (weight || !r.direct || type != kProductBf16))) {
     r.tile = kMid;
   }
   const int64_t down = kProductRows[r.tile], across = product_cols(r.tile, m.op);

@@ -8,16 +8,16 @@ CASES = {
     "bf16 nt deep direct 144": ("nt", "bf16", [1100], 2040, 520, 0),
     "bf16 nt deep direct 224": ("nt", "bf16", [1700], 2040, 72, 0),
     "bf16 nt deep direct 256": ("nt", "bf16", [2048], 2048, 520, 0),
-    "bf16 nt deep direct groups": ("nt", "bf16", [700, 0, 1, 900], 2056, 136, 0),
+    "bf16 nt deep direct groups": ("nt", "bf16", [700, 0, 1, 900], 2056, 392, 0),
     "bf16 nt deep direct few rows": ("nt", "bf16", [37], 16520, 4104, 0),
     "bf16 nn deep direct 144": ("nn", "bf16", [1100], 2040, 520, 0),
     "bf16 nn deep direct 224": ("nn", "bf16", [1700], 2040, 72, 0),
     "bf16 nn deep direct 256": ("nn", "bf16", [2048], 2048, 520, 0),
-    "bf16 nn deep direct groups": ("nn", "bf16", [700, 0, 1, 900], 2056, 136, 0),
+    "bf16 nn deep direct groups": ("nn", "bf16", [700, 0, 1, 900], 2056, 392, 0),
     "bf16 tn deep direct 144": ("tn", "bf16", [520], 1096, 2040, 0),
     "bf16 tn deep direct 240": ("tn", "bf16", [333], 1800, 2040, 0),
     "bf16 tn deep direct 256": ("tn", "bf16", [520], 2048, 2048, 0),
-    "bf16 tn deep direct groups": ("tn", "bf16", [200, 0, 131], 1032, 1032, 0),
+    "bf16 tn deep direct groups": ("tn", "bf16", [1600, 0, 131], 1032, 1032, 0),
 }
 
 for _op in ("nt", "nn"):

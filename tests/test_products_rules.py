@@ -60,6 +60,18 @@ def test_tiles_by_their_number(rules, op):
     assert [r.tile for r in rules(near)] == ["deep"] * 3
 
 
+@pytest.mark.parametrize("product,parts", [
+    (("tn", "bf16", 150, 150 * 2048, 64, 64), 3), (("tn", "bf16", 200, 200 * 1024, 64, 128), 1),
+    (("tn", "bf16", 200, 200 * 1024, 128, 128), 1), (("tn", "bf16", 130, 130 * 512, 128, 128), 1),
+    (("nt", "bf16", 80, 80 * 64, 192, 4096), 1), (("nn", "bf16", 80, 80 * 64, 192, 4096), 1),
+    (("nt", "bf16", 150, 150 * 40, 64, 4096), 1)])
+def test_many_small_groups_keep_small_tiles(rules, product, parts):
+    """Between half as many 128 x 128 tiles as compute units and one each, but of
+    groups that fill little of them, or have few each."""
+    r, = rules([product])
+    assert r.tile in ("small", "thin", "apart") and r.parts == parts, r
+
+
 def test_sums_in_parts_are_of_small_tiles(rules):
     """The joining launch is there for them alone."""
     products = [("tn", kind, groups, rows, n, k)
