@@ -818,7 +818,8 @@ __global__ __launch_bounds__(S::Threads, S::Waves) void k_product(ProductArgs a)
 //   Apart, for no more tiles than compute units: alone on its unit, a workgroup has
 // nothing else that covers a wait, and four waves that each wait alone wait less
 // than four that meet every round (128 x 4096 x 14336 in bf16 64 us, 41 where the
-// memory-side cache has the weights; waves that share the tile's rounds 84).  The joining costs 1 us, so short sums stay there.
+// memory-side cache has the weights; waves that share the tile's rounds 84).  The
+// joining costs 1 us, so short sums stay there.
 template <typename T, typename S, int OP>
 __global__ __launch_bounds__(256, S::Waves) void k_apart(ProductArgs a) {
   constexpr int FM = S::FM, FN = S::FN, BN = S::BN, NS = S::NS, LP = S::LP, LQ = S::LQ;
