@@ -150,12 +150,28 @@ def bind_grouped_matmul(op: str, a, b, c, offsets=None, accumulate: bool = False
     graph's): so any stream may use it, but calls of one binding that may
     overlap in time, on two streams or in replays of two captured graphs, race
     on it."""
-    if workspace is None:
+    given = workspace
+    if given is None:
         workspace = grouped_matmul_workspace(op, a, b, c)
         if workspace is not None and not torch.cuda.is_current_stream_capturing():
             torch.cuda.current_stream(a.device).synchronize()
     args, keep, tensors = _plain(op, a, b, c, offsets, accumulate, workspace)
-    return _bound("fsdp_grouped_matmul", args, keep, tensors)
+    bound = _bound("fsdp_grouped_matmul", args, keep, tensors)
+    if given is not None or workspace is None:
+        return bound
+    current, device = torch._C._cuda_getCurrentRawStream, a.device.index
+    known = {current(device)}
+
+    def run(stream=None):
+        bound(stream)
+        handle = current(device) if stream is None else _b._stream(stream).value or 0
+        if handle not in known:
+            # the allocator may hand the workspace out again, once nobody has the
+            # binding, only when this call is done
+            workspace.record_stream(torch.cuda.ExternalStream(handle))
+            known.add(handle)
+    run.call = bound.call
+    return run
 
 
 def fsdp_grouped_matmul(op: str, a, b, c, offsets=None, accumulate: bool = False,

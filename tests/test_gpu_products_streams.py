@@ -76,6 +76,30 @@ def test_a_binding_waits_for_its_workspace():
     assert torch.equal(c, want) and y.shape == x.shape
 
 
+def test_a_dropped_bindings_workspace_waits_for_its_calls():
+    """Its memory is not handed out while a call on another stream may use it."""
+    a, b, c, want = operands()
+    side = torch.cuda.Stream()
+    x = torch.randn(4096, 4096, device=DEV)
+    ws = F.grouped_matmul_workspace("tn", a, b, c)
+    n = ws.numel()
+    del ws
+    torch.cuda.synchronize()
+    f = F.bind_grouped_matmul("tn", a, b, c)
+    where = f.call._keep[-1].data_ptr()
+    assert f.call._keep[-1].numel() == n
+    with torch.cuda.stream(side):
+        for _ in range(30):
+            y = x @ x
+    f(side)
+    del f
+    new = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert not side.query()
+    assert not new.data_ptr() <= where < new.data_ptr() + n
+    side.synchronize()
+    assert torch.equal(c, want) and y.shape == x.shape
+
+
 def test_bound_while_captured():
     """No wait then (a capture forbids it): the graph's own memory."""
     a, b, c, want = operands()

@@ -39,14 +39,20 @@ def log(monkeypatch):
         return torch.zeros(n, dtype=dtype)
 
     def bound(name, args, keep, tensors):
-        return lambda s=None: events.append(
-            ("called", current[-1] if s is None else getattr(s, "cuda_stream", None) or s.value))
+        def run(s=None):
+            on = current[-1] if s is None else getattr(s, "cuda_stream", None) or s.value
+            events.append(("called", on))
+        run.call = None
+        return run
     monkeypatch.setattr(torch.cuda, "Stream", Side)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Side)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: Side(current[-1], events))
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda *_: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda _, s: events.append(("kept for", s.cuda_stream)))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda _: current[-1],
+                        raising=False)
     monkeypatch.setattr(products, "_matrix", lambda t, *_: ctypes.c_void_p(t.data_ptr()))
     monkeypatch.setattr(products._b, "_dev", lambda t, _: t.data_ptr())
     monkeypatch.setattr(products, "_bound", bound)
@@ -70,7 +76,20 @@ def test_a_kept_workspace_is_free_for_any_stream(log):
     f = F.bind_grouped_matmul("tn", *operands)
     assert events == [("allocated", 7), ("waited", 7)]
     f(Side(9))
-    assert events[2:] == [("called", 9)]
+    assert events[2] == ("called", 9)
+
+
+def test_a_kept_workspace_outlives_its_calls(log):
+    """A binding that nobody has any more leaves its workspace to the allocator:
+    to be handed out again when the calls of every stream are done.  (Calls on the
+    stream that it is of are in order with what comes next there.)"""
+    events, operands = log
+    f = F.bind_grouped_matmul("tn", *operands)
+    for s in (None, Side(9), ctypes.c_void_p(9), ctypes.c_void_p(11), Side(9), None):
+        f(s)
+    with torch.cuda.stream(Side(13)):
+        f()
+    assert [e for e in events if e[0] == "kept for"] == [("kept for", s) for s in (9, 11, 13)]
 
 
 def test_no_workspace_no_wait(log):
